@@ -20,7 +20,11 @@ __all__ = [
     "FiError", "fi_config", "fi_tile", "fi_create", "fi_step", "fi_run_closed_loop", "fi_reset",
     "fi_destroy", "fi_position", "fi_strerror", "fi_tile_at", "fi_run_prompted", "fi_conv_static", "Mixer",
     "fi_stack_config", "fi_stack_create", "fi_stack_run", "fi_stack_destroy", "Stack", "EXPORTS", "lib",
-    "LIB_PATH",
+    "LIB_PATH", "FI_ACT_GELU", "FI_ACT_TANH", "FI_ACT_IDENTITY",
+    "fi_view", "fi_lattn_config", "fi_lattn_args", "fi_lattn_create", "fi_lattn_prompt", "fi_lattn_step",
+    "fi_lattn_destroy", "LinearAttention", "fi_dense_config", "fi_dense_args", "fi_dense_create", "fi_dense_run",
+    "fi_dense_destroy", "Dense", "fi_scores_config", "fi_scores_args", "fi_scores_create", "fi_scores_run",
+    "fi_scores_destroy", "TokenScores",
 ]
 
 FI_F32, FI_BF16 = 0, 1
@@ -50,7 +54,9 @@ lib = ctypes.CDLL(str(LIB_PATH))
 # every symbol include/fi.h declares
 EXPORTS = ("fi_create", "fi_step", "fi_run_closed_loop", "fi_run_prompted", "fi_reset", "fi_destroy",
            "fi_position", "fi_strerror", "fi_tile_at", "fi_conv_static", "fi_stack_create", "fi_stack_run",
-           "fi_stack_destroy")
+           "fi_stack_destroy", "fi_lattn_create", "fi_lattn_prompt", "fi_lattn_step", "fi_lattn_destroy",
+           "fi_dense_create", "fi_dense_run", "fi_dense_destroy", "fi_scores_create", "fi_scores_run",
+           "fi_scores_destroy")
 FI_ACT_GELU, FI_ACT_TANH, FI_ACT_IDENTITY = 0, 1, 2
 FI_STATIC_WORKSPACE_BYTES = 64 << 20
 
@@ -71,6 +77,44 @@ class fi_stack_config(ctypes.Structure):
 class fi_tile(ctypes.Structure):
     _fields_ = [("U", ctypes.c_int64), ("in_lo", ctypes.c_int64), ("in_hi", ctypes.c_int64),
                 ("out_lo", ctypes.c_int64), ("out_hi", ctypes.c_int64)]
+
+
+class fi_view(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_void_p), ("row", ctypes.c_int64), ("pos", ctypes.c_int64), ("head", ctypes.c_int64)]
+
+
+class fi_lattn_config(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int64), ("L", ctypes.c_int64), ("H", ctypes.c_int64), ("Hkv", ctypes.c_int64),
+                ("dk", ctypes.c_int64), ("dv", ctypes.c_int64), ("scale", ctypes.c_float),
+                ("io_dtype", ctypes.c_int32), ("stream", ctypes.c_void_p)]
+
+
+class fi_lattn_args(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int64), ("L", ctypes.c_int64), ("q", fi_view), ("k", fi_view), ("v", fi_view),
+                ("o", fi_view), ("lens", ctypes.c_void_p), ("slots", ctypes.c_void_p), ("n_slots", ctypes.c_int64),
+                ("state", ctypes.c_void_p), ("fresh", ctypes.c_int32)]
+
+
+class fi_dense_config(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64), ("io_dtype", ctypes.c_int32),
+                ("out_dtype", ctypes.c_int32), ("act", ctypes.c_int32), ("stream", ctypes.c_void_p)]
+
+
+class fi_dense_args(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int64), ("x", ctypes.c_void_p), ("ldx", ctypes.c_int64), ("w", ctypes.c_void_p),
+                ("ldw", ctypes.c_int64), ("bias", ctypes.c_void_p), ("res", ctypes.c_void_p), ("ldr", ctypes.c_int64),
+                ("y", ctypes.c_void_p), ("ldy", ctypes.c_int64)]
+
+
+class fi_scores_config(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("V", ctypes.c_int64), ("k", ctypes.c_int32), ("io_dtype", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("stream", ctypes.c_void_p)]
+
+
+class fi_scores_args(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("logits", ctypes.c_void_p), ("ld", ctypes.c_int64),
+                ("targets", ctypes.c_void_p), ("logprob", ctypes.c_void_p), ("entropy", ctypes.c_void_p),
+                ("lse", ctypes.c_void_p), ("top", ctypes.c_void_p), ("top_id", ctypes.c_void_p)]
 
 
 _H = ctypes.c_void_p
@@ -102,6 +146,20 @@ lib.fi_stack_run.argtypes = [_H, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_floa
 lib.fi_stack_run.restype = ctypes.c_int
 lib.fi_stack_destroy.argtypes = [_H]
 lib.fi_stack_destroy.restype = None
+lib.fi_lattn_create.argtypes = [ctypes.POINTER(fi_lattn_config), ctypes.c_void_p, ctypes.POINTER(_H)]
+lib.fi_lattn_create.restype = ctypes.c_int
+lib.fi_lattn_prompt.argtypes = lib.fi_lattn_step.argtypes = [_H, ctypes.POINTER(fi_lattn_args)]
+lib.fi_lattn_prompt.restype = lib.fi_lattn_step.restype = ctypes.c_int
+lib.fi_dense_create.argtypes = [ctypes.POINTER(fi_dense_config), ctypes.POINTER(_H)]
+lib.fi_dense_create.restype = ctypes.c_int
+lib.fi_dense_run.argtypes = [_H, ctypes.POINTER(fi_dense_args)]
+lib.fi_dense_run.restype = ctypes.c_int
+lib.fi_scores_create.argtypes = [ctypes.POINTER(fi_scores_config), ctypes.POINTER(_H)]
+lib.fi_scores_create.restype = ctypes.c_int
+lib.fi_scores_run.argtypes = [_H, ctypes.POINTER(fi_scores_args)]
+lib.fi_scores_run.restype = ctypes.c_int
+for _f in (lib.fi_lattn_destroy, lib.fi_dense_destroy, lib.fi_scores_destroy):
+    _f.argtypes, _f.restype = [_H], None
 # only in the phase-timing build (include/fi_profile.h)
 HAS_PROFILE = hasattr(lib, "fi_profile_read")
 if HAS_PROFILE:
@@ -226,6 +284,159 @@ class Stack:
             self.close()
         except Exception:
             pass
+
+
+def _create(fn, where: str, *args) -> int:
+    out = _H()
+    _check(fn(*args, ctypes.byref(out)), where)
+    return int(out.value)
+
+
+def fi_lattn_create(cfg: fi_lattn_config, log_decay) -> int:
+    return _create(lib.fi_lattn_create, "fi_lattn_create", ctypes.byref(cfg), _ptr(log_decay))
+
+
+def fi_lattn_prompt(s: int, args: fi_lattn_args) -> None:
+    _check(lib.fi_lattn_prompt(s, args), "fi_lattn_prompt")
+
+
+def fi_lattn_step(s: int, args: fi_lattn_args) -> None:
+    _check(lib.fi_lattn_step(s, args), "fi_lattn_step")
+
+
+def fi_lattn_destroy(s) -> None:
+    lib.fi_lattn_destroy(s)
+
+
+def fi_dense_create(cfg: fi_dense_config) -> int:
+    return _create(lib.fi_dense_create, "fi_dense_create", ctypes.byref(cfg))
+
+
+def fi_dense_run(s: int, args: fi_dense_args) -> None:
+    _check(lib.fi_dense_run(s, args), "fi_dense_run")
+
+
+def fi_dense_destroy(s) -> None:
+    lib.fi_dense_destroy(s)
+
+
+def fi_scores_create(cfg: fi_scores_config) -> int:
+    return _create(lib.fi_scores_create, "fi_scores_create", ctypes.byref(cfg))
+
+
+def fi_scores_run(s: int, args: fi_scores_args) -> None:
+    _check(lib.fi_scores_run(s, args), "fi_scores_run")
+
+
+def fi_scores_destroy(s) -> None:
+    lib.fi_scores_destroy(s)
+
+
+class _Owner:
+    """Owns one handle; `_destroy` frees it."""
+
+    handle = 0
+
+    def close(self):
+        if self.handle:
+            self._destroy(self.handle)
+            self.handle = 0
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        self.close()
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def _strides(x, width: int, where: str):
+    """A tensor's strides; its last dimension is `width` adjacent elements."""
+    if x.shape[-1] != width or (width > 1 and x.stride(-1) != 1):
+        raise FiError(FI_ERR_INVALID, where)
+    return x.stride()
+
+
+class LinearAttention(_Owner):
+    """Linear attention with a decay per head, over the caller's states
+    (marshalling only).  q, k, v and o are tensors [B, L, heads, size] of the
+    io type, of any strides as long as a head's elements are adjacent; state
+    is [slots, Hkv, dk, dv], fp32 and contiguous, updated in place; lens and
+    slots are int32 tensors [B] on the device."""
+
+    _destroy = staticmethod(fi_lattn_destroy)
+
+    def __init__(self, B, L, H, Hkv, dk, dv, log_decay, scale=1.0, io_dtype=FI_BF16, stream=None):
+        self.cfg = fi_lattn_config(B=int(B), L=int(L), H=int(H), Hkv=int(Hkv), dk=int(dk), dv=int(dv),
+                                   scale=float(scale), io_dtype=int(io_dtype), stream=_stream(stream))
+        self._heads = (int(H), int(dk)), (int(Hkv), int(dk)), (int(Hkv), int(dv)), (int(H), int(dv))
+        self.handle = fi_lattn_create(self.cfg, log_decay)
+
+    def _call(self, fn, where, q, k, v, o, state, lens, slots, fresh):
+        B, L = q.shape[0], q.shape[1]
+        views = []
+        for x, (heads, size) in zip((q, k, v, o), self._heads):
+            row, pos, head, _ = _strides(x, size, where)
+            if x.shape[:3] != (B, L, heads):
+                raise FiError(FI_ERR_INVALID, where)
+            views.append(fi_view(x.data_ptr(), row, pos, head))
+        a = fi_lattn_args(B, L, *views, _ptr(lens), _ptr(slots), 0 if state is None else state.shape[0], _ptr(state),
+                          1 if fresh else 0)
+        _check(fn(self.handle, a), where)
+
+    def prompt(self, q, k, v, o, state=None, lens=None, slots=None, fresh=False):
+        self._call(lib.fi_lattn_prompt, "fi_lattn_prompt", q, k, v, o, state, lens, slots, fresh)
+
+    def step(self, q, k, v, o, state, slots=None):
+        self._call(lib.fi_lattn_step, "fi_lattn_step", q, k, v, o, state, None, slots, False)
+
+
+class Dense(_Owner):
+    """y = act(x w^T + bias) + res over rows (marshalling only): x [M, K],
+    w [N, K], bias [N], res and y [M, N], rows of any stride."""
+
+    _destroy = staticmethod(fi_dense_destroy)
+
+    def __init__(self, M, N, K, io_dtype=FI_BF16, out_dtype=FI_BF16, act=FI_ACT_IDENTITY, stream=None):
+        self.cfg = fi_dense_config(M=int(M), N=int(N), K=int(K), io_dtype=int(io_dtype), out_dtype=int(out_dtype),
+                                   act=int(act), stream=_stream(stream))
+        self.N, self.K = int(N), int(K)
+        self.handle = fi_dense_create(self.cfg)
+
+    def run(self, x, w, y, bias=None, res=None):
+        M, N, K = x.shape[0], self.N, self.K
+        where = "fi_dense_run"
+        if w.shape[0] != N or y.shape[0] != M or (res is not None and res.shape[0] != M):
+            raise FiError(FI_ERR_INVALID, where)
+        a = fi_dense_args(M, x.data_ptr(), _strides(x, K, where)[0], w.data_ptr(), _strides(w, K, where)[0], _ptr(bias),
+                          _ptr(res), 0 if res is None else _strides(res, N, where)[0], y.data_ptr(),
+                          _strides(y, N, where)[0])
+        _check(lib.fi_dense_run(self.handle, a), where)
+
+
+class TokenScores(_Owner):
+    """Log probabilities of given tokens, entropies and the most probable
+    tokens (marshalling only): logits [rows, V] with rows of any stride;
+    targets int64 [rows]; logprob, entropy, lse fp32 [rows]; top fp32 and
+    top_id int64 [rows, k], contiguous.  Outputs that are None are left out."""
+
+    _destroy = staticmethod(fi_scores_destroy)
+
+    def __init__(self, rows, V, k=0, io_dtype=FI_BF16, scale=1.0, stream=None):
+        self.cfg = fi_scores_config(rows=int(rows), V=int(V), k=int(k), io_dtype=int(io_dtype), scale=float(scale),
+                                    stream=_stream(stream))
+        self.V = int(V)
+        self.handle = fi_scores_create(self.cfg)
+
+    def run(self, logits, targets=None, logprob=None, entropy=None, top=None, top_id=None, lse=None):
+        a = fi_scores_args(logits.shape[0], logits.data_ptr(), _strides(logits, self.V, "fi_scores_run")[0],
+                           _ptr(targets), _ptr(logprob), _ptr(entropy), _ptr(lse), _ptr(top), _ptr(top_id))
+        _check(lib.fi_scores_run(self.handle, a), "fi_scores_run")
 
 
 def fi_profile_read(s: int):

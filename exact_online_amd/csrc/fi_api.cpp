@@ -33,10 +33,31 @@ namespace {
 thread_local char g_errbuf[256];
 thread_local hipError_t g_last_hip = hipSuccess;
 
-int hip_fail(hipError_t e) {
+}  // namespace
+
+int fi::hip_fail(hipError_t e) {
     g_last_hip = e;
     return e == hipErrorOutOfMemory ? FI_ERR_NOMEM : FI_ERR_HIP;
 }
+
+int fi::check_device() {
+    int ndev = 0;
+    if (hipGetDeviceCount(&ndev) != hipSuccess || ndev < 1) {
+        g_last_hip = hipErrorNoDevice;
+        return FI_ERR_UNSUPPORTED;
+    }
+    hipDeviceProp_t prop;
+    int dev = 0;
+    if (hipGetDevice(&dev) != hipSuccess || hipGetDeviceProperties(&prop, dev) != hipSuccess)
+        return FI_ERR_HIP;
+    return std::strncmp(prop.gcnArchName, "gfx950", 6) != 0 ? FI_ERR_UNSUPPORTED : FI_OK;
+}
+
+namespace {
+
+using fi::dalloc;
+using fi::hip_fail;
+using fi::raw_int;
 
 #define FI_HIP(expr)                                 \
     do {                                             \
@@ -65,21 +86,6 @@ void free_state(DevState &d) {
     d.spec = nullptr;
     d.twf = nullptr;
     d.scratch = nullptr;
-}
-
-// A failed hipMalloc also leaves its error as the thread's "last error",
-// which the next launch check (hipGetLastError) would then report as its own:
-// take it back here, so a rejected fi_create leaves no trace for later calls.
-template <typename T>
-hipError_t dalloc(T **p, size_t bytes) {
-    void *v = nullptr;
-    hipError_t e = hipMalloc(&v, bytes < 256 ? 256 : bytes);
-    if (e != hipSuccess) {
-        (void)hipGetLastError();
-        v = nullptr;
-    }
-    *p = static_cast<T *>(v);
-    return e;
 }
 
 // Sizes of a handle's device buffers (bytes) and its persistent-pass grid.
@@ -193,17 +199,6 @@ int build(fi_handle *s, const void *h) {
     return FI_OK;
 }
 
-// The int a caller put in an enum-typed field or argument, read as its
-// bytes: a value outside the enumeration is not one the enum type may hold,
-// so it is never loaded as that type.
-template <typename E>
-int raw_int(const E &e) {
-    static_assert(sizeof(E) == sizeof(int), "an int-sized enum");
-    int v;
-    std::memcpy(&v, &e, sizeof v);
-    return v;
-}
-
 // Validation shared by fi_create and fi_conv_static; fills the handle's
 // configuration fields.
 int configure(const fi_config *cfg, fi_handle *s) {
@@ -227,16 +222,8 @@ int configure(const fi_config *cfg, fi_handle *s) {
     const int64_t C = cfg->B * cfg->D;
     if (C >= lim || (C > 0 && LS > ((int64_t)1 << 46) / C)) return FI_ERR_INVALID;
 
-    int ndev = 0;
-    if (hipGetDeviceCount(&ndev) != hipSuccess || ndev < 1) {
-        g_last_hip = hipErrorNoDevice;
-        return FI_ERR_UNSUPPORTED;
-    }
-    hipDeviceProp_t prop;
-    int dev = 0;
-    if (hipGetDevice(&dev) != hipSuccess || hipGetDeviceProperties(&prop, dev) != hipSuccess)
-        return FI_ERR_HIP;
-    if (std::strncmp(prop.gcnArchName, "gfx950", 6) != 0) return FI_ERR_UNSUPPORTED;
+    const int rc = fi::check_device();
+    if (rc != FI_OK) return rc;
 
     std::memset(&s->d, 0, sizeof(s->d));
     DevState &d = s->d;

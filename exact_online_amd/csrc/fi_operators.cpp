@@ -1,0 +1,254 @@
+// fi_operators.cpp -- host side of the operators around the mixers
+// (fi_lattn_*, fi_dense_*, fi_scores_* of include/fi.h): argument checks,
+// workspaces and launches.
+#include "fi_operators.h"
+
+#include <hip/hip_runtime_api.h>
+
+#include <cmath>
+#include <new>
+#include <vector>
+
+#include "fi.h"
+#include "fi_internal.h"
+
+using namespace fi;
+
+struct fi_lattn {
+    fi_lattn_config cfg;
+    hipStream_t stream;
+    float *ld;     // [Hkv] log decay, device
+};
+
+struct fi_dense {
+    fi_dense_config cfg;
+    hipStream_t stream;
+};
+
+struct fi_scores {
+    fi_scores_config cfg;
+    hipStream_t stream;
+};
+
+namespace {
+
+constexpr int64_t kLim = (int64_t)1 << 31;
+constexpr int64_t kMaxHead = 256;            // largest head size of fi_lattn
+constexpr int64_t kMaxCount = (int64_t)1 << 46;   // elements of one array
+
+#define FI_HIP(expr)                                      \
+    do {                                                  \
+        hipError_t e_ = (expr);                           \
+        if (e_ != hipSuccess) return fi::hip_fail(e_);    \
+    } while (0)
+
+bool dtype_ok(int v) { return v == FI_F32 || v == FI_BF16; }
+int esize(int dt) { return dt == FI_BF16 ? 2 : 4; }
+bool aligned(const void *p, int64_t to) { return reinterpret_cast<uintptr_t>(p) % (uintptr_t)to == 0; }
+
+// a * b * ... of factors >= 1 within `most`
+bool fits(std::initializer_list<int64_t> f, int64_t most) {
+    int64_t n = 1;
+    for (int64_t v : f) {
+        if (v > most / n) return false;
+        n *= v;
+    }
+    return true;
+}
+
+}  // namespace
+
+extern "C" {
+
+// ------------------------------------------------------------ linear attention
+int fi_lattn_create(const fi_lattn_config *cfg, const float *log_decay, fi_lattn **out) {
+    if (out) *out = nullptr;
+    if (!cfg || !log_decay || !out) return FI_ERR_INVALID;
+    if (cfg->B < 1 || cfg->L < 1 || cfg->H < 1 || cfg->Hkv < 1 || cfg->dk < 1 || cfg->dv < 1) return FI_ERR_INVALID;
+    if (cfg->B >= kLim || cfg->L >= kLim || cfg->H >= kLim) return FI_ERR_INVALID;
+    if (cfg->H % cfg->Hkv != 0 || !std::isfinite(cfg->scale) || !dtype_ok(raw_int(cfg->io_dtype))) return FI_ERR_INVALID;
+    if (!fits({cfg->B, cfg->L, cfg->H, cfg->dk}, kMaxCount) || !fits({cfg->B, cfg->L, cfg->H, cfg->dv}, kMaxCount))
+        return FI_ERR_INVALID;
+    if (cfg->dk > kMaxHead || cfg->dv > kMaxHead || cfg->L > FI_MAX_L || cfg->B > kLattnMaxRows / cfg->Hkv)
+        return FI_ERR_UNSUPPORTED;
+    int rc = check_device();
+    if (rc != FI_OK) return rc;
+    fi_lattn *s = new (std::nothrow) fi_lattn();
+    if (!s) return FI_ERR_NOMEM;
+    s->cfg = *cfg;
+    s->stream = static_cast<hipStream_t>(cfg->stream);
+    s->ld = nullptr;
+    const size_t bytes = (size_t)cfg->Hkv * sizeof(float);
+    float *host = new (std::nothrow) float[(size_t)cfg->Hkv];
+    hipError_t e = host ? dalloc(&s->ld, bytes) : hipErrorOutOfMemory;
+    if (e == hipSuccess) e = hipMemcpyAsync(s->ld, log_decay, bytes, hipMemcpyDeviceToDevice, s->stream);
+    if (e == hipSuccess) e = hipMemcpyAsync(host, log_decay, bytes, hipMemcpyDeviceToHost, s->stream);
+    if (e == hipSuccess) e = hipStreamSynchronize(s->stream);
+    bool ok = e == hipSuccess;
+    for (int64_t n = 0; ok && n < cfg->Hkv; ++n) ok = host[n] <= 0.f;   // false for NaN
+    delete[] host;
+    if (e != hipSuccess || !ok) {
+        fi_lattn_destroy(s);
+        return e != hipSuccess ? hip_fail(e) : FI_ERR_INVALID;
+    }
+    *out = s;
+    return FI_OK;
+}
+
+void fi_lattn_destroy(fi_lattn *s) {
+    if (!s) return;
+    (void)hipStreamSynchronize(s->stream);
+    if (s->ld) (void)hipFree(s->ld);
+    delete s;
+}
+
+}  // extern "C"
+
+namespace {
+
+// a view's whole heads load in 16-byte units
+bool view_vec(const fi_view &v, int64_t d, int es) {
+    const int64_t u = 16 / es;
+    return aligned(v.p, 16) && v.row % u == 0 && v.pos % u == 0 && v.head % u == 0 && d % u == 0;
+}
+
+int lattn_call(const fi_lattn *s, const fi_lattn_args *a, LattnCall &c) {
+    if (!s || !a) return FI_ERR_INVALID;
+    const fi_lattn_config &f = s->cfg;
+    if (a->B < 0 || a->B > f.B || a->L < 0 || a->L > f.L) return FI_ERR_INVALID;
+    const int dt = raw_int(f.io_dtype), es = esize(dt);
+    const bool some = a->B > 0 && a->L > 0;   // an empty call's arrays may be NULL
+    for (const fi_view *v : {&a->q, &a->k, &a->v, &a->o})
+        if ((some && !v->p) || !aligned(v->p, es)) return FI_ERR_INVALID;
+    if ((!a->state && !a->fresh) || !aligned(a->state, 16) || !aligned(a->lens, 4) || !aligned(a->slots, 4))
+        return FI_ERR_INVALID;
+    if (a->n_slots < 0 || a->n_slots >= kLim || (!a->slots && a->state && a->n_slots < a->B)) return FI_ERR_INVALID;
+    c.B = a->B;
+    c.L = (int)a->L;
+    c.H = (int)f.H;
+    c.Hkv = (int)f.Hkv;
+    c.G = (int)(f.H / f.Hkv);
+    c.dk = (int)f.dk;
+    c.dv = (int)f.dv;
+    c.scale = f.scale;
+    c.io_bf16 = dt == FI_BF16;
+    c.fresh = a->fresh != 0;
+    c.vec = view_vec(a->q, f.dk, es) && view_vec(a->k, f.dk, es) && view_vec(a->v, f.dv, es) && view_vec(a->o, f.dv, es);
+    c.ld = s->ld;
+    auto view = [](const fi_view &v) { return View{v.p, v.row, v.pos, v.head}; };
+    c.q = view(a->q);
+    c.k = view(a->k);
+    c.v = view(a->v);
+    c.o = view(a->o);
+    c.lens = a->lens;
+    c.slots = a->slots;
+    c.n_slots = a->state ? a->n_slots : kLim;   // without states every slot is fine
+    c.state = a->state;
+    return FI_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int fi_lattn_prompt(fi_lattn *s, const fi_lattn_args *a) {
+    LattnCall c;
+    const int rc = lattn_call(s, a, c);
+    if (rc != FI_OK || c.B == 0) return rc;
+    FI_HIP(launch_lattn_rec(c, s->stream));
+    return FI_OK;
+}
+
+int fi_lattn_step(fi_lattn *s, const fi_lattn_args *a) {
+    LattnCall c;
+    const int rc = lattn_call(s, a, c);
+    if (rc != FI_OK) return rc;
+    if (a->L != 1 || a->lens) return FI_ERR_INVALID;
+    if (c.B == 0) return FI_OK;
+    FI_HIP(launch_lattn_rec(c, s->stream));
+    return FI_OK;
+}
+
+// ------------------------------------------------------------ dense product
+int fi_dense_create(const fi_dense_config *cfg, fi_dense **out) {
+    if (out) *out = nullptr;
+    if (!cfg || !out) return FI_ERR_INVALID;
+    if (cfg->M < 1 || cfg->N < 1 || cfg->K < 1 || cfg->M >= kLim || cfg->N >= kLim || cfg->K >= kLim) return FI_ERR_INVALID;
+    const int act = raw_int(cfg->act);
+    if (!dtype_ok(raw_int(cfg->io_dtype)) || !dtype_ok(raw_int(cfg->out_dtype))) return FI_ERR_INVALID;
+    if (act != FI_ACT_GELU && act != FI_ACT_TANH && act != FI_ACT_IDENTITY) return FI_ERR_INVALID;
+    const int rc = check_device();
+    if (rc != FI_OK) return rc;
+    fi_dense *s = new (std::nothrow) fi_dense();
+    if (!s) return FI_ERR_NOMEM;
+    s->cfg = *cfg;
+    s->stream = static_cast<hipStream_t>(cfg->stream);
+    *out = s;
+    return FI_OK;
+}
+
+int fi_dense_run(fi_dense *s, const fi_dense_args *a) {
+    if (!s || !a || a->M < 0 || a->M > s->cfg.M) return FI_ERR_INVALID;
+    if (a->M == 0) return FI_OK;   // no rows: their arrays may be NULL
+    if (!a->x || !a->w || !a->y) return FI_ERR_INVALID;
+    const fi_dense_config &f = s->cfg;
+    if (a->ldx < f.K || a->ldw < f.K || a->ldy < f.N || (a->res && a->ldr < f.N)) return FI_ERR_INVALID;
+    if (!fits({a->ldx, f.M}, kMaxCount) || !fits({a->ldw, f.N}, kMaxCount) || !fits({a->ldy, f.M}, kMaxCount) ||
+        (a->res && !fits({a->ldr, f.M}, kMaxCount)))
+        return FI_ERR_INVALID;
+    const int io = raw_int(f.io_dtype), od = raw_int(f.out_dtype);
+    if (!aligned(a->x, esize(io)) || !aligned(a->w, esize(io)) || !aligned(a->bias, esize(io)) ||
+        !aligned(a->res, esize(od)) || !aligned(a->y, esize(od)))
+        return FI_ERR_INVALID;
+    const DenseCall c{a->M, f.N, f.K, io == FI_BF16, od == FI_BF16, raw_int(f.act), a->x, a->w, a->bias, a->res, a->y,
+                      a->ldx, a->ldw, a->ldr, a->ldy};
+    FI_HIP(launch_dense(c, s->stream));
+    return FI_OK;
+}
+
+void fi_dense_destroy(fi_dense *s) {
+    if (!s) return;
+    (void)hipStreamSynchronize(s->stream);
+    delete s;
+}
+
+// ------------------------------------------------------------ token scores
+int fi_scores_create(const fi_scores_config *cfg, fi_scores **out) {
+    if (out) *out = nullptr;
+    if (!cfg || !out) return FI_ERR_INVALID;
+    if (cfg->rows < 1 || cfg->V < 1 || cfg->rows >= kLim || cfg->V >= kLim) return FI_ERR_INVALID;
+    if (cfg->k < 0 || cfg->k > FI_SCORES_MAX_K || !dtype_ok(raw_int(cfg->io_dtype))) return FI_ERR_INVALID;
+    if (!(cfg->scale > 0.f) || !std::isfinite(cfg->scale)) return FI_ERR_INVALID;
+    const int rc = check_device();
+    if (rc != FI_OK) return rc;
+    fi_scores *s = new (std::nothrow) fi_scores();
+    if (!s) return FI_ERR_NOMEM;
+    s->cfg = *cfg;
+    s->stream = static_cast<hipStream_t>(cfg->stream);
+    *out = s;
+    return FI_OK;
+}
+
+int fi_scores_run(fi_scores *s, const fi_scores_args *a) {
+    if (!s || !a || a->rows < 0 || a->rows > s->cfg.rows) return FI_ERR_INVALID;
+    if (a->rows == 0) return FI_OK;   // no rows: their arrays may be NULL
+    const fi_scores_config &f = s->cfg;
+    if (!a->logits || a->ld < f.V || !fits({a->ld, f.rows}, kMaxCount)) return FI_ERR_INVALID;
+    if (!a->targets != !a->logprob || (f.k > 0 && (!a->top || !a->top_id))) return FI_ERR_INVALID;
+    const int io = raw_int(f.io_dtype);
+    if (!aligned(a->logits, esize(io)) || !aligned(a->targets, 8) || !aligned(a->top_id, 8)) return FI_ERR_INVALID;
+    for (const float *p : {a->logprob, a->entropy, a->lse, a->top})
+        if (!aligned(p, 4)) return FI_ERR_INVALID;
+    const ScoresCall c{a->rows, f.V, a->ld, f.k, io == FI_BF16, f.scale, a->logits, a->targets, a->logprob, a->entropy,
+                       a->lse, f.k > 0 ? a->top : nullptr, f.k > 0 ? a->top_id : nullptr};
+    FI_HIP(launch_scores(c, s->stream));
+    return FI_OK;
+}
+
+void fi_scores_destroy(fi_scores *s) {
+    if (!s) return;
+    (void)hipStreamSynchronize(s->stream);
+    delete s;
+}
+
+}  // extern "C"

@@ -1,0 +1,60 @@
+// fi_operators.h -- declarations shared by the host side of the operators
+// around the mixers (fi_operators.cpp) and their kernels (fi_lattn.hip,
+// fi_dense.hip, fi_scores.hip).  Not part of the public C ABI.
+#pragma once
+
+#include <hip/hip_runtime_api.h>
+#include <stdint.h>
+
+namespace fi {
+
+// ------------------------------------------------------------ linear attention
+struct View {
+    void *p;
+    int64_t row, pos, head;
+};
+
+// most B Hkv of a call: a launch has at most 2^32 threads, and 8 workgroups of 256 for each
+constexpr int64_t kLattnMaxRows = (int64_t)1 << 20;
+
+struct LattnCall {
+    int64_t B, n_slots;
+    int L, H, Hkv, G, dk, dv;   // G = H / Hkv
+    float scale;
+    int io_bf16, fresh;
+    int vec;                    // every view loads whole 16-byte units
+    const float *ld;            // [Hkv] log decay
+    View q, k, v, o;
+    const int32_t *lens, *slots;
+    float *state;
+};
+
+hipError_t launch_lattn_rec(const LattnCall &c, hipStream_t st);
+
+// ------------------------------------------------------------ dense product
+struct DenseCall {
+    int64_t M, N, K;
+    int io_bf16, out_bf16, act;
+    const void *x, *w, *bias, *res;
+    void *y;
+    int64_t ldx, ldw, ldr, ldy;
+};
+
+hipError_t launch_dense(const DenseCall &c, hipStream_t st);
+
+// ------------------------------------------------------------ token scores
+constexpr int kScoresMaxK = 32;
+
+struct ScoresCall {
+    int64_t rows, V, ld;
+    int k, io_bf16;
+    float scale;
+    const void *logits;
+    const int64_t *targets;
+    float *logprob, *entropy, *lse, *top;
+    int64_t *top_id;
+};
+
+hipError_t launch_scores(const ScoresCall &c, hipStream_t st);
+
+}  // namespace fi

@@ -247,6 +247,176 @@ typedef struct {
 } fi_tile;
 int fi_tile_at(int64_t L, int64_t i, fi_tile *out);
 
+/*
+ * Operators around the mixers: what a decoder that mixes long convolutions
+ * with linear attention runs between and after them.  They stand beside the
+ * convolution and use the same conventions: device pointers, asynchronous on
+ * the config's stream, FI_* status codes, arguments checked before any device
+ * work, and nothing allocated after the create calls.  A handle's calls share
+ * its workspace, so they are made in order on its one stream.
+ *
+ * An array of positions is given as a view: element c of head h at position t
+ * of row b lies at p + b*row + t*pos + h*head + c (strides counted in
+ * elements; any value, 0 broadcasts an input).  Elements of a head are
+ * adjacent.  The values do not depend on strides and alignment; aligned views
+ * (p, strides and head sizes in multiples of 16 bytes) load faster.
+ */
+typedef struct {
+    void *p;              /* aligned to its element */
+    int64_t row, pos, head;
+} fi_view;
+
+/*
+ * Linear attention with a decay per head.  For every row b, key/value head n
+ * and position t, with lam_n = exp(log_decay[n]) in [0, 1]:
+ *
+ *     S[t] = lam_n S[t-1] + k[t] v[t]^T           (S is dk x dv)
+ *     o[t][h] = scale * S[t]^T q[t][h]            for the H/Hkv query heads h of
+ *                                                 group n (h / (H/Hkv) == n)
+ *
+ * q, k, v and o are of io_dtype; S is held, summed and stored in fp32.  A
+ * state array is state[n_slots][Hkv][dk][dv] (fp32, dense, the caller's); row
+ * b uses slot slots[b], or slot b where slots is NULL.  A row whose slot is
+ * outside [0, n_slots) takes no part: its o is zero and no state changes.
+ * Two rows of one call must not share a slot (their updates would race).
+ */
+typedef struct fi_lattn fi_lattn;   /* opaque; owns its device memory */
+typedef struct {
+    int64_t B;                /* most rows of one call, >= 1 */
+    int64_t L;                /* most positions of one fi_lattn_prompt call, >= 1 */
+    int64_t H;                /* query heads, a multiple of Hkv */
+    int64_t Hkv;              /* key/value heads, >= 1 */
+    int64_t dk, dv;           /* sizes of a key and of a value head, 1 .. 256 */
+    float scale;              /* multiplies o; finite */
+    fi_dtype io_dtype;        /* type of q, k, v and o */
+    void *stream;             /* hipStream_t; NULL = the null stream */
+} fi_lattn_config;
+
+typedef struct {
+    int64_t B, L;             /* rows and positions of this call, within the config's */
+    fi_view q, k, v;          /* [B][L][H][dk], [B][L][Hkv][dk], [B][L][Hkv][dv] */
+    fi_view o;                /* [B][L][H][dv]; overlaps no input */
+    const int32_t *lens;      /* [B] on the device: row b has lens[b] positions (taken into [0, L]); NULL:
+                                 all have L.  What lies past a row's end is not read as a number; o is zero there. */
+    const int32_t *slots;     /* [B] on the device, or NULL */
+    int64_t n_slots;          /* states in `state` (>= B where slots is NULL) */
+    float *state;             /* read and updated in place, aligned to 16 bytes; may be NULL in a fresh prompt */
+    int32_t fresh;            /* nonzero: every row begins from S = 0, whatever its slot holds */
+} fi_lattn_args;
+
+/* fi_lattn_create: copies log_decay[Hkv] (device, fp32; each <= 0, -inf for
+ * lam = 0) and allocates the workspace of the longest prompt.  Synchronous.
+ * FI_ERR_INVALID for a NULL pointer, a size < 1, H not a multiple of Hkv, a
+ * NaN or positive log_decay, an infinite or NaN scale, an unknown dtype or
+ * sizes that overflow; FI_ERR_UNSUPPORTED for dk or dv > 256, L > FI_MAX_L,
+ * B Hkv > 2^20 or a device that is not gfx950; FI_ERR_NOMEM / FI_ERR_HIP from the device. */
+int fi_lattn_create(const fi_lattn_config *cfg, const float *log_decay, fi_lattn **out);
+
+/* fi_lattn_prompt: L given positions of every row in the chunked form (matrix
+ * products over chunks of positions), from the row's state, which is left
+ * after its last position.  B = 0 and L = 0 are allowed.  FI_ERR_INVALID for
+ * a NULL pointer, sizes beyond the config's, fewer than B states without
+ * slots, or a pointer that is not aligned to its element.  A NaN or infinity
+ * in k or v at t makes every later output and the state not finite, and can
+ * make outputs of up to 63 positions before t of its row and head NaN. */
+int fi_lattn_prompt(fi_lattn *s, const fi_lattn_args *a);
+
+/* fi_lattn_step: one new position of every row in the recurrent form; L is 1
+ * and lens NULL (else FI_ERR_INVALID).  Errors as fi_lattn_prompt. */
+int fi_lattn_step(fi_lattn *s, const fi_lattn_args *a);
+
+/* fi_lattn_destroy: synchronise the stream and free everything; NULL is a no-op. */
+void fi_lattn_destroy(fi_lattn *s);
+
+/*
+ * Dense product with its epilogue, for any number of rows:
+ *
+ *     y[m][n] = act(sum_k x[m][k] w[n][k] + bias[n]) + res[m][n]
+ *
+ * x[M][K], w[N][K] (row n = output n, as the stack's blocks) and bias[N] are
+ * of io_dtype, res and y of out_dtype; sums are fp32 (fp32 storage: fp32
+ * products), rounded once.  Rows are ld* elements apart.
+ */
+typedef struct fi_dense fi_dense;   /* opaque; owns its device memory */
+typedef struct {
+    int64_t M;                /* most rows of one call, >= 1 */
+    int64_t N, K;             /* outputs and inputs of a row, >= 1 */
+    fi_dtype io_dtype, out_dtype;
+    fi_activation act;
+    void *stream;             /* hipStream_t; NULL = the null stream */
+} fi_dense_config;
+typedef struct {
+    int64_t M;                /* rows of this call, 0 .. the config's */
+    const void *x; int64_t ldx;
+    const void *w; int64_t ldw;
+    const void *bias;         /* or NULL */
+    const void *res; int64_t ldr;   /* res or NULL; res = y with ldr = ldy adds in place */
+    void *y; int64_t ldy;     /* overlaps no other input */
+} fi_dense_args;
+
+/* fi_dense_create: allocates the workspace.  FI_ERR_INVALID for a NULL
+ * pointer, a size < 1 or beyond 2^31 - 1, an unknown dtype or activation;
+ * FI_ERR_UNSUPPORTED when the device is not gfx950; FI_ERR_NOMEM / FI_ERR_HIP
+ * from the device. */
+int fi_dense_create(const fi_dense_config *cfg, fi_dense **out);
+
+/* fi_dense_run: FI_ERR_INVALID for a NULL pointer, M beyond the config's, a
+ * row stride below the row's length (ldx, ldw >= K; ldr, ldy >= N), or a
+ * pointer that is not aligned to its element. */
+int fi_dense_run(fi_dense *s, const fi_dense_args *a);
+
+/* fi_dense_destroy: synchronise the stream and free everything; NULL is a no-op. */
+void fi_dense_destroy(fi_dense *s);
+
+/*
+ * Token scores: per row of logits z[V] (times `scale`, 1/temperature), with
+ * p = softmax(scale z) in fp32,
+ *
+ *     lse = log sum_j exp(scale z[j]),   logprob = scale z[target] - lse,
+ *     entropy = -sum_j p[j] log p[j],
+ *     top[0..k), top_id[0..k): the k most probable tokens, log probability and
+ *         index, most probable first, ties to the lowest index.
+ *
+ * A logit of -inf is a token that a mask rules out: it adds nothing, its log
+ * probability is -inf and it is no alternative; where fewer than k tokens are
+ * left, the further entries are -1 and -inf.  A row without any token has lse
+ * and logprob -inf and entropy 0.  A row with a NaN or +inf has NaN in lse,
+ * logprob, entropy and top, and -1 in top_id.  A target < 0 asks for nothing
+ * (logprob 0); one >= V gives NaN.
+ */
+typedef struct fi_scores fi_scores;   /* opaque; owns its device memory */
+#define FI_SCORES_MAX_K 32
+typedef struct {
+    int64_t rows;             /* most rows of one call, >= 1 */
+    int64_t V;                /* tokens of the vocabulary, 1 .. 2^31 - 1 */
+    int32_t k;                /* alternatives per row, 0 .. FI_SCORES_MAX_K */
+    fi_dtype io_dtype;        /* type of the logits */
+    float scale;              /* finite, > 0 */
+    void *stream;             /* hipStream_t; NULL = the null stream */
+} fi_scores_config;
+typedef struct {
+    int64_t rows;             /* rows of this call, 0 .. the config's */
+    const void *logits; int64_t ld;   /* rows ld >= V elements apart */
+    const int64_t *targets;   /* [rows], or NULL (then logprob is NULL too) */
+    float *logprob, *entropy, *lse;   /* [rows] each; each may be NULL */
+    float *top;               /* [rows][k]; NULL where k = 0 */
+    int64_t *top_id;          /* [rows][k]; NULL where k = 0 */
+} fi_scores_args;
+
+/* fi_scores_create: allocates the workspace.  FI_ERR_INVALID for a NULL
+ * pointer, a size, k or scale out of range or an unknown dtype;
+ * FI_ERR_UNSUPPORTED when the device is not gfx950; FI_ERR_NOMEM / FI_ERR_HIP
+ * from the device. */
+int fi_scores_create(const fi_scores_config *cfg, fi_scores **out);
+
+/* fi_scores_run: FI_ERR_INVALID for a NULL handle, args or logits, rows beyond
+ * the config's, ld < V, logprob without targets (or targets without logprob),
+ * top or top_id NULL where k > 0, or a pointer not aligned to its element. */
+int fi_scores_run(fi_scores *s, const fi_scores_args *a);
+
+/* fi_scores_destroy: synchronise the stream and free everything; NULL is a no-op. */
+void fi_scores_destroy(fi_scores *s);
+
 #ifdef __cplusplus
 }
 #endif
