@@ -18,6 +18,7 @@ struct fi_lattn {
     fi_lattn_config cfg;
     hipStream_t stream;
     float *ld;     // [Hkv] log decay, device
+    float *ws;     // entry states of a split prompt's segments
 };
 
 struct fi_dense {
@@ -77,13 +78,16 @@ int fi_lattn_create(const fi_lattn_config *cfg, const float *log_decay, fi_lattn
     if (!s) return FI_ERR_NOMEM;
     s->cfg = *cfg;
     s->stream = static_cast<hipStream_t>(cfg->stream);
-    s->ld = nullptr;
+    s->ld = s->ws = nullptr;
     const size_t bytes = (size_t)cfg->Hkv * sizeof(float);
     float *host = new (std::nothrow) float[(size_t)cfg->Hkv];
     hipError_t e = host ? dalloc(&s->ld, bytes) : hipErrorOutOfMemory;
     if (e == hipSuccess) e = hipMemcpyAsync(s->ld, log_decay, bytes, hipMemcpyDeviceToDevice, s->stream);
     if (e == hipSuccess) e = hipMemcpyAsync(host, log_decay, bytes, hipMemcpyDeviceToHost, s->stream);
     if (e == hipSuccess) e = hipStreamSynchronize(s->stream);
+    const size_t ws = lattn_ws_bytes(cfg->B, cfg->L, (int)cfg->Hkv, (int)cfg->dk, (int)cfg->dv,
+                                     raw_int(cfg->io_dtype) == FI_BF16);
+    if (e == hipSuccess && ws > 0) e = dalloc(&s->ws, ws);
     bool ok = e == hipSuccess;
     for (int64_t n = 0; ok && n < cfg->Hkv; ++n) ok = host[n] <= 0.f;   // false for NaN
     delete[] host;
@@ -99,6 +103,7 @@ void fi_lattn_destroy(fi_lattn *s) {
     if (!s) return;
     (void)hipStreamSynchronize(s->stream);
     if (s->ld) (void)hipFree(s->ld);
+    if (s->ws) (void)hipFree(s->ws);
     delete s;
 }
 
@@ -144,6 +149,9 @@ int lattn_call(const fi_lattn *s, const fi_lattn_args *a, LattnCall &c) {
     c.slots = a->slots;
     c.n_slots = a->state ? a->n_slots : kLim;   // without states every slot is fine
     c.state = a->state;
+    c.ws = s->ws;
+    c.nseg = 1;
+    c.seg_chunks = 0;
     return FI_OK;
 }
 
@@ -155,7 +163,7 @@ int fi_lattn_prompt(fi_lattn *s, const fi_lattn_args *a) {
     LattnCall c;
     const int rc = lattn_call(s, a, c);
     if (rc != FI_OK || c.B == 0) return rc;
-    FI_HIP(launch_lattn_rec(c, s->stream));
+    FI_HIP(launch_lattn_chunk(c, s->stream));
     return FI_OK;
 }
 
