@@ -105,37 +105,9 @@ hipError_t launch_lattn_rec(const LattnCall& c, hipStream_t st) {
 //     S = lam^C E + K^T diag(lam^{C-1-j}) V
 // A row's first chunk is filled from the back (zero rows in front), so that
 // every later one is whole and ends on the row's last position.
-using BF8 = BF __attribute__((ext_vector_type(8)));
-using BF4 = BF __attribute__((ext_vector_type(4)));
-using S4 = short __attribute__((ext_vector_type(4)));
-
-// Operands of the matrix cores, 16 x KB each: lane l has row (column) l % 16
-// and, with g = l / 16, the E values k(g, e) of the KB long axis.  Products
-// sum over k, so any k(g, e) serves that both operands share.  The result has
-// column l % 16 and rows 4 g .. 4 g + 3.
-template <bool BF16>
-struct Mm;
-template <>
-struct Mm<true> {
-    using T = BF;
-    static constexpr int C = 64, KB = 32, E = 8, Pad = 8;   // positions of a chunk; LDS rows are Pad elements longer
-    using Frag = BF8;
-    static __device__ __forceinline__ V4 mma(Frag a, Frag b, V4 c) {
-        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
-    }
-};
-template <>
-struct Mm<false> {
-    using T = float;
-    static constexpr int C = 32, KB = 16, E = 4, Pad = 4;
-    using Frag = V4;
-    static __device__ __forceinline__ V4 mma(Frag a, Frag b, V4 c) {
-        for (int e = 0; e < 4; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[e], b[e], c, 0, 0, 0);
-        return c;
-    }
-};
-
 constexpr int kLaThreads = 256;
+constexpr int la_chunk(bool bf16) { return bf16 ? 64 : 32; }   // positions of a chunk
+
 
 // 16 bytes of a head's row: elements c .. c + E - 1 below d, zero elsewhere
 template <bool BF16>
@@ -158,8 +130,8 @@ __global__ __launch_bounds__(kLaThreads, 2) void k_lattn_chunk(LattnCall a) {
     using M = Mm<BF16>;
     using T = typename M::T;
     using Frag = typename M::Frag;
-    constexpr int C = M::C, KB = M::KB, E = M::E;
-    constexpr int PK = DK + M::Pad, PV = DVS + M::Pad, PP = C + M::Pad;   // LDS rows
+    constexpr int C = la_chunk(BF16), KB = M::KB, E = M::E;
+    constexpr int PK = DK + E, PV = DVS + E, PP = C + E;   // LDS rows, 16 bytes longer
     constexpr int NT = DVS / 64, KT = DK / 16, CT = C / 16;               // column tiles of a wave; tiles of dk; of C
     constexpr int UK = C * DK / E / kLaThreads, UV = C * DVS / E / kLaThreads;   // 16-byte units per thread
     __shared__ __align__(16) T ks[C * PK], vs[C * PV], qs[OUT ? C * PK : 1], ps[OUT ? C * PP : 1];
@@ -461,7 +433,7 @@ __global__ __launch_bounds__(kLaThreads, 2) void k_lattn_chunk(LattnCall a) {
 // segment s's own products and becomes lam^{n_s} ws[s] + those; ws[0] = S_0.
 template <bool BF16>
 __global__ __launch_bounds__(256) void k_lattn_scan(LattnCall a) {
-    constexpr int C = Mm<BF16>::C;
+    constexpr int C = la_chunk(BF16);
     const int per = a.dk * a.dv, blocks = (per + 255) / 256;
     const int task = blockIdx.x / blocks, b = task / a.Hkv, n = task % a.Hkv;
     const int i = blockIdx.x % blocks * 256 + threadIdx.x;
@@ -514,7 +486,7 @@ void chunk_launches(const LattnCall& c, hipStream_t st) {
 template <bool BF16>
 hipError_t chunk_dims(LattnCall& c, hipStream_t st) {
     const int cols = slice_cols(c.dk);
-    c.nseg = segments(c.B * c.Hkv, (c.dv + cols - 1) / cols, (c.L + Mm<BF16>::C - 1) / Mm<BF16>::C, &c.seg_chunks);
+    c.nseg = segments(c.B * c.Hkv, (c.dv + cols - 1) / cols, (c.L + la_chunk(BF16) - 1) / la_chunk(BF16), &c.seg_chunks);
     if (c.dk <= 64) chunk_launches<BF16, 64, 64>(c, st);
     else if (c.dk <= 128) chunk_launches<BF16, 128, 128>(c, st);
     else chunk_launches<BF16, 256, 64>(c, st);
@@ -524,7 +496,7 @@ hipError_t chunk_dims(LattnCall& c, hipStream_t st) {
 }  // namespace
 
 size_t lattn_ws_bytes(int64_t B, int64_t L, int Hkv, int dk, int dv, int io_bf16) {
-    const int C = io_bf16 ? Mm<true>::C : Mm<false>::C, cols = slice_cols(dk), slices = (dv + cols - 1) / cols;
+    const int C = la_chunk(io_bf16), cols = slice_cols(dk), slices = (dv + cols - 1) / cols;
     int64_t most = 0;   // states of any call's segments; a call of n rows is split into at most kLaWorkgroups / n
     for (int64_t b = 1; b <= B && b * Hkv * slices <= kLaWorkgroups; ++b) {
         int sc;

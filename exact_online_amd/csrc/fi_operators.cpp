@@ -24,6 +24,7 @@ struct fi_lattn {
 struct fi_dense {
     fi_dense_config cfg;
     hipStream_t stream;
+    float *part;   // partial sums of products split over K
 };
 
 struct fi_scores {
@@ -185,12 +186,20 @@ int fi_dense_create(const fi_dense_config *cfg, fi_dense **out) {
     const int act = raw_int(cfg->act);
     if (!dtype_ok(raw_int(cfg->io_dtype)) || !dtype_ok(raw_int(cfg->out_dtype))) return FI_ERR_INVALID;
     if (act != FI_ACT_GELU && act != FI_ACT_TANH && act != FI_ACT_IDENTITY) return FI_ERR_INVALID;
+    if (cfg->M > kDenseMaxRows || cfg->N > kDenseMaxRows) return FI_ERR_UNSUPPORTED;
     const int rc = check_device();
     if (rc != FI_OK) return rc;
     fi_dense *s = new (std::nothrow) fi_dense();
     if (!s) return FI_ERR_NOMEM;
     s->cfg = *cfg;
     s->stream = static_cast<hipStream_t>(cfg->stream);
+    s->part = nullptr;
+    const size_t ws = dense_ws_bytes(cfg->M, cfg->N, cfg->K);
+    const hipError_t e = ws > 0 ? dalloc(&s->part, ws) : hipSuccess;
+    if (e != hipSuccess) {
+        delete s;
+        return hip_fail(e);
+    }
     *out = s;
     return FI_OK;
 }
@@ -209,7 +218,7 @@ int fi_dense_run(fi_dense *s, const fi_dense_args *a) {
         !aligned(a->res, esize(od)) || !aligned(a->y, esize(od)))
         return FI_ERR_INVALID;
     const DenseCall c{a->M, f.N, f.K, io == FI_BF16, od == FI_BF16, raw_int(f.act), a->x, a->w, a->bias, a->res, a->y,
-                      a->ldx, a->ldw, a->ldr, a->ldy};
+                      a->ldx, a->ldw, a->ldr, a->ldy, s->part, 0, 0, 1};
     FI_HIP(launch_dense(c, s->stream));
     return FI_OK;
 }
@@ -217,6 +226,7 @@ int fi_dense_run(fi_dense *s, const fi_dense_args *a) {
 void fi_dense_destroy(fi_dense *s) {
     if (!s) return;
     (void)hipStreamSynchronize(s->stream);
+    if (s->part) (void)hipFree(s->part);
     delete s;
 }
 

@@ -39,15 +39,24 @@ hipError_t launch_lattn_chunk(LattnCall c, hipStream_t st);
 size_t lattn_ws_bytes(int64_t B, int64_t L, int Hkv, int dk, int dv, int io_bf16);
 
 // ------------------------------------------------------------ dense product
+// most M and N: a launch has at most 2^32 threads
+constexpr int64_t kDenseMaxRows = (int64_t)1 << 27;
+
 struct DenseCall {
     int64_t M, N, K;
     int io_bf16, out_bf16, act;
     const void *x, *w, *bias, *res;
     void *y;
     int64_t ldx, ldw, ldr, ldy;
+    // a product split over K: parts of k_split, part[splits][M][ldp]
+    float *part;
+    int64_t k_split, ldp;
+    int splits;
 };
 
-hipError_t launch_dense(const DenseCall &c, hipStream_t st);
+// Chooses the kernel and the split; c.part holds dense_ws_bytes of the handle's M, N, K.
+hipError_t launch_dense(DenseCall c, hipStream_t st);
+size_t dense_ws_bytes(int64_t M, int64_t N, int64_t K);
 
 // ------------------------------------------------------------ token scores
 constexpr int kScoresMaxK = 32;

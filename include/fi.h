@@ -356,8 +356,8 @@ typedef struct {
 
 /* fi_dense_create: allocates the workspace.  FI_ERR_INVALID for a NULL
  * pointer, a size < 1 or beyond 2^31 - 1, an unknown dtype or activation;
- * FI_ERR_UNSUPPORTED when the device is not gfx950; FI_ERR_NOMEM / FI_ERR_HIP
- * from the device. */
+ * FI_ERR_UNSUPPORTED for M or N > 2^27 or when the device is not gfx950;
+ * FI_ERR_NOMEM / FI_ERR_HIP from the device. */
 int fi_dense_create(const fi_dense_config *cfg, fi_dense **out);
 
 /* fi_dense_run: FI_ERR_INVALID for a NULL pointer, M beyond the config's, a
