@@ -30,6 +30,8 @@ struct fi_dense {
 struct fi_scores {
     fi_scores_config cfg;
     hipStream_t stream;
+    float *pst;                  // partial sums and alternatives of rows' parts
+    unsigned long long *pkey;
 };
 
 namespace {
@@ -243,6 +245,16 @@ int fi_scores_create(const fi_scores_config *cfg, fi_scores **out) {
     if (!s) return FI_ERR_NOMEM;
     s->cfg = *cfg;
     s->stream = static_cast<hipStream_t>(cfg->stream);
+    s->pst = nullptr;
+    s->pkey = nullptr;
+    const size_t parts = scores_ws_parts(cfg->rows, cfg->V, raw_int(cfg->io_dtype) == FI_BF16);
+    hipError_t e = hipSuccess;
+    if (parts > 0) e = dalloc(&s->pst, parts * 3 * sizeof(float));
+    if (e == hipSuccess && parts > 0 && cfg->k > 0) e = dalloc(&s->pkey, parts * cfg->k * sizeof(unsigned long long));
+    if (e != hipSuccess) {
+        fi_scores_destroy(s);
+        return hip_fail(e);
+    }
     *out = s;
     return FI_OK;
 }
@@ -258,7 +270,7 @@ int fi_scores_run(fi_scores *s, const fi_scores_args *a) {
     for (const float *p : {a->logprob, a->entropy, a->lse, a->top})
         if (!aligned(p, 4)) return FI_ERR_INVALID;
     const ScoresCall c{a->rows, f.V, a->ld, f.k, io == FI_BF16, f.scale, a->logits, a->targets, a->logprob, a->entropy,
-                       a->lse, f.k > 0 ? a->top : nullptr, f.k > 0 ? a->top_id : nullptr};
+                       a->lse, f.k > 0 ? a->top : nullptr, f.k > 0 ? a->top_id : nullptr, 1, 0, s->pst, s->pkey};
     FI_HIP(launch_scores(c, s->stream));
     return FI_OK;
 }
@@ -266,6 +278,8 @@ int fi_scores_run(fi_scores *s, const fi_scores_args *a) {
 void fi_scores_destroy(fi_scores *s) {
     if (!s) return;
     (void)hipStreamSynchronize(s->stream);
+    if (s->pst) (void)hipFree(s->pst);
+    if (s->pkey) (void)hipFree(s->pkey);
     delete s;
 }
 

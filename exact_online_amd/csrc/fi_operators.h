@@ -69,8 +69,14 @@ struct ScoresCall {
     const int64_t *targets;
     float *logprob, *entropy, *lse, *top;
     int64_t *top_id;
+    // a row's parts of `per` logits; of several: pst[rows][parts][3] and pkey[rows][parts][k]
+    int parts;
+    int64_t per;
+    float *pst;
+    unsigned long long *pkey;
 };
 
-hipError_t launch_scores(const ScoresCall &c, hipStream_t st);
+hipError_t launch_scores(ScoresCall c, hipStream_t st);
+size_t scores_ws_parts(int64_t rows, int64_t V, int io_bf16);   // most rows x parts of a call
 
 }  // namespace fi

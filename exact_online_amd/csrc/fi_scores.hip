@@ -1,15 +1,18 @@
 // fi_scores.hip -- log probability of a given token, entropy and the most
 // probable tokens of every row of logits (fi_scores_*).
 //
-// One pass keeps, with m the largest logit so far and t = (z - m) c, c =
-// scale log2(e): s = sum 2^t and w = sum t 2^t.  Then, in units of log2,
-// lse = c m + log2 s and entropy = log2 s - w / s.
+// One pass keeps, with a reference m near the largest logit and t = (z - m) c,
+// c = scale log2(e): s = sum 2^t and w = sum t 2^t.  Then, in units of log2,
+// lse = c m + log2 s and entropy = log2 s - w / s.  The subtraction comes
+// before the scaling, so large logits lose nothing.
 #include "fi_opdev.hpp"
 
 namespace fi {
 
-constexpr int kScThreads = 256;
+constexpr int kScThreads = 256, kScWaves = kScThreads / kWave;
+constexpr int kScUnroll = 4;          // 16-byte loads of a lane in one batch
 constexpr float kScLow = -16384.f;    // 2^kScLow = 0, and 0 kScLow = 0
+constexpr float kScHigh = 16.f;       // t beyond this moves the reference
 constexpr float kLn2 = 0.69314718055994531f, kLog2e = 1.44269504088896341f;
 
 struct Stats {
@@ -23,84 +26,284 @@ __device__ __forceinline__ Stats join(Stats a, Stats b, float c) {
     return {m, a.s * ea + b.s * eb, ea * (a.w + da * a.s) + eb * (b.w + db * b.s)};
 }
 
+__device__ __forceinline__ Stats join_wave(Stats x, float c) {
+    for (int d = 1; d < kWave; d <<= 1) x = join(x, {__shfl_xor(x.m, d), __shfl_xor(x.s, d), __shfl_xor(x.w, d)}, c);
+    return x;
+}
+
+// Alternatives as one number that orders them: the value's bits, then the
+// index from the back.  0 is none.
+using Key = unsigned long long;
+__device__ __forceinline__ uint32_t ordered(float v) {
+    const uint32_t u = __float_as_uint(v + 0.f);   // -0 ties with 0
+    return u >> 31 ? ~u : u | 0x80000000u;
+}
+__device__ __forceinline__ float value_of(uint32_t o) { return __uint_as_float(o >> 31 ? o & 0x7FFFFFFFu : ~o); }
+__device__ __forceinline__ Key key_of(float v, uint32_t id) { return (Key)ordered(v) << 32 | ~id; }
+
+// A threshold that at least k of a wave's values reach and, where a few steps
+// of bisection find one, at most 3/2 k + 8.
+__device__ __forceinline__ uint32_t reached_by(uint32_t o, int k) {
+    uint32_t lo = 0, hi = 0xFFFFFFFFu;   // lo is reached by k of them, hi + 1 is not
+    while (lo < hi) {
+        const uint32_t mid = lo + (hi - lo) / 2 + 1;
+        const int n = __popcll(__ballot(o >= mid));
+        if (n >= k) {
+            lo = mid;
+            if (n <= k + k / 2 + 8) break;
+        } else hi = mid - 1;
+    }
+    return lo;
+}
+
+// Writes a row's results; lane j < k of the calling wave has alternative j.
 template <bool BF16>
-__global__ __launch_bounds__(kScThreads) void k_scores(ScoresCall a) {
-    __shared__ Stats st[kScThreads];
-    __shared__ float tv[kScThreads];
-    __shared__ int64_t ti[kScThreads];
-    const int tid = threadIdx.x;
-    const float c = a.scale * kLog2e;
-    for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
-        Stats x = {-__FLT_MAX__, 0.f, 0.f};
-        for (int64_t j = tid; j < a.V; j += kScThreads) {
-            const float z = get_io<BF16>(a.logits, r * a.ld + j);
-            if (z > x.m) {
-                x = join(x, {z, 0.f, 0.f}, c);
-            }
-            const float t = (z - x.m) * c, e = exp2f(t);
-            x.s += e;
-            x.w = fmaf(e, fmaxf(t, kScLow), x.w);
-        }
-        st[tid] = x;
-        __syncthreads();
-        for (int d = kScThreads / 2; d > 0; d >>= 1) {
-            if (tid < d) st[tid] = join(st[tid], st[tid + d], c);
-            __syncthreads();
-        }
-        x = st[0];
-        const bool empty = x.s == 0.f, bad = !(x.s < __builtin_inff());
-        const float l2 = log2f(x.s);
-        const float lse = empty ? -__builtin_inff() : fmaf(x.m, a.scale, l2 * kLn2);
-        if (tid == 0) {
-            if (a.lse) a.lse[r] = bad ? __builtin_nanf("") : lse;
-            if (a.entropy) a.entropy[r] = empty ? 0.f : bad ? __builtin_nanf("") : (l2 - x.w / x.s) * kLn2;
-            if (a.logprob) {
-                const int64_t t = a.targets[r];
-                float lp;
-                if (t < 0) lp = 0.f;
-                else if (t >= a.V || bad) lp = __builtin_nanf("");
-                else if (empty) lp = -__builtin_inff();
-                else lp = fmaf(get_io<BF16>(a.logits, r * a.ld + t) - x.m, a.scale, -l2 * kLn2);
-                a.logprob[r] = lp;
-            }
-        }
-        float pv = __builtin_inff();
-        int64_t pi = -1;
-        for (int k = 0; k < a.k; ++k) {
-            // the best of what comes after (pv, pi)
-            float bv = -__builtin_inff();
-            int64_t bi = -1;
-            for (int64_t j = tid; j < a.V; j += kScThreads) {
-                const float z = get_io<BF16>(a.logits, r * a.ld + j);
-                if ((z < pv || (z == pv && j > pi)) && z > bv) bv = z, bi = j;
-            }
-            tv[tid] = bv;
-            ti[tid] = bi;
-            __syncthreads();
-            for (int d = kScThreads / 2; d > 0; d >>= 1) {
-                if (tid < d) {
-                    const float v = tv[tid + d];
-                    const int64_t i = ti[tid + d];
-                    if (i >= 0 && (ti[tid] < 0 || v > tv[tid] || (v == tv[tid] && i < ti[tid]))) tv[tid] = v, ti[tid] = i;
-                }
-                __syncthreads();
-            }
-            pv = tv[0];
-            pi = ti[0];
-            if (tid == 0) {
-                a.top[r * a.k + k] = bad ? __builtin_nanf("") : pi < 0 ? -__builtin_inff() : fmaf(pv - x.m, a.scale, -l2 * kLn2);
-                a.top_id[r * a.k + k] = bad ? -1 : pi;
-            }
-            __syncthreads();
-            if (pi < 0) pv = -__builtin_inff();
-        }
+__device__ __forceinline__ void scores_out(const ScoresCall& a, int64_t r, Stats x, Key alt, int lane) {
+    const float inf = __builtin_inff(), nan = __builtin_nanf("");
+    const bool empty = x.s == 0.f, bad = !(x.s < inf);
+    const float l2 = log2f(x.s), ln = l2 * kLn2;
+    if (lane < a.k) {
+        float v = -inf;
+        if (alt) v = fmaf(value_of((uint32_t)(alt >> 32)) - x.m, a.scale, -ln);
+        a.top[r * a.k + lane] = bad ? nan : v;
+        a.top_id[r * a.k + lane] = bad || !alt ? -1 : (int64_t)(uint32_t)~alt;
+    }
+    if (lane) return;
+    if (a.lse) a.lse[r] = bad ? nan : empty ? -inf : fmaf(x.m, a.scale, ln);
+    if (a.entropy) a.entropy[r] = empty ? 0.f : bad ? nan : (l2 - x.w / x.s) * kLn2;
+    if (a.logprob) {
+        const int64_t t = a.targets[r];
+        float lp;
+        if (t < 0) lp = 0.f;
+        else if (t >= a.V || bad) lp = nan;
+        else if (empty) lp = -inf;
+        else lp = fmaf(get_io<BF16>(a.logits, r * a.ld + t) - x.m, a.scale, -ln);
+        a.logprob[r] = lp;
     }
 }
 
-hipError_t launch_scores(const ScoresCall& c, hipStream_t st) {
-    const unsigned grid = (unsigned)(c.rows < (1 << 22) ? c.rows : 1 << 22);
-    if (c.io_bf16) k_scores<true><<<grid, kScThreads, 0, st>>>(c);
-    else k_scores<false><<<grid, kScThreads, 0, st>>>(c);
+// A workgroup takes one part of one row, each wave a run of it; one part: the
+// whole row, and the results go out at once.
+template <bool BF16>
+__global__ __launch_bounds__(kScThreads) void k_scores(ScoresCall a) {
+    using M = Mm<BF16>;
+    using T = typename M::T;
+    using Frag = typename M::Frag;
+    constexpr int E = M::E, STEP = kWave * E, BATCH = kScUnroll * STEP;
+    __shared__ Stats wst[kScWaves];
+    __shared__ Key wk[kScWaves][kScoresMaxK], out[kScoresMaxK];
+    const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave, k = a.k;
+    const float c = a.scale * kLog2e, inf = __builtin_inff();
+    const int64_t r = blockIdx.x / a.parts;
+    const int part = blockIdx.x % a.parts;
+    const T* row = static_cast<const T*>(a.logits) + r * a.ld;
+    const int64_t v0 = (int64_t)part * a.per + wave * (a.per / kScWaves);
+    int64_t v1 = v0 + a.per / kScWaves;
+    if (v1 > a.V) v1 = a.V;
+
+    Stats x = {-__FLT_MAX__, 0.f, 0.f};   // m is the wave's, s and w the lane's
+    float lv = -inf, thr = -inf;          // the wave's alternatives, best first, one a lane; what a new one exceeds
+    uint32_t li = 0xFFFFFFFFu;
+    const auto load = [&](Frag* f, int64_t v) {
+#pragma unroll
+        for (int u = 0; u < kScUnroll; ++u) {
+            const int64_t at = v + u * STEP + lane * E;
+            using Loose = T __attribute__((ext_vector_type(E), aligned(sizeof(T))));
+            if (at + E <= v1) f[u] = *gmem(reinterpret_cast<const Loose*>(row + at));
+            else
+#pragma unroll
+                for (int e = 0; e < E; ++e) f[u][e] = at + e < v1 ? gmem(row)[at + e] : (T)-inf;
+        }
+    };
+    Frag now[kScUnroll], next[kScUnroll];
+    if (v0 < v1) load(now, v0);
+    for (int64_t v = v0; v < v1; v += BATCH) {
+        if (v + BATCH < v1) load(next, v + BATCH);
+        float big[kScUnroll], most = -inf;
+#pragma unroll
+        for (int u = 0; u < kScUnroll; ++u) {
+            big[u] = (float)now[u][0];
+#pragma unroll
+            for (int e = 1; e < E; ++e) big[u] = fmaxf(big[u], (float)now[u][e]);
+            most = fmaxf(most, big[u]);
+        }
+        if (v == v0 || __ballot((most - x.m) * c > kScHigh)) {
+            float m = fmaxf(most, x.m);
+            for (int d = 1; d < kWave; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
+            const float t = fmaxf((x.m - m) * c, kScLow), e = exp2f(t);
+            x.w = e * (x.w + t * x.s);
+            x.s *= e;
+            x.m = m;
+        }
+#pragma unroll
+        for (int u = 0; u < kScUnroll; ++u)
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const float t = ((float)now[u][e] - x.m) * c, p = __builtin_amdgcn_exp2f(t);
+                x.s += p;
+                x.w = fmaf(p, fmaxf(t, kScLow), x.w);   // -inf: 0 (-2^14)
+            }
+        if (k) {
+            if (v == v0) {
+                // of the first batch, only what reaches the k-th largest lane or so
+                const uint32_t o = reached_by(ordered(most), k);
+                const float f = value_of(o - (o == 0x80000000u ? 2 : 1));   // the next value below; -0 is 0
+                if (o && f > -inf) thr = f;                                  // false for NaN bits too
+            }
+#pragma unroll
+            for (int u = 0; u < kScUnroll; ++u) {
+                uint64_t lanes = __ballot(big[u] > thr);
+                while (lanes) {   // by index: equal values stay in their order
+                    const int l = __builtin_ctzll(lanes);
+#pragma unroll
+                    for (int e = 0; e < E; ++e) {
+                        const float z = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint((float)now[u][e]), l));
+                        if (z > thr) {
+                            const int at = __popcll(__ballot(lv >= z));
+                            const float pv = wave_shr1(lv);
+                            const uint32_t pi = __builtin_amdgcn_update_dpp(0, (int)li, 0x138, 0xf, 0xf, true);
+                            lv = lane < at ? lv : lane == at ? z : pv;
+                            li = lane < at ? li : lane == at ? (uint32_t)(v + u * STEP + l * E + e) : pi;
+                            const float kth = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(lv), k - 1));
+                            thr = fmaxf(thr, kth);
+                        }
+                    }
+                    lanes &= lanes - 1;
+                    lanes &= __ballot(big[u] > thr);
+                }
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kScUnroll; ++u) now[u] = next[u];
+    }
+    x = join_wave(x, c);
+    if (lane == 0) wst[wave] = x;
+    if (lane < k) wk[wave][lane] = lv > -inf ? key_of(lv, li) : 0;
+    if (tid < kScoresMaxK) out[tid] = 0;
+    __syncthreads();
+    if (tid < kScWaves * k) {
+        // an alternative's place: how many of each wave's are better
+        const int w = tid / k, j = tid % k;
+        const Key me = wk[w][j];
+        int place = 0;
+        if (me) {
+            for (int o = 0; o < kScWaves; ++o) {
+                int n = 0;
+                for (int b = 32; b; b >>= 1)
+                    if (n + b <= k && wk[o][n + b - 1] > me) n += b;
+                place += n;
+            }
+            if (place < k) out[place] = me;
+        }
+    }
+    __syncthreads();
+    if (wave) return;
+    x = wst[0];
+    for (int w = 1; w < kScWaves; ++w) x = join(x, wst[w], c);
+    const Key alt = lane < k ? out[lane] : 0;
+    if (a.parts == 1) scores_out<BF16>(a, r, x, alt, lane);
+    else {
+        const int64_t at = r * a.parts + part;
+        if (lane == 0) {
+            a.pst[at * 3] = x.m;
+            a.pst[at * 3 + 1] = x.s;
+            a.pst[at * 3 + 2] = x.w;
+        }
+        if (lane < k) a.pkey[at * k + lane] = alt;
+    }
+}
+
+// Joins a row's parts (at most 64).
+template <bool BF16>
+__global__ __launch_bounds__(kScThreads) void k_scores_join(ScoresCall a) {
+    __shared__ Key got[kWave * kScoresMaxK], out[kScoresMaxK];
+    __shared__ uint32_t least;
+    __shared__ int count;
+    const int tid = threadIdx.x, lane = tid % kWave, k = a.k;
+    const int64_t r = blockIdx.x;
+    const float c = a.scale * kLog2e;
+    const Key* keys = a.pkey + r * a.parts * k;
+    Stats x = {-__FLT_MAX__, 0.f, 0.f};
+    if (tid < kWave && lane < a.parts) {
+        const float* p = a.pst + (r * a.parts + lane) * 3;
+        x = {p[0], p[1], p[2]};
+    }
+    if (k) {
+        if (tid < kWave) {
+            // the k-th best of the parts' best ones bounds what can be among the row's k
+            const uint32_t o = reached_by(lane < a.parts ? (uint32_t)(keys[lane * k] >> 32) : 0, k);
+            if (lane == 0) least = o, count = 0;
+            if (lane < kScoresMaxK) out[lane] = 0;
+        }
+        __syncthreads();
+        for (int i = tid; i < a.parts * k; i += kScThreads) {
+            const Key me = keys[i];
+            if (me && (uint32_t)(me >> 32) >= least) got[atomicAdd(&count, 1)] = me;   // any order: they are ranked
+        }
+        __syncthreads();
+        const int n = count;
+        for (int i = tid; i < n; i += kScThreads) {
+            const Key me = got[i];
+            int place = 0;
+            for (int j = 0; j < n; ++j) place += got[j] > me;
+            if (place < k) out[place] = me;
+        }
+        __syncthreads();
+    }
+    if (tid >= kWave) return;
+    x = join_wave(x, c);
+    scores_out<BF16>(a, r, x, lane < k ? out[lane] : 0, lane);
+}
+
+namespace {
+
+constexpr int kScWorkgroups = 512;   // wanted of a launch
+constexpr int kScMaxParts = 64;      // one wave joins them
+
+// Parts that a row of V logits is split into in a call of `rows`.
+int parts_of(int64_t rows, int64_t V, int io_bf16, int64_t* per) {
+    const int64_t unit = (int64_t)kScThreads * (io_bf16 ? 8 : 4);   // logits of one load of a workgroup
+    int64_t n = kScWorkgroups / rows;
+    if (n > V / (unit * 2)) n = V / (unit * 2);
+    if (n > kScMaxParts) n = kScMaxParts;
+    if (n < 1) n = 1;
+    *per = ((V + n - 1) / n + unit - 1) / unit * unit;
+    return (int)((V + *per - 1) / *per);
+}
+
+}  // namespace
+
+size_t scores_ws_parts(int64_t rows, int64_t V, int io_bf16) {
+    int64_t most = 0, per;
+    for (int64_t r = 1; r <= rows && r <= kScWorkgroups; ++r) {
+        const int n = parts_of(r, V, io_bf16, &per);
+        if (n > 1 && r * n > most) most = r * n;
+    }
+    return (size_t)most;
+}
+
+hipError_t launch_scores(ScoresCall c, hipStream_t st) {
+    c.parts = parts_of(c.rows, c.V, c.io_bf16, &c.per);
+    const ScoresCall all = c;
+    constexpr int64_t kRows = (int64_t)1 << 23;   // of one launch, which has at most 2^32 threads
+    for (int64_t r = 0; r < all.rows; r += kRows) {
+        c.rows = all.rows - r < kRows ? all.rows - r : kRows;
+        c.logits = static_cast<const char*>(all.logits) + r * c.ld * (c.io_bf16 ? 2 : 4);
+        const auto from = [&](auto* p, int64_t n) { return p ? p + n : p; };
+        c.targets = from(all.targets, r);
+        c.logprob = from(all.logprob, r);
+        c.entropy = from(all.entropy, r);
+        c.lse = from(all.lse, r);
+        c.top = from(all.top, r * c.k);
+        c.top_id = from(all.top_id, r * c.k);
+        const unsigned grid = (unsigned)(c.rows * c.parts);   // more than one part only for few rows
+        if (c.io_bf16) k_scores<true><<<grid, kScThreads, 0, st>>>(c);
+        else k_scores<false><<<grid, kScThreads, 0, st>>>(c);
+        if (c.parts > 1) {
+            if (c.io_bf16) k_scores_join<true><<<(unsigned)c.rows, kScThreads, 0, st>>>(c);
+            else k_scores_join<false><<<(unsigned)c.rows, kScThreads, 0, st>>>(c);
+        }
+    }
     return hipGetLastError();
 }
 
