@@ -98,45 +98,30 @@ hipError_t launch_lattn_rec(const LattnCall& c, hipStream_t st) {
 }
 
 // ------------------------------------------------------------ chunked form
-// A workgroup of four waves takes a segment of positions of one (row, head)
-// and a slice of DVS columns of S, chunk by chunk.  With Q, K, V a chunk's
-// rows, E the state before it and i, j < C:
+// A workgroup takes a segment of positions of one (row, head) and a slice of
+// DVS columns of S, chunk by chunk; each of its waves has 16 of the columns.
+// With Q, K, V a chunk's rows, E the state before it and i, j < C:
 //     O = scale (diag(lam^{i+1}) Q E + P V),  P[i][j] = lam^{i-j} q_i . k_j, j <= i
 //     S = lam^C E + K^T diag(lam^{C-1-j}) V
 // A row's first chunk is filled from the back (zero rows in front), so that
 // every later one is whole and ends on the row's last position.
-constexpr int kLaThreads = 256;
 constexpr int la_chunk(bool bf16) { return bf16 ? 64 : 32; }   // positions of a chunk
+constexpr int la_threads(int dvs) { return dvs / 16 * kWave; }
 
-
-// 16 bytes of a head's row: elements c .. c + E - 1 below d, zero elsewhere
-template <bool BF16>
-__device__ __forceinline__ typename Mm<BF16>::Frag load_unit(const void* p, int64_t at, int c, int d, bool vec) {
-    using M = Mm<BF16>;
-    typename M::Frag u = {};
-    const typename M::T* q = static_cast<const typename M::T*>(p) + at + c;
-    if (vec) {
-        if (c < d) u = *gmem(reinterpret_cast<const typename M::Frag*>(q));
-    } else {
-#pragma unroll
-        for (int e = 0; e < M::E; ++e)
-            if (c + e < d) u[e] = gmem(q)[e];
-    }
-    return u;
-}
-
-template <bool BF16, int DK, int DVS, bool OUT>
-__global__ __launch_bounds__(kLaThreads, 2) void k_lattn_chunk(LattnCall a) {
+template <bool BF16, int DK, int DVS, bool OUT, bool VEC>
+__global__ __launch_bounds__(la_threads(DVS), 2) void k_lattn_chunk(LattnCall a) {
     using M = Mm<BF16>;
     using T = typename M::T;
     using Frag = typename M::Frag;
-    constexpr int C = la_chunk(BF16), KB = M::KB, E = M::E;
-    constexpr int PK = DK + E, PV = DVS + E, PP = C + E;   // LDS rows, 16 bytes longer
-    constexpr int NT = DVS / 64, KT = DK / 16, CT = C / 16;               // column tiles of a wave; tiles of dk; of C
-    constexpr int UK = C * DK / E / kLaThreads, UV = C * DVS / E / kLaThreads;   // 16-byte units per thread
+    using Four = T __attribute__((ext_vector_type(4)));
+    constexpr int C = la_chunk(BF16), KB = M::KB, E = M::E, NTH = la_threads(DVS), WAVES = NTH / kWave;
+    constexpr int PK = DK + E, PV = DVS + E, PP = C + E;         // LDS rows, 16 bytes longer
+    constexpr int KT = DK / 16, CT = C / 16;                     // tiles of dk and of C
+    constexpr int UK = C * DK / E / NTH, UV = C * DVS / E / NTH; // 16-byte units of a thread
     __shared__ __align__(16) T ks[C * PK], vs[C * PV], qs[OUT ? C * PK : 1], ps[OUT ? C * PP : 1];
 
-    const int tid = threadIdx.x, wave = tid / kWave, lane = tid % kWave, l16 = lane % 16, g = lane / 16;
+    const int tid = threadIdx.x, lane = tid % kWave, wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+    int l16 = lane % 16, g = lane / 16;
     const int slices = (a.dv + DVS - 1) / DVS, tasks = a.B * a.Hkv;
     // the slices of one segment read the same Q and K: eight workgroups apart, on one XCD and its L2
     const int unit = blockIdx.x / (8 * slices) * 8 + blockIdx.x % 8, slice = blockIdx.x / 8 % slices;
@@ -156,67 +141,80 @@ __global__ __launch_bounds__(kLaThreads, 2) void k_lattn_chunk(LattnCall a) {
     if (OUT) {   // o is zero past the row's end
         const int64_t z1 = seg == a.nseg - 1 ? a.L : (int64_t)(c0 + a.seg_chunks) * C < a.L ? (c0 + a.seg_chunks) * C : a.L;
         const int64_t z0 = len > c0 * C ? len : c0 * C;
-        for (int64_t i = z0 * a.G * DVS + tid; i < z1 * a.G * DVS; i += kLaThreads) {
+        for (int64_t i = z0 * a.G * DVS + tid; i < z1 * a.G * DVS; i += NTH) {
             const int col = col0 + i % DVS, h = n * a.G + i / DVS % a.G;
             if (col < dv) put_io<BF16>(a.o.p, b * a.o.row + i / DVS / a.G * a.o.pos + h * a.o.head + col, 0.f);
         }
         if (c0 >= chunks && !(seg == 0 && in)) return;
     }
 
+    // the lane's part of S: rows 16 kt + row0 + r of column scol
     const float ld = a.ld[n];
-    V4 S[KT][NT];
-    // thread's part of S: rows 16 kt + 4 g + r, columns col0 + 16 (wave NT + nt) + l16
+    V4 S[KT] = {};
     float* const sp = a.state && in ? a.state + (slot * a.Hkv + n) * dk * (int64_t)dv : nullptr;
     float* const wp = a.nseg > 1 ? a.ws + ((int64_t)task * a.nseg + seg) * dk * dv : nullptr;
     const float* const from = !OUT ? nullptr : wp ? wp : a.fresh ? nullptr : sp;
+    const bool full = dk == DK && col0 + DVS <= dv;   // no part of S lies outside
+    if (from) {
+        const int row0 = 4 * g, scol = col0 + 16 * wave + l16;
+        if (full) {
+            const float* p = from + row0 * dv + scol;
 #pragma unroll
-    for (int kt = 0; kt < KT; ++kt)
+            for (int i = 0; i < 4 * KT; ++i) S[i / 4][i % 4] = gmem(p)[(i / 4 * 16 + i % 4) * dv];
+        } else if (scol < dv) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int row = 16 * kt + 4 * g + r, col = col0 + 16 * (wave * NT + nt) + l16;
-                S[kt][nt][r] = from && row < dk && col < dv ? from[row * dv + col] : 0.f;
+            for (int i = 0; i < 4 * KT; ++i) {
+                const int row = row0 + i / 4 * 16 + i % 4;
+                if (row < dk) S[i / 4][i % 4] = gmem(from)[row * dv + scol];
             }
-
-    // decays: of a chunk's rows to its end (per operand element), from its
-    // start, and between positions of one tile and of tiles apart
-    const float em1 = expm1f(C * ld), lamKB = decay_pow(ld, KB), lam16 = decay_pow(ld, 16);
-    float to_end[E], near[4], apart[4];
-#pragma unroll
-    for (int e = 0; e < E; ++e) to_end[e] = decay_pow(ld, KB - 1 - (BF16 ? 8 * g + 2 * (e % 4) + e / 4 : 4 * g + e));
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-        const int j = BF16 ? 8 * (g / 2) + 2 * r + g % 2 : 4 * g + r;   // the key's place in its tile
-        near[r] = l16 >= j ? decay_pow(ld, l16 - j) : 0.f;
-        apart[r] = decay_pow(ld, 16 + l16 - j);
+        }
     }
-    const float from_start = decay_pow(ld, l16 + 1);
 
+    // lam^i, and lam^{C-1-i}: the decay of a chunk's rows to its end
+    __shared__ __align__(16) float lam[C + 1], to_end[C];
+    for (int i = tid; i <= C; i += NTH) {
+        lam[i] = decay_pow(ld, i);
+        if (i < C) to_end[i] = decay_pow(ld, C - 1 - i);
+    }
+    const auto uniform = [](float x) { return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(x))); };
+    const float em1 = uniform(expm1f(C * ld)), em1_first = uniform(expm1f((C - pad) * ld));   // lam^n - 1
+
+    // Staging: a thread has the same columns of rows RK (RV) apart.  Loads are
+    // of valid places always (columns past the head's end and zero rows in
+    // front repeat another one) and are blanked on their way to LDS.
+    constexpr int RK = NTH * E / DK, RV = NTH * E / DVS;
+    const int kcol = tid % (DK / E) * E, krow = tid / (DK / E), vcol = tid % (DVS / E) * E, vrow = tid / (DVS / E);
+    const bool kin = kcol < dk, vin = col0 + vcol < dv;
+    const int kleft = kin ? dk - kcol : 0, vleft = vin ? dv - col0 - vcol : 0;   // elements from there on
+    const int klcol = kin ? kcol : 0, vlcol = vin ? vcol : 0;
+    const T* const kp = static_cast<const T*>(a.k.p) + b * a.k.row + n * a.k.head;
+    const T* const vp = static_cast<const T*>(a.v.p) + b * a.v.row + n * a.v.head + col0;
+    const T* const qp = static_cast<const T*>(a.q.p) + b * a.q.row + (int64_t)n * a.G * a.q.head;
     Frag fk[UK], fv[UV], fq[UK];
-    const auto load_kv = [&](int c) {
-        const int t0 = c * C - pad;
+    // VEC: a chunk of rows spans less than 2^31 bytes, so that a place is a
+    // wave's own base and a lane's 32-bit offset
+    const auto fetch = [&](auto& f, const T* p, int64_t pos, int c, int row, int step, int col, int left) {
+        constexpr int count = sizeof(f) / sizeof(f[0]);
+        const int t0 = c * C - pad, base = t0 > 0 ? t0 : 0;
+        p += base * pos;
 #pragma unroll
-        for (int i = 0; i < UK; ++i) {
-            const int u = tid + i * kLaThreads, t = t0 + u / (DK / E), e = u % (DK / E) * E;
-            fk[i] = t >= 0 ? load_unit<BF16>(a.k.p, b * a.k.row + t * a.k.pos + n * a.k.head, e, dk, a.vec) : Frag{};
-        }
-#pragma unroll
-        for (int i = 0; i < UV; ++i) {
-            const int u = tid + i * kLaThreads, t = t0 + u / (DVS / E), e = u % (DVS / E) * E;
-            fv[i] = t >= 0 ? load_unit<BF16>(a.v.p, b * a.v.row + t * a.v.pos + n * a.v.head, col0 + e, dv, a.vec) : Frag{};
-        }
-    };
-    const auto load_q = [&](int c, int h) {
-        const int t0 = c * C - pad;
-#pragma unroll
-        for (int i = 0; i < UK; ++i) {
-            const int u = tid + i * kLaThreads, t = t0 + u / (DK / E), e = u % (DK / E) * E;
-            fq[i] = t >= 0 ? load_unit<BF16>(a.q.p, b * a.q.row + t * a.q.pos + (n * a.G + h) * a.q.head, e, dk, a.vec) : Frag{};
+        for (int i = 0; i < count; ++i) {
+            const int t = t0 + row + i * step, r = (t > 0 ? t : 0) - base;   // (a zero row in front: the row's first position)
+            if constexpr (VEC) {
+                const uint32_t off = (uint32_t)(r * (int)pos + col) * sizeof(T);
+                f[i] = *gmem(reinterpret_cast<const Frag*>(reinterpret_cast<const char*>(p) + off));
+            } else f[i] = load_loose<BF16>(p + r * pos + col, 0, left);
         }
     };
-    const auto put = [&](T* to, int pitch, int per_row, int u, Frag f) {
-        *smem_ptr(reinterpret_cast<Frag*>(to + u / per_row * pitch + u % per_row * E)) = f;
+    const auto put = [&](T* to, int pitch, const auto& f, int row, int step, int col, bool in, int first) {
+        constexpr int count = sizeof(f) / sizeof(f[0]);
+        T* p = to + row * pitch + col;
+#pragma unroll
+        for (int i = 0; i < count; ++i) {
+            Frag x = f[i];
+            if (!in || row + i * step < first) x = Frag{};
+            *smem_ptr(reinterpret_cast<Frag*>(p + i * step * pitch)) = x;
+        }
     };
     // 16 columns from col, as an operand over the KB positions from row t0
     const auto transposed = [&](const T* from, int pitch, int t0, int col) {
@@ -236,70 +234,74 @@ __global__ __launch_bounds__(kLaThreads, 2) void k_lattn_chunk(LattnCall a) {
             }
         } else {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) f[e] = from[(t0 + 4 * g + e) * pitch + col + l16];
+            for (int e = 0; e < 4; ++e) f[e] = smem_ptr(from)[(t0 + 4 * g + e) * pitch + col + l16];
         }
         return f;
     };
     const auto row_frag = [&](const T* p) { return *smem_ptr(reinterpret_cast<const Frag*>(p)); };
 
     if (c0 < c1) {
-        load_kv(c0);
-        if (OUT) load_q(c0, 0);
+        fetch(fk, kp, a.k.pos, c0, krow, RK, klcol, kleft);
+        fetch(fv, vp, a.v.pos, c0, vrow, RV, vlcol, vleft);
+        if constexpr (OUT) fetch(fq, qp, a.q.pos, c0, krow, RK, klcol, kleft);
     }
     for (int c = c0; c < c1; ++c) {
         const int first = c == 0 ? pad : 0;   // zero rows in front
-#pragma unroll
-        for (int i = 0; i < UK; ++i) put(ks, PK, DK / E, tid + i * kLaThreads, fk[i]);
-#pragma unroll
-        for (int i = 0; i < UV; ++i) put(vs, PV, DVS / E, tid + i * kLaThreads, fv[i]);
+        // the lane's place anew in every chunk: addresses that depend on it
+        // are not all kept in registers around the loop
+        asm volatile("" : "+v"(l16), "+v"(g));
+        put(ks, PK, fk, krow, RK, kcol, kin, first);
+        put(vs, PV, fv, vrow, RV, vcol, vin, first);
+        if constexpr (OUT) put(qs, PK, fq, krow, RK, kcol, kin, first);
+        __syncthreads();
+        // the next chunk's rows (the last one's again at the end: no branch,
+        // so that nothing waits for them before their use)
+        const int ahead = c + 1 < c1 ? c + 1 : c;
+        fetch(fk, kp, a.k.pos, ahead, krow, RK, klcol, kleft);
+        fetch(fv, vp, a.v.pos, ahead, vrow, RV, vlcol, vleft);
         if constexpr (OUT) {
             for (int h = 0; h < a.G; ++h) {
+                const bool last = h + 1 == a.G;
+                fetch(fq, qp + (last ? 0 : h + 1) * a.q.head, a.q.pos, last ? ahead : c, krow, RK, klcol, kleft);
+                // P^T, tiles of 16 keys x 16 queries, jt <= it, shared out among the waves
 #pragma unroll
-                for (int i = 0; i < UK; ++i) put(qs, PK, DK / E, tid + i * kLaThreads, fq[i]);
-                __syncthreads();
-                if (h == 0 && c + 1 < c1) load_kv(c + 1);
-                if (h + 1 < a.G) load_q(c, h + 1);
-                else if (c + 1 < c1) load_q(c + 1, 0);
-                // P^T of the wave's queries: tile jt of keys x its 16 queries
-                if (wave < CT) {
-                    Frag fq16[DK / KB];
+                for (int at = 0; at < CT * (CT + 1) / 2; at += WAVES) {
+                    const int tile = at + wave;
+                    if (tile >= CT * (CT + 1) / 2) break;
+                    const int it = tile < 1 ? 0 : tile < 3 ? 1 : tile < 6 ? 2 : 3, jt = tile - it * (it + 1) / 2;
+                    const int krow_ = BF16 ? 8 * (l16 / 8) + 2 * (l16 % 4) + l16 / 4 % 2 : l16;
+                    V4 p = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                    for (int kb = 0; kb < DK / KB; ++kb) fq16[kb] = row_frag(qs + (16 * wave + l16) * PK + kb * KB + g * E);
-                    const int krow = BF16 ? 8 * (l16 / 8) + 2 * (l16 % 4) + l16 / 4 % 2 : l16;
-                    float far = 1.f;
-                    for (int jt = wave; jt >= 0; --jt) {
-                        V4 p = {0.f, 0.f, 0.f, 0.f};
+                    for (int kb = 0; kb < DK / KB; ++kb)
+                        p = M::mma(row_frag(ks + (16 * jt + krow_) * PK + kb * KB + g * E),
+                                   row_frag(qs + (16 * it + l16) * PK + kb * KB + g * E), p);
+                    T* to = ps + (16 * it + l16) * PP + 16 * jt + 4 * g;
+                    const auto key = [&](int r) { return BF16 ? 8 * (g / 2) + 2 * r + g % 2 : 4 * g + r; };   // its place in its tile
+                    if (it == jt) {
 #pragma unroll
-                        for (int kb = 0; kb < DK / KB; ++kb)
-                            p = M::mma(row_frag(ks + (16 * jt + krow) * PK + kb * KB + g * E), fq16[kb], p);
-                        if (jt == wave) {
-#pragma unroll
-                            for (int r = 0; r < 4; ++r) p[r] = near[r] == 0.f ? 0.f : p[r] * near[r];
-                        } else {
-#pragma unroll
-                            for (int r = 0; r < 4; ++r) p[r] *= apart[r] * far;
-                            far *= lam16;
+                        for (int r = 0; r < 4; ++r) {
+                            const int i = l16 - key(r);
+                            p[r] = i >= 0 ? p[r] * lam[i >= 0 ? i : 0] : 0.f;
                         }
-                        T* to = ps + (16 * wave + l16) * PP + 16 * jt + 4 * g;
-                        if constexpr (BF16) {
-                            BF4 y;
+                        // the rest of the block of keys that the product below takes whole
+                        if (BF16 && it % 2 == 0) *smem_ptr(reinterpret_cast<Four*>(to + 16)) = Four{};
+                    } else {
 #pragma unroll
-                            for (int r = 0; r < 4; ++r) y[r] = (BF)p[r];
-                            *smem_ptr(reinterpret_cast<BF4*>(to)) = y;
-                        } else *smem_ptr(reinterpret_cast<V4*>(to)) = p;
+                        for (int r = 0; r < 4; ++r) p[r] *= lam[16 * (it - jt) + l16 - key(r)];
                     }
-                    // the rest of the key block that the product below takes whole
-                    if (BF16 && wave % 2 == 0) *smem_ptr(reinterpret_cast<BF4*>(ps + (16 * wave + l16) * PP + 16 * (wave + 1) + 4 * g)) = BF4{};
+                    Four y;
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) y[r] = (T)p[r];
+                    *smem_ptr(reinterpret_cast<Four*>(to)) = y;
                 }
+                __builtin_amdgcn_sched_barrier(0);
                 // O^T = E^T Q^T: columns are positions
-                V4 O[NT][CT] = {};
+                V4 O[CT] = {};
 #pragma unroll
                 for (int kb = 0; kb < DK / KB; ++kb) {
-                    Frag fs[NT];
+                    Frag fs;
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int e = 0; e < E; ++e) fs[nt][e] = (T)S[kb * (KB / 16) + e / 4][nt][e % 4];
+                    for (int e = 0; e < E; ++e) fs[e] = (T)S[kb * (KB / 16) + e / 4][e % 4];
 #pragma unroll
                     for (int it = 0; it < CT; ++it) {
                         const T* p = qs + (16 * it + l16) * PK + kb * KB + 4 * g;
@@ -308,125 +310,112 @@ __global__ __launch_bounds__(kLaThreads, 2) void k_lattn_chunk(LattnCall a) {
                             const BF4 lo = *smem_ptr(reinterpret_cast<const BF4*>(p)), hi = *smem_ptr(reinterpret_cast<const BF4*>(p + 16));
                             f = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
                         } else f = row_frag(p);
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) O[nt][it] = M::mma(fs[nt], f, O[nt][it]);
+                        O[it] = M::mma(fs, f, O[it]);
                     }
                 }
-                float w = first ? 1.f : from_start;
+                // lam^{i + 1}, counted from the row's first position in a first chunk
 #pragma unroll
                 for (int it = 0; it < CT; ++it) {
-                    // lam^{i + 1}, counted from the row's first position in a first chunk
                     const int i = 16 * it + l16 + 1 - first;
-                    const float f = first ? decay_pow(ld, i > 0 ? i : 0) : w;
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) O[nt][it] *= f;
-                    w *= lam16;
+                    O[it] *= lam[i > 0 ? i : 0];
                 }
                 __syncthreads();
 #pragma unroll
                 for (int kb = 0; kb < C / KB; ++kb) {
-                    Frag v[NT];
+                    const Frag v = transposed(vs, PV, kb * KB, 16 * wave);
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) v[nt] = transposed(vs, PV, kb * KB, 16 * (wave * NT + nt));
-#pragma unroll
-                    for (int it = 0; it < CT; ++it) {
-                        if (16 * it + 15 < kb * KB) continue;   // keys after every query
-                        const Frag p = row_frag(ps + (16 * it + l16) * PP + kb * KB + g * E);
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) O[nt][it] = M::mma(v[nt], p, O[nt][it]);
-                    }
+                    for (int it = kb * KB / 16; it < CT; ++it)   // queries before every key of the block: nothing
+                        O[it] = M::mma(v, row_frag(ps + (16 * it + l16) * PP + kb * KB + g * E), O[it]);
                 }
-                const int64_t ob = b * a.o.row + (n * a.G + h) * a.o.head;
+                __builtin_amdgcn_sched_barrier(0);
+                T* const op = static_cast<T*>(a.o.p) + b * a.o.row + (n * a.G + h) * a.o.head + (int64_t)(c * C - pad) * a.o.pos + col0 + 16 * wave;
+                const int left = dv - (col0 + 16 * wave + 4 * g);
 #pragma unroll
                 for (int it = 0; it < CT; ++it) {
-                    const int t = c * C - pad + 16 * it + l16;
-                    if (t < 0) continue;
+                    Four y;
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        const int col = col0 + 16 * (wave * NT + nt) + 4 * g;
-                        if (col >= dv) continue;
-                        T* to = static_cast<T*>(a.o.p) + ob + t * a.o.pos + col;
-                        using Four = T __attribute__((ext_vector_type(4)));
-                        Four y;
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) y[r] = (T)(a.scale * O[nt][it][r]);
-                        if (a.vec) *gmem(reinterpret_cast<Four*>(to)) = y;
-                        else
+                    for (int r = 0; r < 4; ++r) y[r] = (T)(a.scale * O[it][r]);
+                    if (16 * it + l16 >= first) {
+                        if constexpr (VEC) {
+                            const uint32_t off = (uint32_t)(l16 * (int)a.o.pos + 4 * g) * sizeof(T);
+                            if (left > 0) *gmem(reinterpret_cast<Four*>(reinterpret_cast<char*>(op + 16 * it * a.o.pos) + off)) = y;
+                        } else {
+                            T* to = op + (16 * it + l16) * a.o.pos + 4 * g;
 #pragma unroll
                             for (int r = 0; r < 4; ++r)
-                                if (col + r < dv) gmem(to)[r] = y[r];
+                                if (r < left) gmem(to)[r] = y[r];
+                        }
                     }
                 }
-                if (h + 1 < a.G) __syncthreads();
+                __builtin_amdgcn_sched_barrier(0);
+                if (!last) {
+                    __syncthreads();
+                    put(qs, PK, fq, krow, RK, kcol, kin, first);
+                    __syncthreads();
+                }
             }
-        } else {
-            __syncthreads();
-            if (c + 1 < c1) load_kv(c + 1);
         }
         // S: its decay as S + (lam^C - 1) S (lam^C's rounding would add up
         // over the chunks of a long memory), then the chunk's own products
-        const float d = first ? expm1f((C - first) * ld) : em1;
+        const float d = c == 0 ? em1_first : em1;
 #pragma unroll
         for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int r = 0; r < 4; ++r) S[kt][r] = fmaf(d, S[kt][r], S[kt][r]);
 #pragma unroll
-                for (int r = 0; r < 4; ++r) S[kt][nt][r] = fmaf(d, S[kt][nt][r], S[kt][nt][r]);
-        float far = 1.f;
+        for (int kb = 0; kb < C / KB; ++kb) {
+            __builtin_amdgcn_sched_barrier(0);
+            const Frag v = transposed(vs, PV, kb * KB, 16 * wave);
+            float w[E];   // of the operand's positions
 #pragma unroll
-        for (int kb = C / KB - 1; kb >= 0; --kb) {
+            for (int e = 0; e < E; e += 4) {
+                const V4 x = *smem_ptr(reinterpret_cast<const V4*>(to_end + kb * KB + E * g + e));
+#pragma unroll
+                for (int i = 0; i < 4; ++i) w[BF16 ? (e + i) / 2 + (i % 2) * 4 : i] = x[i];
+            }
             if constexpr (BF16) {
                 // V's decayed rows as a sum of three bf16 parts (24 bits): the state keeps fp32's precision
-                Frag hi[NT], mid[NT], lo[NT];
+                Frag hi, mid, lo;
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    const Frag v = transposed(vs, PV, kb * KB, 16 * (wave * NT + nt));
-#pragma unroll
-                    for (int e = 0; e < E; ++e) {
-                        const float x = (float)v[e] * (to_end[e] * far);
-                        hi[nt][e] = (BF)x;
-                        const float y = x - (float)hi[nt][e];
-                        mid[nt][e] = (BF)y;
-                        lo[nt][e] = (BF)(y - (float)mid[nt][e]);
-                    }
+                for (int e = 0; e < E; ++e) {
+                    const float x = (float)v[e] * w[e];
+                    hi[e] = (BF)x;
+                    const float y = x - (float)hi[e];
+                    mid[e] = (BF)y;
+                    lo[e] = (BF)(y - (float)mid[e]);
                 }
 #pragma unroll
                 for (int kt = 0; kt < KT; ++kt) {
                     const Frag k = transposed(ks, PK, kb * KB, 16 * kt);
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-                        S[kt][nt] = M::mma(k, hi[nt], M::mma(k, mid[nt], M::mma(k, lo[nt], S[kt][nt])));
+                    S[kt] = M::mma(k, hi, M::mma(k, mid, M::mma(k, lo, S[kt])));
+                    if (kt % 4 == 3) __builtin_amdgcn_sched_barrier(0);
                 }
             } else {
-                Frag v[NT];
+                Frag x;
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    v[nt] = transposed(vs, PV, kb * KB, 16 * (wave * NT + nt));
+                for (int e = 0; e < E; ++e) x[e] = v[e] * w[e];
 #pragma unroll
-                    for (int e = 0; e < E; ++e) v[nt][e] *= to_end[e] * far;
-                }
-#pragma unroll
-                for (int kt = 0; kt < KT; ++kt) {
-                    const Frag k = transposed(ks, PK, kb * KB, 16 * kt);
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) S[kt][nt] = M::mma(k, v[nt], S[kt][nt]);
-                }
+                for (int kt = 0; kt < KT; ++kt) S[kt] = M::mma(transposed(ks, PK, kb * KB, 16 * kt), x, S[kt]);
             }
-            far *= lamKB;
         }
         __syncthreads();
     }
     float* to = OUT ? (c1 == chunks ? sp : nullptr) : wp + (int64_t)dk * dv;
-    if (to)
+    if (!to) return;
+    // the lane's place anew: nothing of the loads above is kept through the loop
+    int row0 = 4 * g, scol = col0 + 16 * wave + l16;
+    asm volatile("" : "+v"(row0), "+v"(scol));
+    if (full) {
+        to += row0 * dv + scol;
 #pragma unroll
-        for (int kt = 0; kt < KT; ++kt)
+        for (int i = 0; i < 4 * KT; ++i) gmem(to)[(i / 4 * 16 + i % 4) * dv] = S[i / 4][i % 4];
+    } else if (scol < dv) {
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int row = 16 * kt + 4 * g + r, col = col0 + 16 * (wave * NT + nt) + l16;
-                    if (row < dk && col < dv) to[row * dv + col] = S[kt][nt][r];
-                }
+        for (int i = 0; i < 4 * KT; ++i) {
+            const int row = row0 + i / 4 * 16 + i % 4;
+            if (row < dk) gmem(to)[row * dv + scol] = S[i / 4][i % 4];
+        }
+    }
 }
 
 // Entry states of a split row's segments, in place: ws[s + 1] holds the
@@ -460,7 +449,7 @@ namespace {
 constexpr int kLaWorkgroups = 512;   // wanted of a launch: two for each CU
 constexpr int kLaMinChunks = 8;      // of a segment
 
-int slice_cols(int dk) { return dk > 64 && dk <= 128 ? 128 : 64; }
+int slice_cols(int dk) { return dk <= 64 ? 64 : 128; }
 
 // segments that a call of `tasks` rows and heads is split into
 int segments(int64_t tasks, int slices, int chunks, int* seg_chunks) {
@@ -471,25 +460,25 @@ int segments(int64_t tasks, int slices, int chunks, int* seg_chunks) {
     return chunks ? (chunks + *seg_chunks - 1) / *seg_chunks : 1;
 }
 
-template <bool BF16, int DK, int DVS>
+template <bool BF16, int DK, int DVS, bool VEC>
 void chunk_launches(const LattnCall& c, hipStream_t st) {
     const int slices = (c.dv + DVS - 1) / DVS;
     const int64_t units = c.B * c.Hkv * c.nseg;
     const unsigned grid = (unsigned)((units + 7) / 8 * 8 * slices);
     if (c.nseg > 1) {
-        k_lattn_chunk<BF16, DK, DVS, false><<<grid, kLaThreads, 0, st>>>(c);
+        k_lattn_chunk<BF16, DK, DVS, false, VEC><<<grid, la_threads(DVS), 0, st>>>(c);
         k_lattn_scan<BF16><<<(unsigned)(c.B * c.Hkv * ((c.dk * c.dv + 255) / 256)), 256, 0, st>>>(c);
     }
-    k_lattn_chunk<BF16, DK, DVS, true><<<grid, kLaThreads, 0, st>>>(c);
+    k_lattn_chunk<BF16, DK, DVS, true, VEC><<<grid, la_threads(DVS), 0, st>>>(c);
 }
 
 template <bool BF16>
 hipError_t chunk_dims(LattnCall& c, hipStream_t st) {
     const int cols = slice_cols(c.dk);
     c.nseg = segments(c.B * c.Hkv, (c.dv + cols - 1) / cols, (c.L + la_chunk(BF16) - 1) / la_chunk(BF16), &c.seg_chunks);
-    if (c.dk <= 64) chunk_launches<BF16, 64, 64>(c, st);
-    else if (c.dk <= 128) chunk_launches<BF16, 128, 128>(c, st);
-    else chunk_launches<BF16, 256, 64>(c, st);
+    if (c.dk <= 64) c.vec ? chunk_launches<BF16, 64, 64, true>(c, st) : chunk_launches<BF16, 64, 64, false>(c, st);
+    else if (c.dk <= 128) c.vec ? chunk_launches<BF16, 128, 128, true>(c, st) : chunk_launches<BF16, 128, 128, false>(c, st);
+    else c.vec ? chunk_launches<BF16, 256, 128, true>(c, st) : chunk_launches<BF16, 256, 128, false>(c, st);
     return hipGetLastError();
 }
 

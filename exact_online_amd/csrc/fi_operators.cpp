@@ -114,10 +114,11 @@ void fi_lattn_destroy(fi_lattn *s) {
 
 namespace {
 
-// a view's whole heads load in 16-byte units
+// a view's whole heads load in 16-byte units, and the rows of a chunk (at most
+// 64) span less than 2^31 bytes
 bool view_vec(const fi_view &v, int64_t d, int es) {
     const int64_t u = 16 / es;
-    return aligned(v.p, 16) && v.row % u == 0 && v.pos % u == 0 && v.head % u == 0 && d % u == 0;
+    return v.pos >= 0 && v.pos < ((int64_t)1 << 22) && aligned(v.p, 16) && v.row % u == 0 && v.pos % u == 0 && v.head % u == 0 && d % u == 0;
 }
 
 int lattn_call(const fi_lattn *s, const fi_lattn_args *a, LattnCall &c) {
