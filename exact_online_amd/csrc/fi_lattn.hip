@@ -109,7 +109,7 @@ constexpr int la_chunk(bool bf16) { return bf16 ? 64 : 32; }   // positions of a
 constexpr int la_threads(int dvs) { return dvs / 16 * kWave; }
 
 template <bool BF16, int DK, int DVS, bool OUT, bool VEC>
-__global__ __launch_bounds__(la_threads(DVS), 2) void k_lattn_chunk(LattnCall a) {
+__global__ __launch_bounds__(la_threads(DVS), DK == 256 ? 2 : 4) void k_lattn_chunk(LattnCall a) {
     using M = Mm<BF16>;
     using T = typename M::T;
     using Frag = typename M::Frag;
@@ -195,26 +195,32 @@ __global__ __launch_bounds__(la_threads(DVS), 2) void k_lattn_chunk(LattnCall a)
     // wave's own base and a lane's 32-bit offset
     const auto fetch = [&](auto& f, const T* p, int64_t pos, int c, int row, int step, int col, int left) {
         constexpr int count = sizeof(f) / sizeof(f[0]);
-        const int t0 = c * C - pad, base = t0 > 0 ? t0 : 0;
-        p += base * pos;
+        const int t0 = c * C - pad;
+        int r[count];
+#pragma unroll
+        for (int i = 0; i < count; ++i) r[i] = row + i * step;
+        if (t0 < 0) {   // (a zero row in front: the row's first position)
+#pragma unroll
+            for (int i = 0; i < count; ++i) r[i] = t0 + r[i] > 0 ? t0 + r[i] : 0;
+        } else p += t0 * pos;
 #pragma unroll
         for (int i = 0; i < count; ++i) {
-            const int t = t0 + row + i * step, r = (t > 0 ? t : 0) - base;   // (a zero row in front: the row's first position)
             if constexpr (VEC) {
-                const uint32_t off = (uint32_t)(r * (int)pos + col) * sizeof(T);
+                const uint32_t off = (uint32_t)(r[i] * (int)pos + col) * sizeof(T);
                 f[i] = *gmem(reinterpret_cast<const Frag*>(reinterpret_cast<const char*>(p) + off));
-            } else f[i] = load_loose<BF16>(p + r * pos + col, 0, left);
+            } else f[i] = load_loose<BF16>(p + r[i] * pos + col, 0, left);
         }
     };
-    const auto put = [&](T* to, int pitch, const auto& f, int row, int step, int col, bool in, int first) {
+    const auto put = [&](T* to, int pitch, auto& f, int row, int step, int col, bool in, bool blank, int first) {
         constexpr int count = sizeof(f) / sizeof(f[0]);
         T* p = to + row * pitch + col;
+        if (blank) {
 #pragma unroll
-        for (int i = 0; i < count; ++i) {
-            Frag x = f[i];
-            if (!in || row + i * step < first) x = Frag{};
-            *smem_ptr(reinterpret_cast<Frag*>(p + i * step * pitch)) = x;
+            for (int i = 0; i < count; ++i)
+                if (!in || row + i * step < first) f[i] = Frag{};
         }
+#pragma unroll
+        for (int i = 0; i < count; ++i) *smem_ptr(reinterpret_cast<Frag*>(p + i * step * pitch)) = f[i];
     };
     // 16 columns from col, as an operand over the KB positions from row t0
     const auto transposed = [&](const T* from, int pitch, int t0, int col) {
@@ -247,12 +253,13 @@ __global__ __launch_bounds__(la_threads(DVS), 2) void k_lattn_chunk(LattnCall a)
     }
     for (int c = c0; c < c1; ++c) {
         const int first = c == 0 ? pad : 0;   // zero rows in front
+        const bool blank = first || !full;
         // the lane's place anew in every chunk: addresses that depend on it
         // are not all kept in registers around the loop
         asm volatile("" : "+v"(l16), "+v"(g));
-        put(ks, PK, fk, krow, RK, kcol, kin, first);
-        put(vs, PV, fv, vrow, RV, vcol, vin, first);
-        if constexpr (OUT) put(qs, PK, fq, krow, RK, kcol, kin, first);
+        put(ks, PK, fk, krow, RK, kcol, kin, blank, first);
+        put(vs, PV, fv, vrow, RV, vcol, vin, blank, first);
+        if constexpr (OUT) put(qs, PK, fq, krow, RK, kcol, kin, blank, first);
         __syncthreads();
         // the next chunk's rows (the last one's again at the end: no branch,
         // so that nothing waits for them before their use)
@@ -262,6 +269,7 @@ __global__ __launch_bounds__(la_threads(DVS), 2) void k_lattn_chunk(LattnCall a)
         if constexpr (OUT) {
             for (int h = 0; h < a.G; ++h) {
                 const bool last = h + 1 == a.G;
+                asm volatile("" : "+v"(l16), "+v"(g));
                 fetch(fq, qp + (last ? 0 : h + 1) * a.q.head, a.q.pos, last ? ahead : c, krow, RK, klcol, kleft);
                 // P^T, tiles of 16 keys x 16 queries, jt <= it, shared out among the waves
 #pragma unroll
@@ -312,6 +320,7 @@ __global__ __launch_bounds__(la_threads(DVS), 2) void k_lattn_chunk(LattnCall a)
                         } else f = row_frag(p);
                         O[it] = M::mma(fs, f, O[it]);
                     }
+                    __builtin_amdgcn_sched_barrier(0);
                 }
                 // lam^{i + 1}, counted from the row's first position in a first chunk
 #pragma unroll
@@ -350,7 +359,7 @@ __global__ __launch_bounds__(la_threads(DVS), 2) void k_lattn_chunk(LattnCall a)
                 __builtin_amdgcn_sched_barrier(0);
                 if (!last) {
                     __syncthreads();
-                    put(qs, PK, fq, krow, RK, kcol, kin, first);
+                    put(qs, PK, fq, krow, RK, kcol, kin, blank, first);
                     __syncthreads();
                 }
             }
