@@ -121,7 +121,7 @@ __global__ __launch_bounds__(la_threads(DVS), DK == 256 ? 2 : 4) void k_lattn_ch
     __shared__ __align__(16) T ks[C * PK], vs[C * PV], qs[OUT ? C * PK : 1], ps[OUT ? C * PP : 1];
 
     const int tid = threadIdx.x, lane = tid % kWave, wave = __builtin_amdgcn_readfirstlane(tid / kWave);
-    int l16 = lane % 16, g = lane / 16;
+    uint32_t l16 = (uint32_t)lane % 16, g = (uint32_t)lane / 16;
     const int slices = (a.dv + DVS - 1) / DVS, tasks = a.B * a.Hkv;
     // the slices of one segment read the same Q and K: eight workgroups apart, on one XCD and its L2
     const int unit = blockIdx.x / (8 * slices) * 8 + blockIdx.x % 8, slice = blockIdx.x / 8 % slices;
@@ -156,7 +156,7 @@ __global__ __launch_bounds__(la_threads(DVS), DK == 256 ? 2 : 4) void k_lattn_ch
     const float* const from = !OUT ? nullptr : wp ? wp : a.fresh ? nullptr : sp;
     const bool full = dk == DK && col0 + DVS <= dv;   // no part of S lies outside
     if (from) {
-        const int row0 = 4 * g, scol = col0 + 16 * wave + l16;
+        const int row0 = 4 * g, scol = col0 + 16 * wave + (int)l16;
         if (full) {
             const float* p = from + row0 * dv + scol;
 #pragma unroll
@@ -222,6 +222,21 @@ __global__ __launch_bounds__(la_threads(DVS), DK == 256 ? 2 : 4) void k_lattn_ch
 #pragma unroll
         for (int i = 0; i < count; ++i) *smem_ptr(reinterpret_cast<Frag*>(p + i * step * pitch)) = f[i];
     };
+    // Q's rows, for whole 16-byte operand reads beside S's (whose lanes hold
+    // rows 4 g .. 4 g + 3 of two tiles): each block of KB columns is stored in
+    // the order 4 (g, tile) + r
+    const auto put_q = [&](bool blank, int first) {
+        if constexpr (!BF16) put(qs, PK, fq, krow, RK, kcol, kin, blank, first);
+        else {
+#pragma unroll
+            for (int i = 0; i < UK; ++i) {
+                if (blank && (!kin || krow + i * RK < first)) fq[i] = Frag{};
+                T* p = qs + (krow + i * RK) * PK + kcol / KB * KB + kcol % 16 * 2 + kcol % KB / 16 * 4;
+                *smem_ptr(reinterpret_cast<BF4*>(p)) = __builtin_shufflevector(fq[i], fq[i], 0, 1, 2, 3);
+                *smem_ptr(reinterpret_cast<BF4*>(p + 8)) = __builtin_shufflevector(fq[i], fq[i], 4, 5, 6, 7);
+            }
+        }
+    };
     // 16 columns from col, as an operand over the KB positions from row t0
     const auto transposed = [&](const T* from, int pitch, int t0, int col) {
         Frag f;
@@ -244,6 +259,13 @@ __global__ __launch_bounds__(la_threads(DVS), DK == 256 ? 2 : 4) void k_lattn_ch
         }
         return f;
     };
+    // the operand in the order of Q's columns, from a row in its own
+    const auto pair_frag = [&](const T* p) -> Frag {
+        if constexpr (BF16) {
+            const BF4 a = *smem_ptr(reinterpret_cast<const BF4*>(p)), b = *smem_ptr(reinterpret_cast<const BF4*>(p + 16));
+            return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+        } else return *smem_ptr(reinterpret_cast<const Frag*>(p));
+    };
     const auto row_frag = [&](const T* p) { return *smem_ptr(reinterpret_cast<const Frag*>(p)); };
 
     if (c0 < c1) {
@@ -259,43 +281,42 @@ __global__ __launch_bounds__(la_threads(DVS), DK == 256 ? 2 : 4) void k_lattn_ch
         asm volatile("" : "+v"(l16), "+v"(g));
         put(ks, PK, fk, krow, RK, kcol, kin, blank, first);
         put(vs, PV, fv, vrow, RV, vcol, vin, blank, first);
-        if constexpr (OUT) put(qs, PK, fq, krow, RK, kcol, kin, blank, first);
+        if constexpr (OUT) put_q(blank, first);
         __syncthreads();
         // the next chunk's rows (the last one's again at the end: no branch,
         // so that nothing waits for them before their use)
         const int ahead = c + 1 < c1 ? c + 1 : c;
         fetch(fk, kp, a.k.pos, ahead, krow, RK, klcol, kleft);
-        fetch(fv, vp, a.v.pos, ahead, vrow, RV, vlcol, vleft);
+        if constexpr (!OUT) fetch(fv, vp, a.v.pos, ahead, vrow, RV, vlcol, vleft);
         if constexpr (OUT) {
             for (int h = 0; h < a.G; ++h) {
                 const bool last = h + 1 == a.G;
                 asm volatile("" : "+v"(l16), "+v"(g));
-                fetch(fq, qp + (last ? 0 : h + 1) * a.q.head, a.q.pos, last ? ahead : c, krow, RK, klcol, kleft);
                 // P^T, tiles of 16 keys x 16 queries, jt <= it, shared out among the waves
 #pragma unroll
                 for (int at = 0; at < CT * (CT + 1) / 2; at += WAVES) {
                     const int tile = at + wave;
                     if (tile >= CT * (CT + 1) / 2) break;
                     const int it = tile < 1 ? 0 : tile < 3 ? 1 : tile < 6 ? 2 : 3, jt = tile - it * (it + 1) / 2;
-                    const int krow_ = BF16 ? 8 * (l16 / 8) + 2 * (l16 % 4) + l16 / 4 % 2 : l16;
+                    const uint32_t krow_ = BF16 ? 8 * (l16 / 8) + 2 * (l16 % 4) + l16 / 4 % 2 : l16;
                     V4 p = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                     for (int kb = 0; kb < DK / KB; ++kb)
-                        p = M::mma(row_frag(ks + (16 * jt + krow_) * PK + kb * KB + g * E),
+                        p = M::mma(pair_frag(ks + (16 * jt + krow_) * PK + kb * KB + 4 * g),
                                    row_frag(qs + (16 * it + l16) * PK + kb * KB + g * E), p);
                     T* to = ps + (16 * it + l16) * PP + 16 * jt + 4 * g;
-                    const auto key = [&](int r) { return BF16 ? 8 * (g / 2) + 2 * r + g % 2 : 4 * g + r; };   // its place in its tile
+                    const auto key = [&](int r) { return (int)(BF16 ? 8 * (g / 2) + 2 * r + g % 2 : 4 * g + r); };   // its place in its tile
                     if (it == jt) {
 #pragma unroll
                         for (int r = 0; r < 4; ++r) {
-                            const int i = l16 - key(r);
-                            p[r] = i >= 0 ? p[r] * lam[i >= 0 ? i : 0] : 0.f;
+                            const int i = (int)l16 - key(r);
+                            p[r] = (i >= 0 ? p[r] : 0.f) * lam[i >= 0 ? i : 0];
                         }
                         // the rest of the block of keys that the product below takes whole
                         if (BF16 && it % 2 == 0) *smem_ptr(reinterpret_cast<Four*>(to + 16)) = Four{};
                     } else {
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) p[r] *= lam[16 * (it - jt) + l16 - key(r)];
+                        for (int r = 0; r < 4; ++r) p[r] *= lam[16 * (it - jt) + (int)l16 - key(r)];
                     }
                     Four y;
 #pragma unroll
@@ -312,20 +333,16 @@ __global__ __launch_bounds__(la_threads(DVS), DK == 256 ? 2 : 4) void k_lattn_ch
                     for (int e = 0; e < E; ++e) fs[e] = (T)S[kb * (KB / 16) + e / 4][e % 4];
 #pragma unroll
                     for (int it = 0; it < CT; ++it) {
-                        const T* p = qs + (16 * it + l16) * PK + kb * KB + 4 * g;
-                        Frag f;
-                        if constexpr (BF16) {
-                            const BF4 lo = *smem_ptr(reinterpret_cast<const BF4*>(p)), hi = *smem_ptr(reinterpret_cast<const BF4*>(p + 16));
-                            f = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-                        } else f = row_frag(p);
-                        O[it] = M::mma(fs, f, O[it]);
+                        O[it] = M::mma(fs, row_frag(qs + (16 * it + l16) * PK + kb * KB + g * E), O[it]);
                     }
                     __builtin_amdgcn_sched_barrier(0);
                 }
+                // (loads in three places: each waits for the address path otherwise)
+                fetch(fq, qp + (last ? 0 : h + 1) * a.q.head, a.q.pos, last ? ahead : c, krow, RK, klcol, kleft);
                 // lam^{i + 1}, counted from the row's first position in a first chunk
 #pragma unroll
                 for (int it = 0; it < CT; ++it) {
-                    const int i = 16 * it + l16 + 1 - first;
+                    const int i = 16 * it + (int)l16 + 1 - first;
                     O[it] *= lam[i > 0 ? i : 0];
                 }
                 __syncthreads();
@@ -338,13 +355,13 @@ __global__ __launch_bounds__(la_threads(DVS), DK == 256 ? 2 : 4) void k_lattn_ch
                 }
                 __builtin_amdgcn_sched_barrier(0);
                 T* const op = static_cast<T*>(a.o.p) + b * a.o.row + (n * a.G + h) * a.o.head + (int64_t)(c * C - pad) * a.o.pos + col0 + 16 * wave;
-                const int left = dv - (col0 + 16 * wave + 4 * g);
+                const int left = dv - (col0 + 16 * wave + 4 * (int)g);
 #pragma unroll
                 for (int it = 0; it < CT; ++it) {
                     Four y;
 #pragma unroll
                     for (int r = 0; r < 4; ++r) y[r] = (T)(a.scale * O[it][r]);
-                    if (16 * it + l16 >= first) {
+                    if (16 * it + (int)l16 >= first) {
                         if constexpr (VEC) {
                             const uint32_t off = (uint32_t)(l16 * (int)a.o.pos + 4 * g) * sizeof(T);
                             if (left > 0) *gmem(reinterpret_cast<Four*>(reinterpret_cast<char*>(op + 16 * it * a.o.pos) + off)) = y;
@@ -359,11 +376,12 @@ __global__ __launch_bounds__(la_threads(DVS), DK == 256 ? 2 : 4) void k_lattn_ch
                 __builtin_amdgcn_sched_barrier(0);
                 if (!last) {
                     __syncthreads();
-                    put(qs, PK, fq, krow, RK, kcol, kin, blank, first);
+                    put_q(blank, first);
                     __syncthreads();
                 }
             }
         }
+        if constexpr (OUT) fetch(fv, vp, a.v.pos, ahead, vrow, RV, vlcol, vleft);
         // S: its decay as S + (lam^C - 1) S (lam^C's rounding would add up
         // over the chunks of a long memory), then the chunk's own products
         const float d = c == 0 ? em1_first : em1;
@@ -412,7 +430,7 @@ __global__ __launch_bounds__(la_threads(DVS), DK == 256 ? 2 : 4) void k_lattn_ch
     float* to = OUT ? (c1 == chunks ? sp : nullptr) : wp + (int64_t)dk * dv;
     if (!to) return;
     // the lane's place anew: nothing of the loads above is kept through the loop
-    int row0 = 4 * g, scol = col0 + 16 * wave + l16;
+    int row0 = 4 * g, scol = col0 + 16 * wave + (int)l16;
     asm volatile("" : "+v"(row0), "+v"(scol));
     if (full) {
         to += row0 * dv + scol;
