@@ -115,10 +115,10 @@ __global__ __launch_bounds__(la_threads(DVS), DK == 256 ? 2 : 4) void k_lattn_ch
     using Frag = typename M::Frag;
     using Four = T __attribute__((ext_vector_type(4)));
     constexpr int C = la_chunk(BF16), KB = M::KB, E = M::E, NTH = la_threads(DVS), WAVES = NTH / kWave;
-    constexpr int PK = DK + E, PV = DVS + E, PP = C + E;         // LDS rows, 16 bytes longer
+    constexpr int PK = DK + E, PV = DVS + E;                     // K's and V's LDS rows, 16 bytes longer
     constexpr int KT = DK / 16, CT = C / 16;                     // tiles of dk and of C
     constexpr int UK = C * DK / E / NTH, UV = C * DVS / E / NTH; // 16-byte units of a thread
-    __shared__ __align__(16) T ks[C * PK], vs[C * PV], qs[OUT ? C * PK : 1], ps[OUT ? C * PP : 1];
+    __shared__ __align__(16) T ks[C * PK], vs[C * PV], qs[OUT ? C * DK : 1], ps[OUT ? C * C : 1];
 
     const int tid = threadIdx.x, lane = tid % kWave, wave = __builtin_amdgcn_readfirstlane(tid / kWave);
     uint32_t l16 = (uint32_t)lane % 16, g = (uint32_t)lane / 16;
@@ -222,18 +222,23 @@ __global__ __launch_bounds__(la_threads(DVS), DK == 256 ? 2 : 4) void k_lattn_ch
 #pragma unroll
         for (int i = 0; i < count; ++i) *smem_ptr(reinterpret_cast<Frag*>(p + i * step * pitch)) = f[i];
     };
+    // Q and P: unit u of row r at u ^ r (rows of 8 units: u ^ r / 2), so that
+    // 16 lanes with 16 rows meet every bank once whichever units they read
+    const auto mixed = [](int units, uint32_t row, uint32_t u) { return (row * units + (u ^ (units == 8 ? row / 2 % 8 : row % 16))) * E; };
     // Q's rows, for whole 16-byte operand reads beside S's (whose lanes hold
     // rows 4 g .. 4 g + 3 of two tiles): each block of KB columns is stored in
     // the order 4 (g, tile) + r
     const auto put_q = [&](bool blank, int first) {
-        if constexpr (!BF16) put(qs, PK, fq, krow, RK, kcol, kin, blank, first);
-        else {
+        {
 #pragma unroll
             for (int i = 0; i < UK; ++i) {
                 if (blank && (!kin || krow + i * RK < first)) fq[i] = Frag{};
-                T* p = qs + (krow + i * RK) * PK + kcol / KB * KB + kcol % 16 * 2 + kcol % KB / 16 * 4;
-                *smem_ptr(reinterpret_cast<BF4*>(p)) = __builtin_shufflevector(fq[i], fq[i], 0, 1, 2, 3);
-                *smem_ptr(reinterpret_cast<BF4*>(p + 8)) = __builtin_shufflevector(fq[i], fq[i], 4, 5, 6, 7);
+                const int row = krow + i * RK, u = kcol / E;
+                if constexpr (BF16) {
+                    const int at = u / 4 * 4 + u % 2 * 2, half = u / 2 % 2 * 4;
+                    *smem_ptr(reinterpret_cast<BF4*>(qs + mixed(DK / E, row, at) + half)) = __builtin_shufflevector(fq[i], fq[i], 0, 1, 2, 3);
+                    *smem_ptr(reinterpret_cast<BF4*>(qs + mixed(DK / E, row, at + 1) + half)) = __builtin_shufflevector(fq[i], fq[i], 4, 5, 6, 7);
+                } else *smem_ptr(reinterpret_cast<Frag*>(qs + mixed(DK / E, row, u))) = fq[i];
             }
         }
     };
@@ -303,8 +308,10 @@ __global__ __launch_bounds__(la_threads(DVS), DK == 256 ? 2 : 4) void k_lattn_ch
 #pragma unroll
                     for (int kb = 0; kb < DK / KB; ++kb)
                         p = M::mma(pair_frag(ks + (16 * jt + krow_) * PK + kb * KB + 4 * g),
-                                   row_frag(qs + (16 * it + l16) * PK + kb * KB + g * E), p);
-                    T* to = ps + (16 * it + l16) * PP + 16 * jt + 4 * g;
+                                   row_frag(qs + mixed(DK / E, 16 * it + l16, kb * 4 + g)), p);
+                    const auto to = [&](int tile) {   // of four of the wave's 16 keys
+                        return smem_ptr(reinterpret_cast<Four*>(ps + mixed(C / E, 16 * it + l16, (16 * tile + 4 * g) / E) + 4 * g % E));
+                    };
                     const auto key = [&](int r) { return (int)(BF16 ? 8 * (g / 2) + 2 * r + g % 2 : 4 * g + r); };   // its place in its tile
                     if (it == jt) {
 #pragma unroll
@@ -313,7 +320,7 @@ __global__ __launch_bounds__(la_threads(DVS), DK == 256 ? 2 : 4) void k_lattn_ch
                             p[r] = (i >= 0 ? p[r] : 0.f) * lam[i >= 0 ? i : 0];
                         }
                         // the rest of the block of keys that the product below takes whole
-                        if (BF16 && it % 2 == 0) *smem_ptr(reinterpret_cast<Four*>(to + 16)) = Four{};
+                        if (BF16 && it % 2 == 0) *to(jt + 1) = Four{};
                     } else {
 #pragma unroll
                         for (int r = 0; r < 4; ++r) p[r] *= lam[16 * (it - jt) + (int)l16 - key(r)];
@@ -321,7 +328,7 @@ __global__ __launch_bounds__(la_threads(DVS), DK == 256 ? 2 : 4) void k_lattn_ch
                     Four y;
 #pragma unroll
                     for (int r = 0; r < 4; ++r) y[r] = (T)p[r];
-                    *smem_ptr(reinterpret_cast<Four*>(to)) = y;
+                    *to(jt) = y;
                 }
                 __builtin_amdgcn_sched_barrier(0);
                 // O^T = E^T Q^T: columns are positions
@@ -333,7 +340,7 @@ __global__ __launch_bounds__(la_threads(DVS), DK == 256 ? 2 : 4) void k_lattn_ch
                     for (int e = 0; e < E; ++e) fs[e] = (T)S[kb * (KB / 16) + e / 4][e % 4];
 #pragma unroll
                     for (int it = 0; it < CT; ++it) {
-                        O[it] = M::mma(fs, row_frag(qs + (16 * it + l16) * PK + kb * KB + g * E), O[it]);
+                        O[it] = M::mma(fs, row_frag(qs + mixed(DK / E, 16 * it + l16, kb * 4 + g)), O[it]);
                     }
                     __builtin_amdgcn_sched_barrier(0);
                 }
@@ -351,7 +358,7 @@ __global__ __launch_bounds__(la_threads(DVS), DK == 256 ? 2 : 4) void k_lattn_ch
                     const Frag v = transposed(vs, PV, kb * KB, 16 * wave);
 #pragma unroll
                     for (int it = kb * KB / 16; it < CT; ++it)   // queries before every key of the block: nothing
-                        O[it] = M::mma(v, row_frag(ps + (16 * it + l16) * PP + kb * KB + g * E), O[it]);
+                        O[it] = M::mma(v, row_frag(ps + mixed(C / E, 16 * it + l16, kb * 4 + g)), O[it]);
                 }
                 __builtin_amdgcn_sched_barrier(0);
                 T* const op = static_cast<T*>(a.o.p) + b * a.o.row + (n * a.G + h) * a.o.head + (int64_t)(c * C - pad) * a.o.pos + col0 + 16 * wave;
@@ -401,16 +408,22 @@ __global__ __launch_bounds__(la_threads(DVS), DK == 256 ? 2 : 4) void k_lattn_ch
                 for (int i = 0; i < 4; ++i) w[BF16 ? (e + i) / 2 + (i % 2) * 4 : i] = x[i];
             }
             if constexpr (BF16) {
-                // V's decayed rows as a sum of three bf16 parts (24 bits): the state keeps fp32's precision
-                Frag hi, mid, lo;
+                // V's decayed rows as the sum of three bf16 parts, each the top
+                // 8 bits of what is left: exact, so that the state keeps fp32's precision
+                uint32_t part[3][E / 2];
 #pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    const float x = (float)v[e] * w[e];
-                    hi[e] = (BF)x;
-                    const float y = x - (float)hi[e];
-                    mid[e] = (BF)y;
-                    lo[e] = (BF)(y - (float)mid[e]);
+                for (int e = 0; e < E; e += 2) {
+                    float x = (float)v[e] * w[e], y = (float)v[e + 1] * w[e + 1];
+#pragma unroll
+                    for (int i = 0; i < 3; ++i) {
+                        const uint32_t ux = __float_as_uint(x), uy = __float_as_uint(y);
+                        part[i][e / 2] = __builtin_amdgcn_perm(uy, ux, 0x07060302);   // the upper halves
+                        x -= __uint_as_float(ux & 0xFFFF0000u);
+                        y -= __uint_as_float(uy & 0xFFFF0000u);
+                    }
                 }
+                const Frag hi = __builtin_bit_cast(Frag, part[0]), mid = __builtin_bit_cast(Frag, part[1]),
+                           lo = __builtin_bit_cast(Frag, part[2]);
 #pragma unroll
                 for (int kt = 0; kt < KT; ++kt) {
                     const Frag k = transposed(ks, PK, kb * KB, 16 * kt);
