@@ -24,12 +24,37 @@ __device__ __forceinline__ void put_io(void* p, int64_t i, float v) {
 // lam^n = exp(n ld), n >= 0; lam^0 = 1 for lam = 0 (ld = -inf) too
 __device__ __forceinline__ float decay_pow(float ld, float n) { return n == 0.f ? 1.f : expf(n * ld); }
 
-// The blocks' activations: 0 GELU (exact), 1 tanh, 2 identity.
-template <int ACT>
-__device__ __forceinline__ float activate(float v) {
-    if constexpr (ACT == 0) return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
-    else if constexpr (ACT == 1) return tanhf(v);
-    else return v;
+// GELU, v Phi(v) = max(v, 0) - |v| Phi(-|v|), with Phi(-|v|) = erfc(|v| /
+// sqrt 2) / 2 from Abramowitz and Stegun's 7.1.26: erfc(x) = (a1 t + .. + a5
+// t^5) e^{-x^2}, t = 1 / (1 + p x), off by 1.5e-7 at most, so GELU by less
+// than a rounding of |v| to fp32.  Without branches: 13 operations and two of
+// the transcendental unit (the library's erff cost three times that).
+__device__ __forceinline__ float gelu(float v) {
+    const float x = fminf(fabsf(v), __FLT_MAX__) * 0.70710678118654752f;   // finite: 0 x = 0 below for v = inf
+    const float t = __builtin_amdgcn_rcpf(fmaf(0.3275911f, x, 1.f));
+    const float e = __builtin_amdgcn_exp2f(x * x * -1.4426950408889634f);
+    float q = fmaf(t, 1.061405429f, -1.453152027f);
+    q = fmaf(t, q, 1.421413741f);
+    q = fmaf(t, q, -0.284496736f);
+    q = fmaf(t, q, 0.254829592f);
+    // (x carries 1 / sqrt 2, q t e twice Phi)
+    return fmaf(-0.70710678118654752f * x, q * t * e, fmaxf(v, 0.f)) + (v != v ? v : 0.f);
+}
+
+// tanh |v| = 1 - 2 / (1 + e^{2 |v|}), and for small v, where that cancels, its
+// series to v^9 (the next term is 5e-8 v at the seam).
+__device__ __forceinline__ float tanh_flat(float v) {
+    const float x = fabsf(v), s = v * v;
+    const float big = copysignf(fmaf(-2.f, __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(x * 2.8853900817779268f)), 1.f), v);
+    float q = fmaf(s, 62.f / 2835.f, -17.f / 315.f);
+    q = fmaf(s, q, 2.f / 15.f);
+    q = fmaf(s, q, -1.f / 3.f);
+    return x < 0.3f ? fmaf(v * s, q, v) : big;
+}
+
+// The blocks' activations: 0 GELU, 1 tanh, 2 identity.
+__device__ __forceinline__ float activate(float v, int act) {
+    return act == 0 ? gelu(v) : act == 1 ? tanh_flat(v) : v;
 }
 
 using BF8 = BF __attribute__((ext_vector_type(8)));
