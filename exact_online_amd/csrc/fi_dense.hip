@@ -49,165 +49,231 @@ __device__ __forceinline__ void load_bias(const DenseCall& a, int64_t n, float* 
 }
 
 // ------------------------------------------------------------ tiles of many rows
-// A workgroup of WM x WN waves has a BM x BN tile of y at a time; K goes by in
-// steps of 128 bytes of a row, two LDS buffers, the next step's loads in
-// flight during a step's products (the next tile's first step during a tile's
-// last results).  A row's eight 16-byte units are stored at u ^ (row / 2 % 8):
-// the 16 lanes that read one unit of 16 rows then meet every bank once.  The
-// products are taken as w x^T, so that a lane's results are neighbours in a
-// row of y; they go through LDS once more, so that whole lines are stored.
-template <bool BF16, int BM, int BN, int WM, int WN, bool DIRECT>
-__global__ __launch_bounds__(WM* WN * kWave) void k_dense(DenseCall a) {
+// A workgroup of WM x WN waves has one BM x BN tile of y, a wave TM x TN
+// products of 32 x 32; the products are taken as w x^T, so that a lane's
+// results are neighbours in a row of y.
+
+// Workgroups go round the 8 XCDs: each XCD gets one run of tiles, in which
+// four rows of tiles go together along N (they share w in its L2).
+template <int BM, int BN>
+struct Tile {
+    int64_t m0, n0, k0, k1;
+    uint32_t split;
+    __device__ __forceinline__ Tile(const DenseCall& a, uint32_t job) {
+        const uint32_t tm = (uint32_t)((a.M + BM - 1) / BM), tn = (uint32_t)((a.N + BN - 1) / BN), tiles = tm * tn;
+        const uint32_t at = job % tiles, per = tiles / 8, over = tiles % 8, xcd = at % 8;
+        split = job / tiles;
+        const uint32_t id = xcd * per + (xcd < over ? xcd : over) + at / 8;
+        const uint32_t gm = id / (4 * tn) * 4, rows = tm - gm < 4 ? tm - gm : 4, in = id - gm * tn;
+        m0 = (int64_t)(gm + in % rows) * BM;
+        n0 = (int64_t)(in / rows) * BN;
+        k0 = split * a.k_split;
+        k1 = k0 + a.k_split < a.K ? k0 + a.k_split : a.K;
+    }
+};
+
+// A wave's results, 32 rows at a time through its part of LDS (`out`, 32 rows
+// of TN * 32), so that whole lines are stored.
+template <bool IO, int TM, int TN>
+__device__ __forceinline__ void dense_results(const DenseCall& a, int64_t m, int64_t n, uint32_t split, V16 (&acc)[TN][TM],
+                                              float* out, uint32_t lane) {
+    constexpr int UR = TN * 8, LANES = UR / 2, STEP = kWave / LANES;   // 16-byte units of a row; lanes, 8 results each; rows at once
+    const auto unit_of = [](uint32_t row, uint32_t u) { return (row * UR + (u ^ (UR == 8 ? row / 2 % 8 : row % 16))) * 4; };
+    const uint32_t l32 = lane % 32, half = lane / 32, row_ = lane / LANES, col = lane % LANES;
+    float bias[8];
+    load_bias<IO, 8>(a, n + col * 8, bias);
+#pragma unroll
+    for (int j = 0; j < TM; ++j) {
+#pragma unroll
+        for (int i = 0; i < TN; ++i)
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                *smem_ptr(reinterpret_cast<V4*>(out + unit_of(l32, 8 * i + 2 * q + half))) =
+                    V4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+        wave_order();
+#pragma unroll 1
+        for (int r = 0; r < 32; r += STEP) {
+            const uint32_t row = r + row_;
+            const V4 v0 = *smem_ptr(reinterpret_cast<const V4*>(out + unit_of(row, 2 * col)));
+            const V4 v1 = *smem_ptr(reinterpret_cast<const V4*>(out + unit_of(row, 2 * col + 1)));
+            float v[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+            const int64_t mm = m + 32 * j + row, nn = n + col * 8;
+            if (a.splits == 1) dense_out<IO, 8>(a, mm, nn, bias, v);
+            else if (mm < a.M && nn < a.ldp) {   // rows of `part` are a multiple of eight long
+                V4* to = reinterpret_cast<V4*>(a.part + (split * a.M + mm) * a.ldp + nn);
+                gmem(to)[0] = v0;
+                gmem(to)[1] = v1;
+            }
+        }
+        wave_order();
+    }
+}
+
+template <bool BF16, int TM, int TN>
+__device__ __forceinline__ void dense_mma(V16 (&acc)[TN][TM], const typename Mm<BF16>::Frag (&fw)[TN],
+                                          const typename Mm<BF16>::Frag (&fx)[TM]) {
+#pragma unroll
+    for (int i = 0; i < TN; ++i)
+#pragma unroll
+        for (int j = 0; j < TM; ++j) {
+            if constexpr (BF16) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fw[i], fx[j], acc[i][j], 0, 0, 0);
+            else
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x2f32(fw[i][e], fx[j][e], acc[i][j], 0, 0, 0);
+        }
+}
+
+// Rows in whole 16-byte units.  K goes by in steps of 64 bytes of a row,
+// loaded straight into one of three LDS buffers two steps ahead; a step has
+// two halves, and the operands of each are read during the products of the
+// one before.  A row's four units are stored at u ^ (row / 4 % 4): the lanes
+// that read one unit of 16 rows then meet every bank once.
+template <bool BF16, int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__(WM* WN * kWave, 2) void k_dense(DenseCall a) {
     using M = Mm<BF16>;
     using T = typename M::T;
     using Frag = typename M::Frag;
-    constexpr int E = M::E, BK = 8 * E, NTH = WM * WN * kWave, ROWS = BM + BN;
-    constexpr int UX = BM * 8 / NTH, UN = ROWS * 8 / NTH;      // units per thread: of x, of both
-    constexpr int TM = BM / WM / 32, TN = BN / WN / 32;        // 32 x 32 products of a wave
-    constexpr int UR = TN * 8;                                 // 16-byte units of a wave's row of results
-    static_assert(WM * WN * 32 * UR * 16 <= ROWS * BK * (int)sizeof(T), "the waves' results fit one buffer");
+    constexpr int E = M::E, U = 4, BK = U * E, NTH = WM * WN * kWave, ROWS = BM + BN, STAGES = 3;
+    constexpr int UX = BM * U / NTH, UN = ROWS * U / NTH;      // units per thread: of x, of both
+    constexpr int TM = BM / WM / 32, TN = BN / WN / 32;
+    static_assert(UX * NTH == BM * U && UN * NTH == ROWS * U, "every thread loads the same");
+    static_assert(WM * WN * 32 * TN * 32 * 4 <= STAGES * ROWS * 64, "the waves' results fit");
+    __shared__ __align__(16) T lds[STAGES][ROWS * BK];
+
+    const int tid = threadIdx.x, lane = tid % kWave, wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+    const uint32_t l32 = lane % 32, half = lane / 32;
+    const int wm = wave / WN * (BM / WM), wn = wave % WN * (BN / WN);
+    const Tile<BM, BN> t(a, blockIdx.x);
+    // a unit's place: a wave's own base and the lane's offset in bytes (the
+    // rows of a tile span less than 2^32)
+    const char* const xb = reinterpret_cast<const char*>(static_cast<const T*>(a.x) + t.m0 * a.ldx + t.k0);
+    const char* const wb = reinterpret_cast<const char*>(static_cast<const T*>(a.w) + t.n0 * a.ldw + t.k0);
+    uint32_t off[UN];
+#pragma unroll
+    for (int i = 0; i < UN; ++i) {
+        const int u = i * NTH + tid, unit = u % U ^ (u / U / 4 % U);
+        const int64_t last = (i < UX ? a.M - t.m0 : a.N - t.n0) - 1;   // rows beyond the end are not stored
+        int row = u / U - (i < UX ? 0 : BM);
+        row = row < last ? row : (int)last;
+        off[i] = ((uint32_t)row * (uint32_t)(i < UX ? a.ldx : a.ldw) + unit * E) * (uint32_t)sizeof(T);
+    }
+    const auto fetch = [&](int k, int stage) {
+#pragma unroll
+        for (int i = 0; i < UN; ++i)
+            __builtin_amdgcn_global_load_lds((const FI_GLOBAL void*)((i < UX ? xb : wb) + (int64_t)k * 64 + off[i]),
+                                             (FI_SHARED void*)(&lds[stage][(i * NTH + wave * kWave) * E]), 16, 0, 0);
+    };
+    V16 acc[TN][TM] = {};
+    const auto read = [&](Frag (&fw)[TN], Frag (&fx)[TM], int stage, int s) {
+        const uint32_t unit = (2 * s + half) ^ (l32 / 4 % U);
+#pragma unroll
+        for (int i = 0; i < TN; ++i)
+            fw[i] = *smem_ptr(reinterpret_cast<const Frag*>(&lds[stage][((BM + wn + 32 * i + l32) * U + unit) * E]));
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+            fx[i] = *smem_ptr(reinterpret_cast<const Frag*>(&lds[stage][((wm + 32 * i + l32) * U + unit) * E]));
+    };
+    // All loads but the newest step's have arrived in LDS and the wave's reads
+    // of LDS are done, in every wave.  (Loads into LDS count as vector memory
+    // operations and complete in order; a fence would wait for all of them.)
+    const auto arrive = [&](bool newest) {
+        if (newest) asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(UN) : "memory");
+        else asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    };
+    const int steps = (int)((t.k1 - t.k0) / BK), tail = (int)((t.k1 - t.k0) % BK);
+    if (steps > 0) fetch(0, 0);
+    if (steps > 1) fetch(1, 1);
+    arrive(steps > 1);
+    Frag w0[TN], x0[TM], w1[TN] = {}, x1[TM] = {};
+    int stage = 0;
+    for (int k = 0; k < steps; ++k) {
+        const int next = stage == STAGES - 1 ? 0 : stage + 1;
+        if (k + 2 < steps) fetch(k + 2, next == STAGES - 1 ? 0 : next + 1);   // the buffer of step k - 1
+        read(w0, x0, stage, 0);
+        __builtin_amdgcn_sched_barrier(0);   // the reads go out ahead of the products
+        dense_mma<BF16, TM, TN>(acc, w1, x1);
+        __builtin_amdgcn_sched_barrier(0);
+        read(w1, x1, stage, 1);
+        __builtin_amdgcn_sched_barrier(0);
+        dense_mma<BF16, TM, TN>(acc, w0, x0);
+        __builtin_amdgcn_sched_barrier(0);
+        arrive(k + 2 < steps);
+        stage = next;
+    }
+    dense_mma<BF16, TM, TN>(acc, w1, x1);
+    if (tail) {   // the last, shorter step
+#pragma unroll
+        for (int i = 0; i < UN; ++i) {
+            const int u = i * NTH + tid, unit = u % U ^ (u / U / 4 % U);
+            const Frag f = load_loose<BF16>(reinterpret_cast<const T*>((i < UX ? xb : wb) + (int64_t)steps * 64 + off[i]), 0, tail - unit * E);
+            *smem_ptr(reinterpret_cast<Frag*>(&lds[0][u * E])) = f;
+        }
+        team_sync();
+        read(w0, x0, 0, 0);
+        read(w1, x1, 0, 1);
+        dense_mma<BF16, TM, TN>(acc, w0, x0);
+        dense_mma<BF16, TM, TN>(acc, w1, x1);
+        team_sync();
+    }
+    dense_results<BF16, TM, TN>(a, t.m0 + wm, t.n0 + wn, t.split, acc,
+                                reinterpret_cast<float*>(&lds[0][0]) + wave * 32 * TN * 32, lane);
+}
+
+// Rows at any alignment: K in steps of 128 bytes through registers into two
+// LDS buffers (a row's eight units at u ^ (row / 2 % 8)).
+template <bool BF16, int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__(WM* WN * kWave) void k_dense_loose(DenseCall a) {
+    using M = Mm<BF16>;
+    using T = typename M::T;
+    using Frag = typename M::Frag;
+    constexpr int E = M::E, U = 8, BK = U * E, NTH = WM * WN * kWave, ROWS = BM + BN;
+    constexpr int UX = BM * U / NTH, UN = ROWS * U / NTH;
+    constexpr int TM = BM / WM / 32, TN = BN / WN / 32;
     __shared__ __align__(16) T lds[2][ROWS * BK];
 
     const int tid = threadIdx.x, lane = tid % kWave, wave = __builtin_amdgcn_readfirstlane(tid / kWave);
     const uint32_t l32 = lane % 32, half = lane / 32;
     const int wm = wave / WN * (BM / WM), wn = wave % WN * (BN / WN);
-    const int64_t tm = (a.M + BM - 1) / BM, tn = (a.N + BN - 1) / BN, tiles = tm * tn, all = tiles * a.splits;
-    int64_t m0, n0, k0, k1, split;
-    // a unit's place: a wave's own base and the lane's offset in bytes (DIRECT:
-    // the rows of a tile span less than 2^32)
-    using Off = std::conditional_t<DIRECT, uint32_t, int64_t>;
-    const char *xb, *wb;
-    Off off[UN];
-    // workgroups go round the 8 XCDs: each XCD gets one run of tiles, in which
-    // four rows of tiles go together along N (they share w in its L2)
-    const auto place = [&](int64_t job) {
-        const int64_t at = job % tiles, per = tiles / 8, over = tiles % 8, xcd = at % 8;
-        split = job / tiles;
-        const int64_t id = xcd * per + (xcd < over ? xcd : over) + at / 8;
-        const int64_t gm = id / (4 * tn) * 4, rows = tm - gm < 4 ? tm - gm : 4, in = id - gm * tn;
-        m0 = (gm + in % rows) * BM;
-        n0 = in / rows * BN;
-        k0 = split * a.k_split;
-        k1 = k0 + a.k_split < a.K ? k0 + a.k_split : a.K;
-        xb = reinterpret_cast<const char*>(static_cast<const T*>(a.x) + m0 * a.ldx);
-        wb = reinterpret_cast<const char*>(static_cast<const T*>(a.w) + n0 * a.ldw);
+    const Tile<BM, BN> t(a, blockIdx.x);
+    Frag hold[UN];
+    const auto fetch = [&](int64_t k) {
 #pragma unroll
         for (int i = 0; i < UN; ++i) {
-            const int u = i * NTH + tid, unit = u % 8 ^ (u / 16 % 8);
-            int row = u / 8 - (i < UX ? 0 : BM);
-            const int64_t last = (i < UX ? a.M - m0 : a.N - n0) - 1;   // rows beyond the end are not stored
-            row = row < last ? row : (int)last;
-            off[i] = ((Off)row * (Off)(i < UX ? a.ldx : a.ldw) + unit * E) * (Off)sizeof(T);
+            const int u = i * NTH + tid, unit = u % U ^ (u / U / 2 % U), row = u / U - (i < UX ? 0 : BM);
+            const int64_t r = (i < UX ? t.m0 : t.n0) + row, last = (i < UX ? a.M : a.N) - 1;
+            const T* p = static_cast<const T*>(i < UX ? a.x : a.w) + (r < last ? r : last) * (i < UX ? a.ldx : a.ldw);
+            hold[i] = load_loose<BF16>(p, k + unit * E, t.k1);
         }
     };
-    Frag hold[UN];
-    const auto whole = [&](int64_t k) { return DIRECT && k + BK <= k1; };
-    const auto fetch = [&](int64_t k, int buf) {
-        if (whole(k)) {
-#pragma unroll
-            for (int i = 0; i < UN; ++i)
-                __builtin_amdgcn_global_load_lds((const FI_GLOBAL void*)((i < UX ? xb : wb) + k * (int)sizeof(T) + off[i]),
-                                                 (FI_SHARED void*)(&lds[buf][(i * NTH + wave * kWave) * E]), 16, 0, 0);
-        } else {
-#pragma unroll
-            for (int i = 0; i < UN; ++i) {
-                const int u = i * NTH + tid, unit = u % 8 ^ (u / 8 / 2 % 8);
-                hold[i] = load_loose<BF16>(reinterpret_cast<const T*>((i < UX ? xb : wb) + off[i]) + k, 0, k1 - k - unit * E);
-            }
-        }
-    };
-    const auto settle = [&](int64_t k, int buf) {
-        if (whole(k)) return;
+    const auto settle = [&](int buf) {
 #pragma unroll
         for (int i = 0; i < UN; ++i) *smem_ptr(reinterpret_cast<Frag*>(&lds[buf][(i * NTH + tid) * E])) = hold[i];
     };
+    V16 acc[TN][TM] = {};
+    fetch(t.k0);
+    settle(0);
     int buf = 0;
-    int64_t job = blockIdx.x;
-    place(job);
-    fetch(k0, 0);
-    while (true) {
-        settle(k0, buf);
-        V16 acc[TN][TM] = {};
-        for (int64_t k = k0; k < k1; k += BK, buf ^= 1) {
-            __syncthreads();
-            const bool more = k + BK < k1;
-            if (more) fetch(k + BK, buf ^ 1);
+    for (int64_t k = t.k0; k < t.k1; k += BK, buf ^= 1) {
+        team_sync();
+        const bool more = k + BK < t.k1;
+        if (more) fetch(k + BK);
 #pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                Frag fw[TN], fx[TM];
-#pragma unroll
-                for (int i = 0; i < TN; ++i) {
-                    const uint32_t row = BM + wn + 32 * i + l32;
-                    fw[i] = *smem_ptr(reinterpret_cast<const Frag*>(&lds[buf][(row * 8 + ((2 * s + half) ^ (l32 / 2 % 8))) * E]));
-                }
-#pragma unroll
-                for (int i = 0; i < TM; ++i) {
-                    const uint32_t row = wm + 32 * i + l32;
-                    fx[i] = *smem_ptr(reinterpret_cast<const Frag*>(&lds[buf][(row * 8 + ((2 * s + half) ^ (l32 / 2 % 8))) * E]));
-                }
-#pragma unroll
-                for (int i = 0; i < TN; ++i)
-#pragma unroll
-                    for (int j = 0; j < TM; ++j) {
-                        if constexpr (BF16) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fw[i], fx[j], acc[i][j], 0, 0, 0);
-                        else
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x2f32(fw[i][e], fx[j][e], acc[i][j], 0, 0, 0);
-                    }
-            }
-            if (more) settle(k + BK, buf ^ 1);
-        }
-        // buf is the buffer of the step before the last one, free for the next
-        // tile since the last step's barrier; the last step's takes the results
-        const int64_t m = m0 + wm, n = n0 + wn, part = split;
-        job += gridDim.x;
-        const bool next = job < all;
-        if (next) {
-            place(job);
-            if (whole(k0)) fetch(k0, buf);
-        }
-        __syncthreads();
-        float* const out = reinterpret_cast<float*>(lds[buf ^ 1]) + wave * 32 * UR * 4;
-        const auto unit_of = [](uint32_t row, uint32_t u) { return (row * UR + (u ^ (UR == 8 ? row / 2 % 8 : row % 16))) * 4; };
-        constexpr int LANES = UR / 2, STEP = kWave / LANES;   // lanes of a row, 8 results each; rows of an instruction
-        const uint32_t row_ = lane / LANES, col = lane % LANES;
-        float bias[8];
-        load_bias<BF16, 8>(a, n + col * 8, bias);
-#pragma unroll
-        for (int j = 0; j < TM; ++j) {
+        for (int s = 0; s < 4; ++s) {
+            Frag fw[TN], fx[TM];
+            const uint32_t unit = (2 * s + half) ^ (l32 / 2 % U);
 #pragma unroll
             for (int i = 0; i < TN; ++i)
+                fw[i] = *smem_ptr(reinterpret_cast<const Frag*>(&lds[buf][((BM + wn + 32 * i + l32) * U + unit) * E]));
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    *smem_ptr(reinterpret_cast<V4*>(out + unit_of(l32, 8 * i + 2 * q + half))) =
-                        V4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
-            // a wave's LDS operations are performed in order
-            __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-            __builtin_amdgcn_wave_barrier();
-            __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-#pragma unroll 1
-            for (int r = 0; r < 32; r += STEP) {
-                const uint32_t row = r + row_;
-                const V4 v0 = *smem_ptr(reinterpret_cast<const V4*>(out + unit_of(row, 2 * col)));
-                const V4 v1 = *smem_ptr(reinterpret_cast<const V4*>(out + unit_of(row, 2 * col + 1)));
-                float v[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
-                const int64_t mm = m + 32 * j + row, nn = n + col * 8;
-                if (a.splits == 1) dense_out<BF16, 8>(a, mm, nn, bias, v);
-                else if (mm < a.M) {   // rows of `part` are a multiple of eight long
-                    V4* to = reinterpret_cast<V4*>(a.part + (part * a.M + mm) * a.ldp + nn);
-                    if (nn < a.ldp) {
-                        gmem(to)[0] = v0;
-                        gmem(to)[1] = v1;
-                    }
-                }
-            }
-            __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-            __builtin_amdgcn_wave_barrier();
-            __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+            for (int i = 0; i < TM; ++i)
+                fx[i] = *smem_ptr(reinterpret_cast<const Frag*>(&lds[buf][((wm + 32 * i + l32) * U + unit) * E]));
+            dense_mma<BF16, TM, TN>(acc, fw, fx);
         }
-        if (!next) return;
-        if (!whole(k0)) fetch(k0, buf);
+        if (more) settle(buf ^ 1);
     }
+    team_sync();
+    dense_results<BF16, TM, TN>(a, t.m0 + wm, t.n0 + wn, t.split, acc,
+                                reinterpret_cast<float*>(&lds[0][0]) + wave * 32 * TN * 32, lane);
 }
 
 // The parts of a product split over K, summed in their order.
@@ -291,6 +357,10 @@ __global__ __launch_bounds__((KW > 4 ? KW : 4) * kWave) void k_dense_few(DenseCa
 
 namespace {
 
+constexpr int64_t kCus = 256;
+
+int64_t tiles_of(int64_t M, int64_t N, int bm, int bn) { return ((M + bm - 1) / bm) * ((N + bn - 1) / bn); }
+
 template <bool BF16, int MT, int KW>
 void few(const DenseCall& c, bool direct, hipStream_t st) {
     constexpr int WAVES = KW > 4 ? KW : 4;
@@ -300,23 +370,17 @@ void few(const DenseCall& c, bool direct, hipStream_t st) {
     else k_dense_few<BF16, MT, KW, false><<<grid, WAVES * kWave, 0, st>>>(c);
 }
 
-constexpr int64_t kCus = 256;
-
 template <bool BF16, int BM, int BN, int WM, int WN>
 void tile(const DenseCall& c, bool direct, hipStream_t st) {
-    const int64_t jobs = ((c.M + BM - 1) / BM) * ((c.N + BN - 1) / BN) * c.splits;
-    constexpr int64_t kRoom = kCus * (BM == 256 ? 1 : BM == 128 ? 2 : 4);   // workgroups that are resident together
-    const unsigned grid = (unsigned)(jobs < kRoom ? jobs : kRoom);
-    if (direct) k_dense<BF16, BM, BN, WM, WN, true><<<grid, WM * WN * kWave, 0, st>>>(c);
-    else k_dense<BF16, BM, BN, WM, WN, false><<<grid, WM * WN * kWave, 0, st>>>(c);
+    const unsigned grid = (unsigned)(tiles_of(c.M, c.N, BM, BN) * c.splits);
+    if (direct) k_dense<BF16, BM, BN, WM, WN><<<grid, WM * WN * kWave, 0, st>>>(c);
+    else k_dense_loose<BF16, BM, BN, WM, WN><<<grid, WM * WN * kWave, 0, st>>>(c);
     if (c.splits > 1)
         k_dense_join<BF16><<<(unsigned)((c.M * (c.ldp / 8) + 255) / 256), 256, 0, st>>>(c);
 }
 
 constexpr int64_t kFewRows = 32;
 constexpr int64_t kMinSplitK = 256;    // of K, for one part
-
-int64_t tiles_of(int64_t M, int64_t N, int bm, int bn) { return ((M + bm - 1) / bm) * ((N + bn - 1) / bn); }
 
 // parts that K of a product of M rows is split into (tiles of 64 x 64)
 int64_t splits_of(int64_t M, int64_t N, int64_t K) {
@@ -329,7 +393,7 @@ int64_t splits_of(int64_t M, int64_t N, int64_t K) {
 
 template <bool BF16>
 hipError_t run(DenseCall& c, hipStream_t st) {
-    constexpr int es = BF16 ? 2 : 4, E = 16 / es, BK = 8 * E;
+    constexpr int E = BF16 ? 8 : 4, BK = 8 * E;
     const auto whole = [](const void* p, int64_t ld) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % E == 0 && ld < (1 << 21); };
     const bool direct = whole(c.x, c.ldx) && whole(c.w, c.ldw);
     c.splits = 1;
@@ -356,8 +420,8 @@ hipError_t run(DenseCall& c, hipStream_t st) {
     }
     if (c.splits == 1) c.part = nullptr;
     if (c.splits > 1 || tiles_of(c.M, c.N, 128, 128) < kCus) tile<BF16, 64, 64, 2, 2>(c, direct, st);
-    else if (tiles_of(c.M, c.N, 256, 256) < kCus) tile<BF16, 128, 128, 2, 2>(c, direct, st);
-    else tile<BF16, 256, 256, 2, 4>(c, direct, st);
+    else if (!direct || tiles_of(c.M, c.N, 256, 128) < 2 * kCus) tile<BF16, 128, 128, 2, 2>(c, direct, st);
+    else k_dense<BF16, 256, 128, 2, 2><<<(unsigned)tiles_of(c.M, c.N, 256, 128), 4 * kWave, 0, st>>>(c);
     return hipGetLastError();
 }
 

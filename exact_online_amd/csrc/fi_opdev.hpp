@@ -21,6 +21,14 @@ __device__ __forceinline__ void put_io(void* p, int64_t i, float v) {
     else gmem(static_cast<float*>(p))[i] = v;
 }
 
+// A wave's own LDS operations before this come before those after it (they
+// are performed in order; the compiler has to keep them so).
+__device__ __forceinline__ void wave_order() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
+}
+
 // lam^n = exp(n ld), n >= 0; lam^0 = 1 for lam = 0 (ld = -inf) too
 __device__ __forceinline__ float decay_pow(float ld, float n) { return n == 0.f ? 1.f : expf(n * ld); }
 
