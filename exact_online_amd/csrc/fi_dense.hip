@@ -91,7 +91,7 @@ __device__ __forceinline__ void dense_results(const DenseCall& a, int64_t m, int
                 *smem_ptr(reinterpret_cast<V4*>(out + unit_of(l32, 8 * i + 2 * q + half))) =
                     V4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
         wave_order();
-#pragma unroll 1
+#pragma unroll 2
         for (int r = 0; r < 32; r += STEP) {
             const uint32_t row = r + row_;
             const V4 v0 = *smem_ptr(reinterpret_cast<const V4*>(out + unit_of(row, 2 * col)));
@@ -109,36 +109,38 @@ __device__ __forceinline__ void dense_results(const DenseCall& a, int64_t m, int
     }
 }
 
-template <bool BF16, int TM, int TN>
+// The products of a wave's TN x TM, `between(p)` after the p-th.
+template <bool BF16, int TM, int TN, class F>
 __device__ __forceinline__ void dense_mma(V16 (&acc)[TN][TM], const typename Mm<BF16>::Frag (&fw)[TN],
-                                          const typename Mm<BF16>::Frag (&fx)[TM]) {
+                                          const typename Mm<BF16>::Frag (&fx)[TM], F between) {
 #pragma unroll
-    for (int i = 0; i < TN; ++i)
+    for (int p = 0; p < TM * TN; ++p) {
+        const int i = p / TM, j = p % TM;
+        if constexpr (BF16) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fw[i], fx[j], acc[i][j], 0, 0, 0);
+        else
 #pragma unroll
-        for (int j = 0; j < TM; ++j) {
-            if constexpr (BF16) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fw[i], fx[j], acc[i][j], 0, 0, 0);
-            else
-#pragma unroll
-                for (int e = 0; e < 4; ++e) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x2f32(fw[i][e], fx[j][e], acc[i][j], 0, 0, 0);
-        }
+            for (int e = 0; e < 4; ++e) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x2f32(fw[i][e], fx[j][e], acc[i][j], 0, 0, 0);
+        between(p);
+    }
 }
 
-// Rows in whole 16-byte units.  K goes by in steps of 64 bytes of a row,
-// loaded straight into one of three LDS buffers two steps ahead; a step has
-// two halves, and the operands of each are read during the products of the
-// one before.  A row's four units are stored at u ^ (row / 4 % 4): the lanes
-// that read one unit of 16 rows then meet every bank once.
+// Rows in whole 16-byte units.  K goes by in steps of 128 bytes of a row (half
+// lines cost the L2 as much as whole ones), loaded straight into one of two
+// LDS buffers, a step ahead; a step has four parts, and the operands of each
+// are read during the products of the one before.  A row's eight units are
+// stored at u ^ (row / 2 % 8): the lanes that read one unit of 16 rows then
+// meet every bank once.
 template <bool BF16, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(WM* WN * kWave, 2) void k_dense(DenseCall a) {
     using M = Mm<BF16>;
     using T = typename M::T;
     using Frag = typename M::Frag;
-    constexpr int E = M::E, U = 4, BK = U * E, NTH = WM * WN * kWave, ROWS = BM + BN, STAGES = 3;
+    constexpr int E = M::E, U = 8, BK = U * E, NTH = WM * WN * kWave, ROWS = BM + BN;
     constexpr int UX = BM * U / NTH, UN = ROWS * U / NTH;      // units per thread: of x, of both
     constexpr int TM = BM / WM / 32, TN = BN / WN / 32;
     static_assert(UX * NTH == BM * U && UN * NTH == ROWS * U, "every thread loads the same");
-    static_assert(WM * WN * 32 * TN * 32 * 4 <= STAGES * ROWS * 64, "the waves' results fit");
-    __shared__ __align__(16) T lds[STAGES][ROWS * BK];
+    static_assert(WM * WN * 32 * TN * 32 * 4 <= 2 * ROWS * U * 16, "the waves' results fit");
+    __shared__ __align__(16) T lds[2][ROWS * BK];
 
     const int tid = threadIdx.x, lane = tid % kWave, wave = __builtin_amdgcn_readfirstlane(tid / kWave);
     const uint32_t l32 = lane % 32, half = lane / 32;
@@ -151,68 +153,84 @@ __global__ __launch_bounds__(WM* WN * kWave, 2) void k_dense(DenseCall a) {
     uint32_t off[UN];
 #pragma unroll
     for (int i = 0; i < UN; ++i) {
-        const int u = i * NTH + tid, unit = u % U ^ (u / U / 4 % U);
+        const int u = i * NTH + tid, unit = u % U ^ (u / U / 2 % U);
         const int64_t last = (i < UX ? a.M - t.m0 : a.N - t.n0) - 1;   // rows beyond the end are not stored
         int row = u / U - (i < UX ? 0 : BM);
         row = row < last ? row : (int)last;
         off[i] = ((uint32_t)row * (uint32_t)(i < UX ? a.ldx : a.ldw) + unit * E) * (uint32_t)sizeof(T);
     }
-    const auto fetch = [&](int k, int stage) {
-#pragma unroll
-        for (int i = 0; i < UN; ++i)
-            __builtin_amdgcn_global_load_lds((const FI_GLOBAL void*)((i < UX ? xb : wb) + (int64_t)k * 64 + off[i]),
-                                             (FI_SHARED void*)(&lds[stage][(i * NTH + wave * kWave) * E]), 16, 0, 0);
+    // (the empty asm: the places stay a scalar base and a 32-bit offset, and are
+    // not turned into 64-bit ones that are carried through the loop)
+    const auto fetch_one = [&](int i, int k, int stage) {
+        uint32_t o = off[i];
+        asm volatile("" : "+v"(o));
+        __builtin_amdgcn_global_load_lds((const FI_GLOBAL void*)((i < UX ? xb : wb) + (int64_t)k * (U * 16) + o),
+                                         (FI_SHARED void*)(&lds[stage][(i * NTH + wave * kWave) * E]), 16, 0, 0);
     };
     V16 acc[TN][TM] = {};
-    const auto read = [&](Frag (&fw)[TN], Frag (&fx)[TM], int stage, int s) {
-        const uint32_t unit = (2 * s + half) ^ (l32 / 4 % U);
-#pragma unroll
-        for (int i = 0; i < TN; ++i)
-            fw[i] = *smem_ptr(reinterpret_cast<const Frag*>(&lds[stage][((BM + wn + 32 * i + l32) * U + unit) * E]));
-#pragma unroll
-        for (int i = 0; i < TM; ++i)
-            fx[i] = *smem_ptr(reinterpret_cast<const Frag*>(&lds[stage][((wm + 32 * i + l32) * U + unit) * E]));
+    uint32_t lane_at = (l32 * U + (half ^ (l32 / 2 % U))) * 16;   // of part 0's unit in the lane's row
+    // operand r of a part: w's first tile, x's tiles, w's other tiles (the order of their use)
+    const auto read_one = [&](Frag (&fw)[TN], Frag (&fx)[TM], int r, int stage, int s) {
+        const uint32_t at = (lane_at ^ (2 * s * 16)) + stage * (ROWS * U * 16);   // bytes
+        const FI_SHARED char* p = smem_ptr(reinterpret_cast<const char*>(&lds[0][0])) + at;
+        if (r == 0 || r > TM) {
+            const int i = r == 0 ? 0 : r - TM;
+            fw[i] = *reinterpret_cast<const FI_SHARED Frag*>(p + (BM + wn + 32 * i) * U * 16);
+        } else fx[r - 1] = *reinterpret_cast<const FI_SHARED Frag*>(p + (wm + 32 * (r - 1)) * U * 16);
     };
-    // All loads but the newest step's have arrived in LDS and the wave's reads
-    // of LDS are done, in every wave.  (Loads into LDS count as vector memory
-    // operations and complete in order; a fence would wait for all of them.)
-    const auto arrive = [&](bool newest) {
-        if (newest) asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(UN) : "memory");
-        else asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    // The products of one part; behind each goes one read of the next part's
+    // operands, in the first half of them, and (LOAD) a share of the loads of step
+    // `load`: a product takes 32 cycles of the matrix pipe, which the wave's other
+    // instructions fill.
+    const auto part = [&](Frag (&cw)[TN], Frag (&cx)[TM], Frag (&nw)[TN], Frag (&nx)[TM], int stage, int s, auto LOAD, int load) {
+        asm volatile("" : "+v"(lane_at));   // one address a part, not all of them throughout
+        constexpr int P = TM * TN, R = TM + TN, RP = (2 * R + P - 1) / P, FP = (UN + P - 1) / P;
+        dense_mma<BF16, TM, TN>(acc, cw, cx, [&](int p) {
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int r = p * RP; r < (p + 1) * RP && r < R; ++r) read_one(nw, nx, r, stage, s);
+            if constexpr (LOAD)
+#pragma unroll
+                for (int i = p * FP; i < (p + 1) * FP && i < UN; ++i) fetch_one(i, load, stage ^ 1);
+            __builtin_amdgcn_sched_barrier(0);
+        });
     };
+    // The wave's loads have arrived in LDS and its reads of LDS are done, in
+    // every wave.  (Loads into LDS count as vector memory operations.)
+    const auto arrive = [] { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); };
     const int steps = (int)((t.k1 - t.k0) / BK), tail = (int)((t.k1 - t.k0) % BK);
-    if (steps > 0) fetch(0, 0);
-    if (steps > 1) fetch(1, 1);
-    arrive(steps > 1);
+    if (steps > 0)
+#pragma unroll
+        for (int i = 0; i < UN; ++i) fetch_one(i, 0, 0);
+    arrive();
     Frag w0[TN], x0[TM], w1[TN] = {}, x1[TM] = {};
-    int stage = 0;
-    for (int k = 0; k < steps; ++k) {
-        const int next = stage == STAGES - 1 ? 0 : stage + 1;
-        if (k + 2 < steps) fetch(k + 2, next == STAGES - 1 ? 0 : next + 1);   // the buffer of step k - 1
-        read(w0, x0, stage, 0);
-        __builtin_amdgcn_sched_barrier(0);   // the reads go out ahead of the products
-        dense_mma<BF16, TM, TN>(acc, w1, x1);
-        __builtin_amdgcn_sched_barrier(0);
-        read(w1, x1, stage, 1);
-        __builtin_amdgcn_sched_barrier(0);
-        dense_mma<BF16, TM, TN>(acc, w0, x0);
-        __builtin_amdgcn_sched_barrier(0);
-        arrive(k + 2 < steps);
-        stage = next;
+    using std::false_type;
+    using std::true_type;
+    for (int k = 0, stage = 0; k < steps; ++k, stage ^= 1) {
+        // the last part of step k - 1, and the loads of step k + 1 into that
+        // step's buffer (at the end the last step's again: no branch)
+        part(w1, x1, w0, x0, stage, 0, true_type{}, k + 1 < steps ? k + 1 : k);
+        part(w0, x0, w1, x1, stage, 1, false_type{}, 0);
+        part(w1, x1, w0, x0, stage, 2, false_type{}, 0);
+        part(w0, x0, w1, x1, stage, 3, false_type{}, 0);
+        arrive();
     }
-    dense_mma<BF16, TM, TN>(acc, w1, x1);
+    const auto nothing = [](int) {};
+    dense_mma<BF16, TM, TN>(acc, w1, x1, nothing);
     if (tail) {   // the last, shorter step
 #pragma unroll
         for (int i = 0; i < UN; ++i) {
-            const int u = i * NTH + tid, unit = u % U ^ (u / U / 4 % U);
-            const Frag f = load_loose<BF16>(reinterpret_cast<const T*>((i < UX ? xb : wb) + (int64_t)steps * 64 + off[i]), 0, tail - unit * E);
+            const int u = i * NTH + tid, unit = u % U ^ (u / U / 2 % U);
+            const Frag f = load_loose<BF16>(reinterpret_cast<const T*>((i < UX ? xb : wb) + (int64_t)steps * (U * 16) + off[i]), 0, tail - unit * E);
             *smem_ptr(reinterpret_cast<Frag*>(&lds[0][u * E])) = f;
         }
         team_sync();
-        read(w0, x0, 0, 0);
-        read(w1, x1, 0, 1);
-        dense_mma<BF16, TM, TN>(acc, w0, x0);
-        dense_mma<BF16, TM, TN>(acc, w1, x1);
+#pragma unroll 1
+        for (int s = 0; s < U / 2; ++s) {
+#pragma unroll
+            for (int r = 0; r < TM + TN; ++r) read_one(w0, x0, r, 0, s);
+            dense_mma<BF16, TM, TN>(acc, w0, x0, nothing);
+        }
         team_sync();
     }
     dense_results<BF16, TM, TN>(a, t.m0 + wm, t.n0 + wn, t.split, acc,
@@ -235,28 +253,26 @@ __global__ __launch_bounds__(WM* WN * kWave) void k_dense_loose(DenseCall a) {
     const uint32_t l32 = lane % 32, half = lane / 32;
     const int wm = wave / WN * (BM / WM), wn = wave % WN * (BN / WN);
     const Tile<BM, BN> t(a, blockIdx.x);
-    Frag hold[UN];
-    const auto fetch = [&](int64_t k) {
+    const T* row[UN];
 #pragma unroll
-        for (int i = 0; i < UN; ++i) {
-            const int u = i * NTH + tid, unit = u % U ^ (u / U / 2 % U), row = u / U - (i < UX ? 0 : BM);
-            const int64_t r = (i < UX ? t.m0 : t.n0) + row, last = (i < UX ? a.M : a.N) - 1;
-            const T* p = static_cast<const T*>(i < UX ? a.x : a.w) + (r < last ? r : last) * (i < UX ? a.ldx : a.ldw);
-            hold[i] = load_loose<BF16>(p, k + unit * E, t.k1);
-        }
+    for (int i = 0; i < UN; ++i) {
+        const int u = i * NTH + tid;
+        const int64_t r = i < UX ? t.m0 + u / U : t.n0 + u / U - BM, last = (i < UX ? a.M : a.N) - 1;   // rows beyond the end are not stored
+        row[i] = static_cast<const T*>(i < UX ? a.x : a.w) + (r < last ? r : last) * (i < UX ? a.ldx : a.ldw) + t.k0 +
+                 (u % U ^ (u / U / 2 % U)) * E;
+    }
+    using Loose = T __attribute__((ext_vector_type(E), aligned(sizeof(T))));
+    Frag hold[UN];
+    const auto fetch = [&](int k) {   // a whole step: no branch, so that nothing waits for the loads before their use
+#pragma unroll
+        for (int i = 0; i < UN; ++i) hold[i] = *gmem(reinterpret_cast<const Loose*>(row[i] + (int64_t)k * BK));
     };
     const auto settle = [&](int buf) {
 #pragma unroll
         for (int i = 0; i < UN; ++i) *smem_ptr(reinterpret_cast<Frag*>(&lds[buf][(i * NTH + tid) * E])) = hold[i];
     };
     V16 acc[TN][TM] = {};
-    fetch(t.k0);
-    settle(0);
-    int buf = 0;
-    for (int64_t k = t.k0; k < t.k1; k += BK, buf ^= 1) {
-        team_sync();
-        const bool more = k + BK < t.k1;
-        if (more) fetch(k + BK);
+    const auto products = [&](int buf) {
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
             Frag fw[TN], fx[TM];
@@ -267,9 +283,30 @@ __global__ __launch_bounds__(WM* WN * kWave) void k_dense_loose(DenseCall a) {
 #pragma unroll
             for (int i = 0; i < TM; ++i)
                 fx[i] = *smem_ptr(reinterpret_cast<const Frag*>(&lds[buf][((wm + 32 * i + l32) * U + unit) * E]));
-            dense_mma<BF16, TM, TN>(acc, fw, fx);
+            dense_mma<BF16, TM, TN>(acc, fw, fx, [](int) {});
         }
-        if (more) settle(buf ^ 1);
+    };
+    const int steps = (int)((t.k1 - t.k0) / BK), tail = (int)((t.k1 - t.k0) % BK);
+    if (steps > 0) {
+        fetch(0);
+        settle(0);
+        for (int k = 0; k < steps; ++k) {
+            team_sync();
+            fetch(k + 1 < steps ? k + 1 : k);
+            products(k & 1);
+            settle(k & 1 ^ 1);
+        }
+        team_sync();
+    }
+    if (tail) {   // the last, shorter step
+#pragma unroll
+        for (int i = 0; i < UN; ++i) {
+            const int u = i * NTH + tid;
+            hold[i] = load_loose<BF16>(row[i] + (int64_t)steps * BK, 0, tail - (u % U ^ (u / U / 2 % U)) * E);
+        }
+        settle(0);
+        team_sync();
+        products(0);
     }
     team_sync();
     dense_results<BF16, TM, TN>(a, t.m0 + wm, t.n0 + wn, t.split, acc,
@@ -420,8 +457,8 @@ hipError_t run(DenseCall& c, hipStream_t st) {
     }
     if (c.splits == 1) c.part = nullptr;
     if (c.splits > 1 || tiles_of(c.M, c.N, 128, 128) < kCus) tile<BF16, 64, 64, 2, 2>(c, direct, st);
-    else if (!direct || tiles_of(c.M, c.N, 256, 128) < 2 * kCus) tile<BF16, 128, 128, 2, 2>(c, direct, st);
-    else k_dense<BF16, 256, 128, 2, 2><<<(unsigned)tiles_of(c.M, c.N, 256, 128), 4 * kWave, 0, st>>>(c);
+    else if (!direct || tiles_of(c.M, c.N, 256, 256) < kCus) tile<BF16, 128, 128, 2, 2>(c, direct, st);
+    else k_dense<BF16, 256, 256, 2, 4><<<(unsigned)tiles_of(c.M, c.N, 256, 256), 8 * kWave, 0, st>>>(c);
     return hipGetLastError();
 }
 

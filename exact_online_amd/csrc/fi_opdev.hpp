@@ -32,21 +32,21 @@ __device__ __forceinline__ void wave_order() {
 // lam^n = exp(n ld), n >= 0; lam^0 = 1 for lam = 0 (ld = -inf) too
 __device__ __forceinline__ float decay_pow(float ld, float n) { return n == 0.f ? 1.f : expf(n * ld); }
 
-// GELU, v Phi(v) = max(v, 0) - |v| Phi(-|v|), with Phi(-|v|) = erfc(|v| /
-// sqrt 2) / 2 from Abramowitz and Stegun's 7.1.26: erfc(x) = (a1 t + .. + a5
-// t^5) e^{-x^2}, t = 1 / (1 + p x), off by 1.5e-7 at most, so GELU by less
-// than a rounding of |v| to fp32.  Without branches: 13 operations and two of
-// the transcendental unit (the library's erff cost three times that).
+// GELU, v Phi(v) = max(v, 0) - |v| h, h = Phi(-|v|) = erfc(x) / 2 at x = |v| /
+// sqrt 2, with Abramowitz and Stegun's 7.1.26: erfc(x) = (a1 t + .. + a5 t^5)
+// e^{-x^2}, t = 1 / (1 + p x), off by 1.5e-7 at most; with fp32's roundings GELU
+// is off by 3e-7 |v| at most.  Without branches: 12 operations and two of the
+// transcendental unit (the library's erff cost three times that).  |v| is
+// bounded in the last product only: h is 0 there, or NaN with v.
 __device__ __forceinline__ float gelu(float v) {
-    const float x = fminf(fabsf(v), __FLT_MAX__) * 0.70710678118654752f;   // finite: 0 x = 0 below for v = inf
-    const float t = __builtin_amdgcn_rcpf(fmaf(0.3275911f, x, 1.f));
-    const float e = __builtin_amdgcn_exp2f(x * x * -1.4426950408889634f);
-    float q = fmaf(t, 1.061405429f, -1.453152027f);
-    q = fmaf(t, q, 1.421413741f);
-    q = fmaf(t, q, -0.284496736f);
-    q = fmaf(t, q, 0.254829592f);
-    // (x carries 1 / sqrt 2, q t e twice Phi)
-    return fmaf(-0.70710678118654752f * x, q * t * e, fmaxf(v, 0.f)) + (v != v ? v : 0.f);
+    const float t = __builtin_amdgcn_rcpf(fmaf(fabsf(v), 0.3275911f * 0.70710678118654752f, 1.f));
+    const float s = v * 0.84932180028801904f;   // e^{-v^2 / 2} = 2^{-s^2}
+    const float e = __builtin_amdgcn_exp2f(-(s * s));
+    float q = fmaf(t, 0.5f * 1.061405429f, 0.5f * -1.453152027f);
+    q = fmaf(t, q, 0.5f * 1.421413741f);
+    q = fmaf(t, q, 0.5f * -0.284496736f);
+    q = fmaf(t, q, 0.5f * 0.254829592f);
+    return fmaf(-fminf(fabsf(v), 1e6f), q * t * e, fmaxf(v, 0.f));
 }
 
 // tanh |v| = 1 - 2 / (1 + e^{2 |v|}), and for small v, where that cancels, its
