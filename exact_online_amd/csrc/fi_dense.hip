@@ -125,12 +125,12 @@ __device__ __forceinline__ void dense_mma(V16 (&acc)[TN][TM], const typename Mm<
 }
 
 // Rows in whole 16-byte units.  K goes by in steps of 128 bytes of a row (half
-// lines cost the L2 as much as whole ones), loaded straight into one of two
-// LDS buffers, a step ahead; a step has four parts, and the operands of each
+// lines cost the L2 as much as whole ones), loaded straight into one of STAGES
+// LDS buffers, STAGES - 1 steps ahead; a step has four parts, and the operands of each
 // are read during the products of the one before.  A row's eight units are
 // stored at u ^ (row / 2 % 8): the lanes that read one unit of 16 rows then
 // meet every bank once.
-template <bool BF16, int BM, int BN, int WM, int WN>
+template <bool BF16, int BM, int BN, int WM, int WN, int STAGES>
 __global__ __launch_bounds__(WM* WN * kWave, 2) void k_dense(DenseCall a) {
     using M = Mm<BF16>;
     using T = typename M::T;
@@ -139,8 +139,8 @@ __global__ __launch_bounds__(WM* WN * kWave, 2) void k_dense(DenseCall a) {
     constexpr int UX = BM * U / NTH, UN = ROWS * U / NTH;      // units per thread: of x, of both
     constexpr int TM = BM / WM / 32, TN = BN / WN / 32;
     static_assert(UX * NTH == BM * U && UN * NTH == ROWS * U, "every thread loads the same");
-    static_assert(WM * WN * 32 * TN * 32 * 4 <= 2 * ROWS * U * 16, "the waves' results fit");
-    __shared__ __align__(16) T lds[2][ROWS * BK];
+    static_assert(WM * WN * 32 * TN * 32 * 4 <= STAGES * ROWS * U * 16, "the waves' results fit");
+    __shared__ __align__(16) T lds[STAGES][ROWS * BK];
 
     const int tid = threadIdx.x, lane = tid % kWave, wave = __builtin_amdgcn_readfirstlane(tid / kWave);
     const uint32_t l32 = lane % 32, half = lane / 32;
@@ -182,7 +182,7 @@ __global__ __launch_bounds__(WM* WN * kWave, 2) void k_dense(DenseCall a) {
     // operands, in the first half of them, and (LOAD) a share of the loads of step
     // `load`: a product takes 32 cycles of the matrix pipe, which the wave's other
     // instructions fill.
-    const auto part = [&](Frag (&cw)[TN], Frag (&cx)[TM], Frag (&nw)[TN], Frag (&nx)[TM], int stage, int s, auto LOAD, int load) {
+    const auto part = [&](Frag (&cw)[TN], Frag (&cx)[TM], Frag (&nw)[TN], Frag (&nx)[TM], int stage, int s, auto LOAD, int load, int into) {
         asm volatile("" : "+v"(lane_at));   // one address a part, not all of them throughout
         constexpr int P = TM * TN, R = TM + TN, RP = (2 * R + P - 1) / P, FP = (UN + P - 1) / P;
         dense_mma<BF16, TM, TN>(acc, cw, cx, [&](int p) {
@@ -191,29 +191,40 @@ __global__ __launch_bounds__(WM* WN * kWave, 2) void k_dense(DenseCall a) {
             for (int r = p * RP; r < (p + 1) * RP && r < R; ++r) read_one(nw, nx, r, stage, s);
             if constexpr (LOAD)
 #pragma unroll
-                for (int i = p * FP; i < (p + 1) * FP && i < UN; ++i) fetch_one(i, load, stage ^ 1);
+                for (int i = p * FP; i < (p + 1) * FP && i < UN; ++i) fetch_one(i, load, into);
             __builtin_amdgcn_sched_barrier(0);
         });
     };
-    // The wave's loads have arrived in LDS and its reads of LDS are done, in
-    // every wave.  (Loads into LDS count as vector memory operations.)
-    const auto arrive = [] { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); };
+    // The wave's loads but the newest `left` steps' have arrived in LDS and its
+    // reads of LDS are done, in every wave.  (Loads into LDS count as vector
+    // memory operations and complete in order; a fence would wait for all.)
+    const auto arrive = [](auto left) {
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(left * UN) : "memory");
+    };
+    using Some = std::integral_constant<int, STAGES - 2>;
     const int steps = (int)((t.k1 - t.k0) / BK), tail = (int)((t.k1 - t.k0) % BK);
-    if (steps > 0)
-#pragma unroll
-        for (int i = 0; i < UN; ++i) fetch_one(i, 0, 0);
-    arrive();
     Frag w0[TN], x0[TM], w1[TN] = {}, x1[TM] = {};
-    using std::false_type;
-    using std::true_type;
-    for (int k = 0, stage = 0; k < steps; ++k, stage ^= 1) {
-        // the last part of step k - 1, and the loads of step k + 1 into that
-        // step's buffer (at the end the last step's again: no branch)
-        part(w1, x1, w0, x0, stage, 0, true_type{}, k + 1 < steps ? k + 1 : k);
-        part(w0, x0, w1, x1, stage, 1, false_type{}, 0);
-        part(w1, x1, w0, x0, stage, 2, false_type{}, 0);
-        part(w0, x0, w1, x1, stage, 3, false_type{}, 0);
-        arrive();
+    if (steps > 0) {
+        // (beyond the end the last step's loads again: no branch, one count of loads)
+#pragma unroll
+        for (int k = 0; k < STAGES - 1; ++k)
+#pragma unroll
+            for (int i = 0; i < UN; ++i) fetch_one(i, k < steps ? k : steps - 1, k);
+        arrive(Some{});
+        using std::false_type;
+        using std::true_type;
+        int stage = 0, into = STAGES - 1;   // buffers of step k and of the step that is loaded during it
+        for (int k = 0; k < steps; ++k) {
+            // the last part of step k - 1, and loads into that step's buffer
+            part(w1, x1, w0, x0, stage, 0, true_type{}, k + STAGES - 1 < steps ? k + STAGES - 1 : steps - 1, into);
+            part(w0, x0, w1, x1, stage, 1, false_type{}, 0, 0);
+            part(w1, x1, w0, x0, stage, 2, false_type{}, 0, 0);
+            part(w0, x0, w1, x1, stage, 3, false_type{}, 0, 0);
+            arrive(Some{});
+            into = stage;
+            stage = stage == STAGES - 1 ? 0 : stage + 1;
+        }
+        arrive(std::integral_constant<int, 0>{});
     }
     const auto nothing = [](int) {};
     dense_mma<BF16, TM, TN>(acc, w1, x1, nothing);
@@ -262,14 +273,14 @@ __global__ __launch_bounds__(WM* WN * kWave) void k_dense_loose(DenseCall a) {
                  (u % U ^ (u / U / 2 % U)) * E;
     }
     using Loose = T __attribute__((ext_vector_type(E), aligned(sizeof(T))));
-    Frag hold[UN];
-    const auto fetch = [&](int k) {   // a whole step: no branch, so that nothing waits for the loads before their use
+    Frag hold[2][UN];   // two steps in flight
+    const auto fetch = [&](Frag (&h)[UN], int k) {   // a whole step: no branch, so that nothing waits for the loads before their use
 #pragma unroll
-        for (int i = 0; i < UN; ++i) hold[i] = *gmem(reinterpret_cast<const Loose*>(row[i] + (int64_t)k * BK));
+        for (int i = 0; i < UN; ++i) h[i] = *gmem(reinterpret_cast<const Loose*>(row[i] + (int64_t)k * BK));
     };
-    const auto settle = [&](int buf) {
+    const auto settle = [&](const Frag (&h)[UN], int buf) {
 #pragma unroll
-        for (int i = 0; i < UN; ++i) *smem_ptr(reinterpret_cast<Frag*>(&lds[buf][(i * NTH + tid) * E])) = hold[i];
+        for (int i = 0; i < UN; ++i) *smem_ptr(reinterpret_cast<Frag*>(&lds[buf][(i * NTH + tid) * E])) = h[i];
     };
     V16 acc[TN][TM] = {};
     const auto products = [&](int buf) {
@@ -287,14 +298,21 @@ __global__ __launch_bounds__(WM* WN * kWave) void k_dense_loose(DenseCall a) {
         }
     };
     const int steps = (int)((t.k1 - t.k0) / BK), tail = (int)((t.k1 - t.k0) % BK);
+    const auto some = [&](int k) { return k < steps ? k : steps - 1; };
     if (steps > 0) {
-        fetch(0);
-        settle(0);
-        for (int k = 0; k < steps; ++k) {
+        fetch(hold[0], 0);
+        fetch(hold[1], some(1));
+        settle(hold[0], 0);
+        fetch(hold[0], some(2));
+        for (int k = 0; k < steps; k += 2) {
             team_sync();
-            fetch(k + 1 < steps ? k + 1 : k);
-            products(k & 1);
-            settle(k & 1 ^ 1);
+            products(0);
+            settle(hold[1], 1);
+            fetch(hold[1], some(k + 3));
+            team_sync();
+            if (k + 1 < steps) products(1);
+            settle(hold[0], 0);
+            fetch(hold[0], some(k + 4));
         }
         team_sync();
     }
@@ -302,9 +320,9 @@ __global__ __launch_bounds__(WM* WN * kWave) void k_dense_loose(DenseCall a) {
 #pragma unroll
         for (int i = 0; i < UN; ++i) {
             const int u = i * NTH + tid;
-            hold[i] = load_loose<BF16>(row[i] + (int64_t)steps * BK, 0, tail - (u % U ^ (u / U / 2 % U)) * E);
+            hold[0][i] = load_loose<BF16>(row[i] + (int64_t)steps * BK, 0, tail - (u % U ^ (u / U / 2 % U)) * E);
         }
-        settle(0);
+        settle(hold[0], 0);
         team_sync();
         products(0);
     }
@@ -407,10 +425,10 @@ void few(const DenseCall& c, bool direct, hipStream_t st) {
     else k_dense_few<BF16, MT, KW, false><<<grid, WAVES * kWave, 0, st>>>(c);
 }
 
-template <bool BF16, int BM, int BN, int WM, int WN>
+template <bool BF16, int BM, int BN, int WM, int WN, int STAGES>
 void tile(const DenseCall& c, bool direct, hipStream_t st) {
     const unsigned grid = (unsigned)(tiles_of(c.M, c.N, BM, BN) * c.splits);
-    if (direct) k_dense<BF16, BM, BN, WM, WN><<<grid, WM * WN * kWave, 0, st>>>(c);
+    if (direct) k_dense<BF16, BM, BN, WM, WN, STAGES><<<grid, WM * WN * kWave, 0, st>>>(c);
     else k_dense_loose<BF16, BM, BN, WM, WN><<<grid, WM * WN * kWave, 0, st>>>(c);
     if (c.splits > 1)
         k_dense_join<BF16><<<(unsigned)((c.M * (c.ldp / 8) + 255) / 256), 256, 0, st>>>(c);
@@ -456,9 +474,9 @@ hipError_t run(DenseCall& c, hipStream_t st) {
         c.splits = (int)((c.K + c.k_split - 1) / c.k_split);
     }
     if (c.splits == 1) c.part = nullptr;
-    if (c.splits > 1 || tiles_of(c.M, c.N, 128, 128) < kCus) tile<BF16, 64, 64, 2, 2>(c, direct, st);
-    else if (!direct || tiles_of(c.M, c.N, 256, 256) < kCus) tile<BF16, 128, 128, 2, 2>(c, direct, st);
-    else k_dense<BF16, 256, 256, 2, 4><<<(unsigned)tiles_of(c.M, c.N, 256, 256), 8 * kWave, 0, st>>>(c);
+    if (c.splits > 1 || tiles_of(c.M, c.N, 128, 128) < kCus) tile<BF16, 64, 64, 2, 2, 3>(c, direct, st);
+    else if (!direct || tiles_of(c.M, c.N, 256, 256) < kCus) tile<BF16, 128, 128, 2, 2, 2>(c, direct, st);
+    else k_dense<BF16, 256, 256, 2, 4, 2><<<(unsigned)tiles_of(c.M, c.N, 256, 256), 8 * kWave, 0, st>>>(c);
     return hipGetLastError();
 }
 
