@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from pathlib import Path
 
 __all__ = [
@@ -355,11 +356,11 @@ class _Owner:
             pass
 
 
-def _strides(x, width: int, where: str):
-    """A tensor's strides; its last dimension is `width` adjacent elements."""
-    if x.shape[-1] != width or (width > 1 and x.stride(-1) != 1):
-        raise FiError(FI_ERR_INVALID, where)
-    return x.stride()
+def _refuse(where: str):
+    raise FiError(FI_ERR_INVALID, where)
+
+
+_LATTN_ARGS = struct.Struct("@2q" + "P3q" * 4 + "2PqPi4x")   # 4x: the trailing padding
 
 
 class LinearAttention(_Owner):
@@ -374,20 +375,28 @@ class LinearAttention(_Owner):
     def __init__(self, B, L, H, Hkv, dk, dv, log_decay, scale=1.0, io_dtype=FI_BF16, stream=None):
         self.cfg = fi_lattn_config(B=int(B), L=int(L), H=int(H), Hkv=int(Hkv), dk=int(dk), dv=int(dv),
                                    scale=float(scale), io_dtype=int(io_dtype), stream=_stream(stream))
-        self._heads = (int(H), int(dk)), (int(Hkv), int(dk)), (int(Hkv), int(dv)), (int(H), int(dv))
+        self._heads = int(H), int(Hkv), int(dk), int(dv)
+        self._args = fi_lattn_args()
         self.handle = fi_lattn_create(self.cfg, log_decay)
 
     def _call(self, fn, where, q, k, v, o, state, lens, slots, fresh):
-        B, L = q.shape[0], q.shape[1]
-        views = []
-        for x, (heads, size) in zip((q, k, v, o), self._heads):
-            row, pos, head, _ = _strides(x, size, where)
-            if x.shape[:3] != (B, L, heads):
-                raise FiError(FI_ERR_INVALID, where)
-            views.append(fi_view(x.data_ptr(), row, pos, head))
-        a = fi_lattn_args(B, L, *views, _ptr(lens), _ptr(slots), 0 if state is None else state.shape[0], _ptr(state),
-                          1 if fresh else 0)
-        _check(fn(self.handle, a), where)
+        shape = q.shape
+        B, L = shape[0], shape[1]
+        H, Hkv, dk, dv = self._heads
+        qs, ks, vs, os_ = q.stride(), k.stride(), v.stride(), o.stride()
+        if (shape != (B, L, H, dk) or k.shape != (B, L, Hkv, dk) or v.shape != (B, L, Hkv, dv)
+                or o.shape != (B, L, H, dv) or (dk > 1 and (qs[3] != 1 or ks[3] != 1))
+                or (dv > 1 and (vs[3] != 1 or os_[3] != 1))):
+            _refuse(where)
+        # the struct's fields in their order (fi_lattn_args, native layout)
+        _LATTN_ARGS.pack_into(
+            self._args, 0, B, L, q.data_ptr(), qs[0], qs[1], qs[2], k.data_ptr(), ks[0], ks[1], ks[2],
+            v.data_ptr(), vs[0], vs[1], vs[2], o.data_ptr(), os_[0], os_[1], os_[2],
+            0 if lens is None else lens.data_ptr(), 0 if slots is None else slots.data_ptr(),
+            0 if state is None else state.shape[0], 0 if state is None else state.data_ptr(), 1 if fresh else 0)
+        status = fn(self.handle, self._args)
+        if status < 0:
+            raise FiError(status, where)
 
     def prompt(self, q, k, v, o, state=None, lens=None, slots=None, fresh=False):
         self._call(lib.fi_lattn_prompt, "fi_lattn_prompt", q, k, v, o, state, lens, slots, fresh)
@@ -411,11 +420,16 @@ class Dense(_Owner):
     def run(self, x, w, y, bias=None, res=None):
         M, N, K = x.shape[0], self.N, self.K
         where = "fi_dense_run"
-        if w.shape[0] != N or y.shape[0] != M or (res is not None and res.shape[0] != M):
-            raise FiError(FI_ERR_INVALID, where)
-        a = fi_dense_args(M, x.data_ptr(), _strides(x, K, where)[0], w.data_ptr(), _strides(w, K, where)[0], _ptr(bias),
-                          _ptr(res), 0 if res is None else _strides(res, N, where)[0], y.data_ptr(),
-                          _strides(y, N, where)[0])
+        xs, ws, ys = x.stride(), w.stride(), y.stride()
+        if (x.shape != (M, K) or w.shape != (N, K) or y.shape != (M, N) or (K > 1 and (xs[1] != 1 or ws[1] != 1))
+                or (N > 1 and ys[1] != 1)):
+            _refuse(where)
+        ldr = 0
+        if res is not None:
+            ldr, inner = res.stride()
+            if res.shape != (M, N) or (N > 1 and inner != 1):
+                _refuse(where)
+        a = fi_dense_args(M, x.data_ptr(), xs[0], w.data_ptr(), ws[0], _ptr(bias), _ptr(res), ldr, y.data_ptr(), ys[0])
         _check(lib.fi_dense_run(self.handle, a), where)
 
 
@@ -434,8 +448,11 @@ class TokenScores(_Owner):
         self.handle = fi_scores_create(self.cfg)
 
     def run(self, logits, targets=None, logprob=None, entropy=None, top=None, top_id=None, lse=None):
-        a = fi_scores_args(logits.shape[0], logits.data_ptr(), _strides(logits, self.V, "fi_scores_run")[0],
-                           _ptr(targets), _ptr(logprob), _ptr(entropy), _ptr(lse), _ptr(top), _ptr(top_id))
+        rows, ld = logits.shape[0], logits.stride(0)
+        if logits.shape != (rows, self.V) or (self.V > 1 and logits.stride(1) != 1):
+            _refuse("fi_scores_run")
+        a = fi_scores_args(rows, logits.data_ptr(), ld, _ptr(targets), _ptr(logprob), _ptr(entropy), _ptr(lse),
+                           _ptr(top), _ptr(top_id))
         _check(lib.fi_scores_run(self.handle, a), "fi_scores_run")
 
 

@@ -33,7 +33,8 @@ struct LattnCall {
     float *ws;
 };
 
-hipError_t launch_lattn_rec(const LattnCall &c, hipStream_t st);
+// One position (L = 1), recurrent form.
+hipError_t launch_lattn_step(const LattnCall &c, hipStream_t st);
 // Chunked form; sets the call's segments.  ws holds lattn_ws_bytes.
 hipError_t launch_lattn_chunk(LattnCall c, hipStream_t st);
 size_t lattn_ws_bytes(int64_t B, int64_t L, int Hkv, int dk, int dv, int io_bf16);
