@@ -11,6 +11,8 @@ namespace fi {
 
 constexpr int kScThreads = 256, kScWaves = kScThreads / kWave;
 constexpr int kScUnroll = 4;          // 16-byte loads of a lane in one batch
+constexpr int kScBuffer = 96;         // candidates that a wave collects before it ranks them
+constexpr int kScEnough = 32;         // ranked after a batch when there are so many
 constexpr float kScLow = -16384.f;    // 2^kScLow = 0, and 0 kScLow = 0
 constexpr float kScHigh = 16.f;       // t beyond this moves the reference
 constexpr float kLn2 = 0.69314718055994531f, kLog2e = 1.44269504088896341f;
@@ -82,6 +84,100 @@ __device__ __forceinline__ void scores_out(const ScoresCall& a, int64_t r, Stats
     }
 }
 
+// A wave's best k so far, sorted, and the candidates that came after them, in
+// LDS (keys[0 .. 32) and keys[32 ..)).  A lane's 16 bytes with a logit that can
+// still be among the k go into a queue first (the loop over the logits holds
+// only that); the queue's logits are then looked at one a lane, and the
+// candidates ranked by counting what is better: no order of arrival is
+// needed, and nothing is moved one by one.
+template <bool BF16>
+struct Best {
+    using Frag = typename Mm<BF16>::Frag;
+    FI_SHARED Key* keys;
+    FI_SHARED Frag* queue;
+    FI_SHARED uint32_t* ids;   // of the queue's first logits
+    int k, lane;
+    int size, count, queued;   // sorted ones, candidates, queue
+    Key floor;          // candidates exceed this
+    float thr;          // logits of later tokens exceed this (the floor's value)
+
+    __device__ __forceinline__ void rank() {
+        if (!count) return;
+        wave_order();
+        const Key a = lane < size ? keys[lane] : 0, b = lane < count ? keys[kScoresMaxK + lane] : 0,
+                  c = lane + kWave < count ? keys[kScoresMaxK + kWave + lane] : 0;
+        int pa = 0, pb = 0, pc = 0;
+        for (int j = 0; j < size; ++j) {
+            const Key o = keys[j];
+            pa += o > a;
+            pb += o > b;
+            pc += o > c;
+        }
+        for (int j = 0; j < count; ++j) {
+            const Key o = keys[kScoresMaxK + j];
+            pa += o > a;
+            pb += o > b;
+            pc += o > c;
+        }
+        wave_order();
+        if (a && pa < k) keys[pa] = a;
+        if (b && pb < k) keys[pb] = b;
+        if (c && pc < k) keys[pc] = c;
+        wave_order();
+        size = size + count < k ? size + count : k;
+        count = 0;
+        if (size == k) {
+            const Key last = keys[k - 1];
+            const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(last >> 32)),
+                           lo = __builtin_amdgcn_readfirstlane((uint32_t)last);
+            const Key kth = (Key)hi << 32 | lo;
+            if (kth > floor) {
+                floor = kth;
+                thr = value_of(hi);
+            }
+        }
+    }
+    // offers every lane's logit z of token id
+    __device__ __forceinline__ void offer(float z, uint32_t id) {
+        const Key me = key_of(z, id);
+        const bool some = z > -__builtin_inff();   // false for NaN
+        uint64_t m = __ballot(some && me > floor);
+        if (!m) return;
+        if (count + __popcll(m) > kScBuffer) {
+            rank();
+            m = __ballot(some && me > floor);
+        }
+        if (m >> lane & 1) keys[kScoresMaxK + count + __popcll(m & (((uint64_t)1 << lane) - 1))] = me;
+        count += __popcll(m);
+    }
+    __device__ __forceinline__ void drain() {
+        constexpr int E = Mm<BF16>::E;
+        wave_order();
+        for (int i = lane; __builtin_amdgcn_readfirstlane(i) < queued * E; i += kWave) {
+            const bool some = i < queued * E;
+            const FI_SHARED typename Mm<BF16>::T* z = (const FI_SHARED typename Mm<BF16>::T*)queue;
+            offer(some ? (float)z[i] : -__builtin_inff(), some ? ids[i / E] + i % E : 0);
+        }
+        wave_order();
+        queued = 0;
+    }
+    // a lane's logits f from token id, the largest of them z
+    __device__ __forceinline__ void enqueue(const Frag& f, float z, uint32_t id) {
+        uint64_t m = __ballot(z > thr);
+        if (!m) return;
+        if (queued + __popcll(m) > kWave) {
+            drain();
+            m = __ballot(z > thr);
+        }
+        if (m >> lane & 1) {
+            const int at = queued + __popcll(m & (((uint64_t)1 << lane) - 1));
+            queue[at] = f;
+            ids[at] = id;
+        }
+        queued += __popcll(m);
+    }
+};
+
 // A workgroup takes one part of one row, each wave a run of it; one part: the
 // whole row, and the results go out at once.
 template <bool BF16>
@@ -91,8 +187,10 @@ __global__ __launch_bounds__(kScThreads) void k_scores(ScoresCall a) {
     using Frag = typename M::Frag;
     constexpr int E = M::E, STEP = kWave * E, BATCH = kScUnroll * STEP;
     __shared__ Stats wst[kScWaves];
-    __shared__ Key wk[kScWaves][kScoresMaxK], out[kScoresMaxK];
-    const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave, k = a.k;
+    __shared__ Key wk[kScWaves][kScoresMaxK + kScBuffer], out[kScoresMaxK];
+    __shared__ __align__(16) Frag wq[kScWaves][kWave];
+    __shared__ uint32_t wi[kScWaves][kWave];
+    const int tid = threadIdx.x, lane = tid % kWave, wave = __builtin_amdgcn_readfirstlane(tid / kWave), k = a.k;
     const float c = a.scale * kLog2e, inf = __builtin_inff();
     const int64_t r = blockIdx.x / a.parts;
     const int part = blockIdx.x % a.parts;
@@ -102,8 +200,7 @@ __global__ __launch_bounds__(kScThreads) void k_scores(ScoresCall a) {
     if (v1 > a.V) v1 = a.V;
 
     Stats x = {-__FLT_MAX__, 0.f, 0.f};   // m is the wave's, s and w the lane's
-    float lv = -inf, thr = -inf;          // the wave's alternatives, best first, one a lane; what a new one exceeds
-    uint32_t li = 0xFFFFFFFFu;
+    Best<BF16> best = {smem_ptr(wk[wave]), smem_ptr(wq[wave]), smem_ptr(wi[wave]), k, lane, 0, 0, 0, 0, -inf};
     const auto load = [&](Frag* f, int64_t v) {
 #pragma unroll
         for (int u = 0; u < kScUnroll; ++u) {
@@ -148,53 +245,38 @@ __global__ __launch_bounds__(kScThreads) void k_scores(ScoresCall a) {
                 // of the first batch, only what reaches the k-th largest lane or so
                 const uint32_t o = reached_by(ordered(most), k);
                 const float f = value_of(o - (o == 0x80000000u ? 2 : 1));   // the next value below; -0 is 0
-                if (o && f > -inf) thr = f;                                  // false for NaN bits too
+                if (o && f > -inf) {                                        // false for NaN bits too
+                    best.thr = f;
+                    best.floor = ((Key)o << 32) - 1;
+                }
             }
 #pragma unroll
-            for (int u = 0; u < kScUnroll; ++u) {
-                uint64_t lanes = __ballot(big[u] > thr);
-                while (lanes) {   // by index: equal values stay in their order
-                    const int l = __builtin_ctzll(lanes);
-#pragma unroll
-                    for (int e = 0; e < E; ++e) {
-                        const float z = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint((float)now[u][e]), l));
-                        if (z > thr) {
-                            const int at = __popcll(__ballot(lv >= z));
-                            const float pv = wave_shr1(lv);
-                            const uint32_t pi = __builtin_amdgcn_update_dpp(0, (int)li, 0x138, 0xf, 0xf, true);
-                            lv = lane < at ? lv : lane == at ? z : pv;
-                            li = lane < at ? li : lane == at ? (uint32_t)(v + u * STEP + l * E + e) : pi;
-                            const float kth = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(lv), k - 1));
-                            thr = fmaxf(thr, kth);
-                        }
-                    }
-                    lanes &= lanes - 1;
-                    lanes &= __ballot(big[u] > thr);
-                }
+            for (int u = 0; u < kScUnroll; ++u) best.enqueue(now[u], big[u], (uint32_t)(v + u * STEP + lane * E));
+            if (best.queued) {
+                best.drain();
+                if (v == v0 || best.count >= kScEnough) best.rank();
             }
         }
 #pragma unroll
         for (int u = 0; u < kScUnroll; ++u) now[u] = next[u];
     }
+    best.rank();
     x = join_wave(x, c);
     if (lane == 0) wst[wave] = x;
-    if (lane < k) wk[wave][lane] = lv > -inf ? key_of(lv, li) : 0;
+    if (lane >= best.size && lane < k) wk[wave][lane] = 0;
     if (tid < kScoresMaxK) out[tid] = 0;
     __syncthreads();
     if (tid < kScWaves * k) {
         // an alternative's place: how many of each wave's are better
-        const int w = tid / k, j = tid % k;
-        const Key me = wk[w][j];
-        int place = 0;
-        if (me) {
-            for (int o = 0; o < kScWaves; ++o) {
-                int n = 0;
-                for (int b = 32; b; b >>= 1)
-                    if (n + b <= k && wk[o][n + b - 1] > me) n += b;
-                place += n;
-            }
-            if (place < k) out[place] = me;
-        }
+        const Key me = wk[tid / k][tid % k];
+        int n[kScWaves] = {};
+#pragma unroll
+        for (int b = 32; b; b >>= 1)
+#pragma unroll
+            for (int o = 0; o < kScWaves; ++o)
+                if (n[o] + b <= k && wk[o][n[o] + b - 1] > me) n[o] += b;
+        const int place = n[0] + n[1] + n[2] + n[3];
+        if (me && place < k) out[place] = me;
     }
     __syncthreads();
     if (wave) return;
@@ -257,7 +339,7 @@ __global__ __launch_bounds__(kScThreads) void k_scores_join(ScoresCall a) {
 
 namespace {
 
-constexpr int kScWorkgroups = 512;   // wanted of a launch
+constexpr int kScWorkgroups = 1024;  // wanted of a launch: four for each CU
 constexpr int kScMaxParts = 64;      // one wave joins them
 
 // Parts that a row of V logits is split into in a call of `rows`.
