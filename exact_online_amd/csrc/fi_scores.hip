@@ -1,10 +1,10 @@
 // fi_scores.hip -- log probability of a given token, entropy and the most
 // probable tokens of every row of logits (fi_scores_*).
 //
-// One pass keeps, with a reference m near the largest logit and t = (z - m) c,
-// c = scale log2(e): s = sum 2^t and w = sum t 2^t.  Then, in units of log2,
-// lse = c m + log2 s and entropy = log2 s - w / s.  The subtraction comes
-// before the scaling, so large logits lose nothing.
+// One pass keeps, with a reference m near the largest logit, c = scale log2(e),
+// R = m c rounded and t = z c - R (one fused operation, so that large logits
+// lose nothing): s = sum 2^t and w = sum t 2^t.  Then, in units of log2,
+// lse = R + log2 s and entropy = log2 s - w / s.
 #include "fi_opdev.hpp"
 
 namespace fi {
@@ -21,9 +21,27 @@ struct Stats {
     float m, s, w;
 };
 
+// Logits beyond this are taken by differences, since z c would overflow (rows
+// of a type's lowest value alone); below it by their scaled references.
+constexpr float kScHuge = 1e30f;
+// The scaled reference, rounded by itself everywhere (it is what the sums are
+// taken against: m c inside a fused operation would be another number).
+__device__ __forceinline__ float reference(float m, float c) {
+#pragma clang fp contract(off)
+    const float r = m * c;
+    return r;
+}
+__device__ __forceinline__ float scaled(float z, float m, float c) {
+    return fabsf(m) < kScHuge ? fmaf(z, c, -reference(m, c)) : (z - m) * c;
+}
+__device__ __forceinline__ float scaled_ref(float a, float m, float c) {   // of sums by a against those by m
+#pragma clang fp contract(off)
+    return fabsf(a) < kScHuge && fabsf(m) < kScHuge ? reference(a, c) - reference(m, c) : (a - m) * c;
+}
+
 __device__ __forceinline__ Stats join(Stats a, Stats b, float c) {
     const float m = fmaxf(a.m, b.m);
-    const float da = fmaxf((a.m - m) * c, kScLow), db = fmaxf((b.m - m) * c, kScLow);
+    const float da = fmaxf(scaled_ref(a.m, m, c), kScLow), db = fmaxf(scaled_ref(b.m, m, c), kScLow);
     const float ea = exp2f(da), eb = exp2f(db);
     return {m, a.s * ea + b.s * eb, ea * (a.w + da * a.s) + eb * (b.w + db * b.s)};
 }
@@ -63,15 +81,18 @@ template <bool BF16>
 __device__ __forceinline__ void scores_out(const ScoresCall& a, int64_t r, Stats x, Key alt, int lane) {
     const float inf = __builtin_inff(), nan = __builtin_nanf("");
     const bool empty = x.s == 0.f, bad = !(x.s < inf);
-    const float l2 = log2f(x.s), ln = l2 * kLn2;
+    const float c = a.scale * kLog2e, l2 = log2f(x.s);
+    const auto log_p = [&](float z) {
+        return fabsf(z) < kScHuge ? (scaled(z, x.m, c) - l2) * kLn2 : fmaf(z - x.m, a.scale, -l2 * kLn2);
+    };
     if (lane < a.k) {
         float v = -inf;
-        if (alt) v = fmaf(value_of((uint32_t)(alt >> 32)) - x.m, a.scale, -ln);
+        if (alt) v = log_p(value_of((uint32_t)(alt >> 32)));
         a.top[r * a.k + lane] = bad ? nan : v;
         a.top_id[r * a.k + lane] = bad || !alt ? -1 : (int64_t)(uint32_t)~alt;
     }
     if (lane) return;
-    if (a.lse) a.lse[r] = bad ? nan : empty ? -inf : fmaf(x.m, a.scale, ln);
+    if (a.lse) a.lse[r] = bad ? nan : empty ? -inf : fabsf(x.m) < kScHuge ? (reference(x.m, c) + l2) * kLn2 : fmaf(x.m, a.scale, l2 * kLn2);
     if (a.entropy) a.entropy[r] = empty ? 0.f : bad ? nan : (l2 - x.w / x.s) * kLn2;
     if (a.logprob) {
         const int64_t t = a.targets[r];
@@ -79,7 +100,7 @@ __device__ __forceinline__ void scores_out(const ScoresCall& a, int64_t r, Stats
         if (t < 0) lp = 0.f;
         else if (t >= a.V || bad) lp = nan;
         else if (empty) lp = -inf;
-        else lp = fmaf(get_io<BF16>(a.logits, r * a.ld + t) - x.m, a.scale, -ln);
+        else lp = log_p(get_io<BF16>(a.logits, r * a.ld + t));
         a.logprob[r] = lp;
     }
 }
@@ -178,26 +199,24 @@ struct Best {
     }
 };
 
-// A workgroup takes one part of one row, each wave a run of it; one part: the
-// whole row, and the results go out at once.
+// A wave takes one part of one row (four of them make a workgroup, and meet
+// nowhere); one part: the whole row, and the results go out at once.
 template <bool BF16>
 __global__ __launch_bounds__(kScThreads) void k_scores(ScoresCall a) {
     using M = Mm<BF16>;
     using T = typename M::T;
     using Frag = typename M::Frag;
     constexpr int E = M::E, STEP = kWave * E, BATCH = kScUnroll * STEP;
-    __shared__ Stats wst[kScWaves];
-    __shared__ Key wk[kScWaves][kScoresMaxK + kScBuffer], out[kScoresMaxK];
+    __shared__ Key wk[kScWaves][kScoresMaxK + kScBuffer];
     __shared__ __align__(16) Frag wq[kScWaves][kWave];
     __shared__ uint32_t wi[kScWaves][kWave];
-    const int tid = threadIdx.x, lane = tid % kWave, wave = __builtin_amdgcn_readfirstlane(tid / kWave), k = a.k;
+    const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), k = a.k;
     const float c = a.scale * kLog2e, inf = __builtin_inff();
-    const int64_t r = blockIdx.x / a.parts;
-    const int part = blockIdx.x % a.parts;
+    const int64_t unit = (int64_t)blockIdx.x * kScWaves + wave, r = unit / a.parts;
+    if (r >= a.rows) return;
+    const int part = (int)(unit - r * a.parts);
     const T* row = static_cast<const T*>(a.logits) + r * a.ld;
-    const int64_t v0 = (int64_t)part * a.per + wave * (a.per / kScWaves);
-    int64_t v1 = v0 + a.per / kScWaves;
-    if (v1 > a.V) v1 = a.V;
+    const int64_t v0 = (int64_t)part * a.per, v1 = v0 + a.per < a.V ? v0 + a.per : a.V;
 
     Stats x = {-__FLT_MAX__, 0.f, 0.f};   // m is the wave's, s and w the lane's
     Best<BF16> best = {smem_ptr(wk[wave]), smem_ptr(wq[wave]), smem_ptr(wi[wave]), k, lane, 0, 0, 0, 0, -inf};
@@ -213,7 +232,7 @@ __global__ __launch_bounds__(kScThreads) void k_scores(ScoresCall a) {
         }
     };
     Frag now[kScUnroll], next[kScUnroll];
-    if (v0 < v1) load(now, v0);
+    load(now, v0);
     for (int64_t v = v0; v < v1; v += BATCH) {
         if (v + BATCH < v1) load(next, v + BATCH);
         float big[kScUnroll], most = -inf;
@@ -224,22 +243,29 @@ __global__ __launch_bounds__(kScThreads) void k_scores(ScoresCall a) {
             for (int e = 1; e < E; ++e) big[u] = fmaxf(big[u], (float)now[u][e]);
             most = fmaxf(most, big[u]);
         }
-        if (v == v0 || __ballot((most - x.m) * c > kScHigh)) {
+        if (v == v0 || __ballot(scaled(most, x.m, c) > kScHigh)) {
             float m = fmaxf(most, x.m);
             for (int d = 1; d < kWave; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
-            const float t = fmaxf((x.m - m) * c, kScLow), e = exp2f(t);
+            m = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(m)));
+            const float t = fmaxf(scaled_ref(x.m, m, c), kScLow), e = exp2f(t);
             x.w = e * (x.w + t * x.s);
             x.s *= e;
             x.m = m;
         }
+        const auto sums = [&](auto t_of) {
 #pragma unroll
-        for (int u = 0; u < kScUnroll; ++u)
+            for (int u = 0; u < kScUnroll; ++u)
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const float t = ((float)now[u][e] - x.m) * c, p = __builtin_amdgcn_exp2f(t);
-                x.s += p;
-                x.w = fmaf(p, fmaxf(t, kScLow), x.w);   // -inf: 0 (-2^14)
-            }
+                for (int e = 0; e < E; ++e) {
+                    const float t = t_of((float)now[u][e]), p = __builtin_amdgcn_exp2f(t);
+                    x.s += p;
+                    x.w = fmaf(p, fmaxf(t, kScLow), x.w);   // -inf: 0 (-2^14)
+                }
+        };
+        if (fabsf(x.m) < kScHuge) {
+            const float ref = reference(x.m, c);
+            sums([&](float z) { return fmaf(z, c, -ref); });
+        } else sums([&](float z) { return (z - x.m) * c; });
         if (k) {
             if (v == v0) {
                 // of the first batch, only what reaches the k-th largest lane or so
@@ -262,43 +288,24 @@ __global__ __launch_bounds__(kScThreads) void k_scores(ScoresCall a) {
     }
     best.rank();
     x = join_wave(x, c);
-    if (lane == 0) wst[wave] = x;
-    if (lane >= best.size && lane < k) wk[wave][lane] = 0;
-    if (tid < kScoresMaxK) out[tid] = 0;
-    __syncthreads();
-    if (tid < kScWaves * k) {
-        // an alternative's place: how many of each wave's are better
-        const Key me = wk[tid / k][tid % k];
-        int n[kScWaves] = {};
-#pragma unroll
-        for (int b = 32; b; b >>= 1)
-#pragma unroll
-            for (int o = 0; o < kScWaves; ++o)
-                if (n[o] + b <= k && wk[o][n[o] + b - 1] > me) n[o] += b;
-        const int place = n[0] + n[1] + n[2] + n[3];
-        if (me && place < k) out[place] = me;
-    }
-    __syncthreads();
-    if (wave) return;
-    x = wst[0];
-    for (int w = 1; w < kScWaves; ++w) x = join(x, wst[w], c);
-    const Key alt = lane < k ? out[lane] : 0;
+    const Key alt = lane < best.size ? wk[wave][lane] : 0;
     if (a.parts == 1) scores_out<BF16>(a, r, x, alt, lane);
     else {
-        const int64_t at = r * a.parts + part;
         if (lane == 0) {
-            a.pst[at * 3] = x.m;
-            a.pst[at * 3 + 1] = x.s;
-            a.pst[at * 3 + 2] = x.w;
+            a.pst[unit * 3] = x.m;
+            a.pst[unit * 3 + 1] = x.s;
+            a.pst[unit * 3 + 2] = x.w;
         }
-        if (lane < k) a.pkey[at * k + lane] = alt;
+        if (lane < k) a.pkey[unit * k + lane] = alt;
     }
 }
 
-// Joins a row's parts (at most 64).
+// Joins a row's parts (at most two for each lane of a wave).
+constexpr int kScMaxParts = 2 * kWave;
+
 template <bool BF16>
 __global__ __launch_bounds__(kScThreads) void k_scores_join(ScoresCall a) {
-    __shared__ Key got[kWave * kScoresMaxK], out[kScoresMaxK];
+    __shared__ Key got[kScMaxParts * kScoresMaxK], out[kScoresMaxK];
     __shared__ uint32_t least;
     __shared__ int count;
     const int tid = threadIdx.x, lane = tid % kWave, k = a.k;
@@ -306,14 +313,20 @@ __global__ __launch_bounds__(kScThreads) void k_scores_join(ScoresCall a) {
     const float c = a.scale * kLog2e;
     const Key* keys = a.pkey + r * a.parts * k;
     Stats x = {-__FLT_MAX__, 0.f, 0.f};
-    if (tid < kWave && lane < a.parts) {
-        const float* p = a.pst + (r * a.parts + lane) * 3;
-        x = {p[0], p[1], p[2]};
-    }
+    if (tid < kWave)
+        for (int p = lane; p < a.parts; p += kWave) {
+            const float* q = a.pst + (r * a.parts + p) * 3;
+            x = join(x, {q[0], q[1], q[2]}, c);
+        }
     if (k) {
         if (tid < kWave) {
-            // the k-th best of the parts' best ones bounds what can be among the row's k
-            const uint32_t o = reached_by(lane < a.parts ? (uint32_t)(keys[lane * k] >> 32) : 0, k);
+            // the k-th best of the lanes' best ones bounds what can be among the row's k
+            uint32_t head = 0;
+            for (int p = lane; p < a.parts; p += kWave) {
+                const uint32_t h = (uint32_t)(keys[(int64_t)p * k] >> 32);
+                head = head > h ? head : h;
+            }
+            const uint32_t o = reached_by(head, k);
             if (lane == 0) least = o, count = 0;
             if (lane < kScoresMaxK) out[lane] = 0;
         }
@@ -339,14 +352,14 @@ __global__ __launch_bounds__(kScThreads) void k_scores_join(ScoresCall a) {
 
 namespace {
 
-constexpr int kScWorkgroups = 1024;  // wanted of a launch: four for each CU
-constexpr int kScMaxParts = 64;      // one wave joins them
+constexpr int kScPartsWanted = 4096;   // of a launch: four waves for each SIMD
 
-// Parts that a row of V logits is split into in a call of `rows`.
+// Parts that a row of V logits is split into in a call of `rows`: each at
+// least a batch of loads of one wave.
 int parts_of(int64_t rows, int64_t V, int io_bf16, int64_t* per) {
-    const int64_t unit = (int64_t)kScThreads * (io_bf16 ? 8 : 4);   // logits of one load of a workgroup
-    int64_t n = kScWorkgroups / rows;
-    if (n > V / (unit * 2)) n = V / (unit * 2);
+    const int64_t unit = (int64_t)kWave * (io_bf16 ? 8 : 4);   // logits of one load of a wave
+    int64_t n = kScPartsWanted / rows;
+    if (n > V / (unit * kScUnroll)) n = V / (unit * kScUnroll);
     if (n > kScMaxParts) n = kScMaxParts;
     if (n < 1) n = 1;
     *per = ((V + n - 1) / n + unit - 1) / unit * unit;
@@ -357,7 +370,7 @@ int parts_of(int64_t rows, int64_t V, int io_bf16, int64_t* per) {
 
 size_t scores_ws_parts(int64_t rows, int64_t V, int io_bf16) {
     int64_t most = 0, per;
-    for (int64_t r = 1; r <= rows && r <= kScWorkgroups; ++r) {
+    for (int64_t r = 1; r <= rows && r <= kScPartsWanted / 2; ++r) {
         const int n = parts_of(r, V, io_bf16, &per);
         if (n > 1 && r * n > most) most = r * n;
     }
@@ -378,7 +391,7 @@ hipError_t launch_scores(ScoresCall c, hipStream_t st) {
         c.lse = from(all.lse, r);
         c.top = from(all.top, r * c.k);
         c.top_id = from(all.top_id, r * c.k);
-        const unsigned grid = (unsigned)(c.rows * c.parts);   // more than one part only for few rows
+        const unsigned grid = (unsigned)((c.rows * c.parts + kScWaves - 1) / kScWaves);   // several parts only for few rows
         if (c.io_bf16) k_scores<true><<<grid, kScThreads, 0, st>>>(c);
         else k_scores<false><<<grid, kScThreads, 0, st>>>(c);
         if (c.parts > 1) {
