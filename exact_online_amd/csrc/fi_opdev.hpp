@@ -29,6 +29,29 @@ __device__ __forceinline__ void wave_order() {
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
 }
 
+// A wave's sum (largest value) of v, in every lane: neighbours, quads, halves
+// and rows of 16 lanes exchange through the data-parallel moves, the rows'
+// totals through scalars.
+template <int CTRL>
+__device__ __forceinline__ float moved(float v) {
+    return __uint_as_float(__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), CTRL, 0xf, 0xf, true));
+}
+template <class F>
+__device__ __forceinline__ float wave_reduce(float v, F f) {
+    v = f(v, moved<0xB1>(v));    // lanes 1, 0, 3, 2
+    v = f(v, moved<0x4E>(v));    // lanes 2, 3, 0, 1
+    v = f(v, moved<0x141>(v));   // half rows mirrored
+    v = f(v, moved<0x140>(v));   // rows mirrored
+    const auto lane = [&](int l) { return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), l)); };
+    return f(f(lane(0), lane(16)), f(lane(32), lane(48)));
+}
+__device__ __forceinline__ float wave_sum(float v) {
+    return wave_reduce(v, [](float a, float b) { return a + b; });
+}
+__device__ __forceinline__ float wave_max(float v) {
+    return wave_reduce(v, [](float a, float b) { return fmaxf(a, b); });
+}
+
 // lam^n = exp(n ld), n >= 0; lam^0 = 1 for lam = 0 (ld = -inf) too
 __device__ __forceinline__ float decay_pow(float ld, float n) { return n == 0.f ? 1.f : expf(n * ld); }
 

@@ -46,9 +46,14 @@ __device__ __forceinline__ Stats join(Stats a, Stats b, float c) {
     return {m, a.s * ea + b.s * eb, ea * (a.w + da * a.s) + eb * (b.w + db * b.s)};
 }
 
+// the same sums by another reference
+__device__ __forceinline__ Stats moved_to(Stats a, float m, float c) {
+    const float t = fmaxf(scaled_ref(a.m, m, c), kScLow), e = exp2f(t);
+    return {m, a.s * e, e * (a.w + t * a.s)};
+}
 __device__ __forceinline__ Stats join_wave(Stats x, float c) {
-    for (int d = 1; d < kWave; d <<= 1) x = join(x, {__shfl_xor(x.m, d), __shfl_xor(x.s, d), __shfl_xor(x.w, d)}, c);
-    return x;
+    x = moved_to(x, wave_max(x.m), c);
+    return {x.m, wave_sum(x.s), wave_sum(x.w)};
 }
 
 // Alternatives as one number that orders them: the value's bits, then the
@@ -76,9 +81,24 @@ __device__ __forceinline__ uint32_t reached_by(uint32_t o, int k) {
     return lo;
 }
 
-// Writes a row's results; lane j < k of the calling wave has alternative j.
+// The logit of a row's given token (lane 0; asked for early, as it takes two
+// loads one after the other).
+struct Target {
+    int64_t id;
+    float z;
+};
 template <bool BF16>
-__device__ __forceinline__ void scores_out(const ScoresCall& a, int64_t r, Stats x, Key alt, int lane) {
+__device__ __forceinline__ Target target_of(const ScoresCall& a, int64_t r, int lane) {
+    Target t = {-1, 0.f};
+    if (lane == 0 && a.targets) {
+        t.id = a.targets[r];
+        if (t.id >= 0 && t.id < a.V) t.z = get_io<BF16>(a.logits, r * a.ld + t.id);
+    }
+    return t;
+}
+
+// Writes a row's results; lane j < k of the calling wave has alternative j.
+__device__ __forceinline__ void scores_out(const ScoresCall& a, int64_t r, Stats x, Key alt, Target t, int lane) {
     const float inf = __builtin_inff(), nan = __builtin_nanf("");
     const bool empty = x.s == 0.f, bad = !(x.s < inf);
     const float c = a.scale * kLog2e, l2 = log2f(x.s);
@@ -95,12 +115,11 @@ __device__ __forceinline__ void scores_out(const ScoresCall& a, int64_t r, Stats
     if (a.lse) a.lse[r] = bad ? nan : empty ? -inf : fabsf(x.m) < kScHuge ? (reference(x.m, c) + l2) * kLn2 : fmaf(x.m, a.scale, l2 * kLn2);
     if (a.entropy) a.entropy[r] = empty ? 0.f : bad ? nan : (l2 - x.w / x.s) * kLn2;
     if (a.logprob) {
-        const int64_t t = a.targets[r];
         float lp;
-        if (t < 0) lp = 0.f;
-        else if (t >= a.V || bad) lp = nan;
+        if (t.id < 0) lp = 0.f;
+        else if (t.id >= a.V || bad) lp = nan;
         else if (empty) lp = -inf;
-        else lp = log_p(get_io<BF16>(a.logits, r * a.ld + t));
+        else lp = log_p(t.z);
         a.logprob[r] = lp;
     }
 }
@@ -124,22 +143,25 @@ struct Best {
 
     __device__ __forceinline__ void rank() {
         if (!count) return;
+        constexpr int RUN = 8;   // at once; runs are filled up with none
+        if (lane < RUN) keys[kScoresMaxK + count + lane] = 0;
+        if (lane >= size && lane < kScoresMaxK) keys[lane] = 0;
         wave_order();
         const Key a = lane < size ? keys[lane] : 0, b = lane < count ? keys[kScoresMaxK + lane] : 0,
                   c = lane + kWave < count ? keys[kScoresMaxK + kWave + lane] : 0;
         int pa = 0, pb = 0, pc = 0;
-        for (int j = 0; j < size; ++j) {
-            const Key o = keys[j];
-            pa += o > a;
-            pb += o > b;
-            pc += o > c;
-        }
-        for (int j = 0; j < count; ++j) {
-            const Key o = keys[kScoresMaxK + j];
-            pa += o > a;
-            pb += o > b;
-            pc += o > c;
-        }
+        const auto better = [&](int from, int to) {
+            for (int j = from; j < to; j += RUN)
+#pragma unroll
+                for (int u = 0; u < RUN; ++u) {
+                    const Key o = keys[j + u];
+                    pa += o > a;
+                    pb += o > b;
+                    pc += o > c;
+                }
+        };
+        better(0, size);
+        better(kScoresMaxK, kScoresMaxK + count);
         wave_order();
         if (a && pa < k) keys[pa] = a;
         if (b && pb < k) keys[pb] = b;
@@ -207,7 +229,7 @@ __global__ __launch_bounds__(kScThreads) void k_scores(ScoresCall a) {
     using T = typename M::T;
     using Frag = typename M::Frag;
     constexpr int E = M::E, STEP = kWave * E, BATCH = kScUnroll * STEP;
-    __shared__ Key wk[kScWaves][kScoresMaxK + kScBuffer];
+    __shared__ __align__(16) Key wk[kScWaves][kScoresMaxK + kScBuffer + 8];   // (8: the end of a run)
     __shared__ __align__(16) Frag wq[kScWaves][kWave];
     __shared__ uint32_t wi[kScWaves][kWave];
     const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), k = a.k;
@@ -244,13 +266,7 @@ __global__ __launch_bounds__(kScThreads) void k_scores(ScoresCall a) {
             most = fmaxf(most, big[u]);
         }
         if (v == v0 || __ballot(scaled(most, x.m, c) > kScHigh)) {
-            float m = fmaxf(most, x.m);
-            for (int d = 1; d < kWave; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
-            m = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(m)));
-            const float t = fmaxf(scaled_ref(x.m, m, c), kScLow), e = exp2f(t);
-            x.w = e * (x.w + t * x.s);
-            x.s *= e;
-            x.m = m;
+            x = moved_to(x, fmaxf(wave_max(most), x.m), c);
         }
         const auto sums = [&](auto t_of) {
 #pragma unroll
@@ -287,9 +303,10 @@ __global__ __launch_bounds__(kScThreads) void k_scores(ScoresCall a) {
         for (int u = 0; u < kScUnroll; ++u) now[u] = next[u];
     }
     best.rank();
-    x = join_wave(x, c);
+    x.s = wave_sum(x.s);
+    x.w = wave_sum(x.w);
     const Key alt = lane < best.size ? wk[wave][lane] : 0;
-    if (a.parts == 1) scores_out<BF16>(a, r, x, alt, lane);
+    if (a.parts == 1) scores_out(a, r, x, alt, target_of<BF16>(a, r, lane), lane);
     else {
         if (lane == 0) {
             a.pst[unit * 3] = x.m;
@@ -305,49 +322,67 @@ constexpr int kScMaxParts = 2 * kWave;
 
 template <bool BF16>
 __global__ __launch_bounds__(kScThreads) void k_scores_join(ScoresCall a) {
-    __shared__ Key got[kScMaxParts * kScoresMaxK], out[kScoresMaxK];
+    constexpr int MINE = kScMaxParts * kScoresMaxK / kScThreads, RUN = 8;
+    __shared__ __align__(16) Key got[kScMaxParts * kScoresMaxK + RUN];
+    __shared__ Key out[kScoresMaxK];
     __shared__ uint32_t least;
     __shared__ int count;
-    const int tid = threadIdx.x, lane = tid % kWave, k = a.k;
+    __shared__ Target given;
+    const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave, k = a.k, all = a.parts * k;
     const int64_t r = blockIdx.x;
     const float c = a.scale * kLog2e;
-    const Key* keys = a.pkey + r * a.parts * k;
+    const Key* const keys = a.pkey + r * all;
+    // one wave joins the sums and writes the results, another bounds the
+    // alternatives, a third gets the given token's logit
+    Key mine[MINE];
+#pragma unroll
+    for (int i = 0; i < MINE; ++i)
+        if (i * kScThreads < all) mine[i] = i * kScThreads + tid < all ? keys[i * kScThreads + tid] : 0;
     Stats x = {-__FLT_MAX__, 0.f, 0.f};
-    if (tid < kWave)
+    if (wave == 0) {
         for (int p = lane; p < a.parts; p += kWave) {
             const float* q = a.pst + (r * a.parts + p) * 3;
             x = join(x, {q[0], q[1], q[2]}, c);
         }
-    if (k) {
-        if (tid < kWave) {
-            // the k-th best of the lanes' best ones bounds what can be among the row's k
+        x = join_wave(x, c);
+    } else if (wave == 1) {
+        // the k-th best of the lanes' best ones bounds what can be among the row's k
+        if (lane < kScoresMaxK) out[lane] = 0;
+        if (lane == 0) count = 0;
+        if (k) {
             uint32_t head = 0;
             for (int p = lane; p < a.parts; p += kWave) {
-                const uint32_t h = (uint32_t)(keys[(int64_t)p * k] >> 32);
+                const uint32_t h = (uint32_t)(keys[p * k] >> 32);
                 head = head > h ? head : h;
             }
             const uint32_t o = reached_by(head, k);
-            if (lane == 0) least = o, count = 0;
-            if (lane < kScoresMaxK) out[lane] = 0;
+            if (lane == 0) least = o;
         }
-        __syncthreads();
-        for (int i = tid; i < a.parts * k; i += kScThreads) {
-            const Key me = keys[i];
-            if (me && (uint32_t)(me >> 32) >= least) got[atomicAdd(&count, 1)] = me;   // any order: they are ranked
-        }
+    } else if (wave == 2) {
+        const Target t = target_of<BF16>(a, r, lane);
+        if (lane == 0) given = t;
+    }
+    __syncthreads();
+    if (k) {
+#pragma unroll
+        for (int i = 0; i < MINE; ++i)
+            if (i * kScThreads < all && mine[i] && (uint32_t)(mine[i] >> 32) >= least)
+                got[atomicAdd(&count, 1)] = mine[i];   // any order: they are ranked
         __syncthreads();
         const int n = count;
+        if (tid < RUN) got[n + tid] = 0;
+        __syncthreads();
         for (int i = tid; i < n; i += kScThreads) {
             const Key me = got[i];
             int place = 0;
-            for (int j = 0; j < n; ++j) place += got[j] > me;
+            for (int j = 0; j < n; j += RUN)
+#pragma unroll
+                for (int u = 0; u < RUN; ++u) place += got[j + u] > me;
             if (place < k) out[place] = me;
         }
         __syncthreads();
     }
-    if (tid >= kWave) return;
-    x = join_wave(x, c);
-    scores_out<BF16>(a, r, x, lane < k ? out[lane] : 0, lane);
+    if (wave == 0) scores_out(a, r, x, lane < k ? out[lane] : 0, given, lane);
 }
 
 namespace {
