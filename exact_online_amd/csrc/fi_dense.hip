@@ -434,16 +434,43 @@ void tile(const DenseCall& c, bool direct, hipStream_t st) {
         k_dense_join<BF16><<<(unsigned)((c.M * (c.ldp / 8) + 255) / 256), 256, 0, st>>>(c);
 }
 
-constexpr int64_t kFewRows = 32;
-constexpr int64_t kMinSplitK = 256;    // of K, for one part
+// Rows that k_dense_few takes: 16 at any size, and 32 where w is small (32
+// rows, us here / in tiles: 4096 x 1024 6.4 / 7.1, but 2048 x 4096 14.5 / 10.6
+// and 32768 x 1024 24.1 / 16.6: x is read again by every 16 outputs).
+bool few_rows(int64_t M, int64_t N, int64_t K) { return M <= 16 || (M <= 32 && N < 8192 && K <= 2048); }
 
-// parts that K of a product of M rows is split into (tiles of 64 x 64)
+// Parts that K is split into, where tiles of 64 x 64 are fewer than half the
+// CUs: at least 1024 long each, as the join costs what 600 of K do (64 rows by
+// 4096, us whole / in two or four parts: K = 1024 7.5 / 12.5, 2048 11.1 / 11.1,
+// 8192 34 / 19.6; 256 rows by 1024, K = 4096, in parts of 512 14.8, 1024 12.8,
+// 2048 14.6).
+constexpr int64_t kMinSplitK = 1024;
 int64_t splits_of(int64_t M, int64_t N, int64_t K) {
     const int64_t t = tiles_of(M, N, 64, 64);
-    if (M <= kFewRows || 2 * t > kCus) return 1;
+    if (few_rows(M, N, K) || 2 * t > kCus) return 1;
     int64_t n = 2 * kCus / t;
     if (n > K / kMinSplitK) n = K / kMinSplitK;
     return n < 1 ? 1 : n;
+}
+
+// The time of a launch in rounds over the CUs, which hold at most `at_once`
+// workgroups each: a round with i on a CU costs cost[i], measured with K =
+// 1024, in hundredths of bf16's round of 256 x 256 tiles (36 us) and of fp32's
+// two 128 x 128 tiles on a CU (150 us; fp32 keeps the matrix cores busy with one
+// workgroup on a CU).  So bf16's 4096 x 4096 goes by 256 (us by 256 / 128 /
+// 64: 37.6 / 41.7 / 61.0), 2048 x 4096 by 128 (35.0 / 22.5 / 37.4), 1024 x 1024 by
+// 64 (25.7 / 12.7 / 8.3), 3000 x 3000 by 256 (36.6 / 46.4 / 50.3), and fp32's
+// 2048 x 2048 by 128 (240 / 78 / 100), 1777 x 1025 by 64 (242 / 74 / 45).
+int64_t rounds(int64_t tiles, int at_once, const int* cost) {
+    const int64_t round = at_once * kCus, over = tiles % round;
+    return tiles / round * cost[at_once] + cost[(over + kCus - 1) / kCus];
+}
+int best_tile(int64_t M, int64_t N, bool io_bf16, bool direct) {
+    static constexpr int c64[2][4] = {{0, 16, 30, 45}, {0, 22, 26, 34}}, c128[2][3] = {{0, 50, 95}, {0, 42, 58}}, c256[2][2] = {{0, 156}, {0, 100}};
+    const int64_t by64 = rounds(tiles_of(M, N, 64, 64), 3, c64[io_bf16]), by128 = rounds(tiles_of(M, N, 128, 128), 2, c128[io_bf16]),
+                  by256 = rounds(tiles_of(M, N, 256, 256), 1, c256[io_bf16]);
+    if (direct && by256 <= by128 && by256 <= by64) return 256;
+    return by128 <= by64 ? 128 : 64;
 }
 
 template <bool BF16>
@@ -453,19 +480,18 @@ hipError_t run(DenseCall& c, hipStream_t st) {
     const bool direct = whole(c.x, c.ldx) && whole(c.w, c.ldw);
     c.splits = 1;
     c.k_split = c.K;
-    if (c.M <= kFewRows) {
+    if (few_rows(c.M, c.N, c.K)) {
         c.part = nullptr;
         const bool al = direct && c.K % E == 0;
-        const int64_t t = (c.N + 15) / 16;   // 16 outputs each: one wave, or four or sixteen, for some eight waves per CU
-        if (c.M <= 16) {
-            if (t >= 8 * kCus) few<BF16, 1, 1>(c, al, st);
-            else if (t >= 2 * kCus) few<BF16, 1, 4>(c, al, st);
-            else few<BF16, 1, 16>(c, al, st);
-        } else {
-            if (t >= 8 * kCus) few<BF16, 2, 1>(c, al, st);
-            else if (t >= 2 * kCus) few<BF16, 2, 4>(c, al, st);
-            else few<BF16, 2, 16>(c, al, st);
-        }
+        // 16 outputs for one wave, or for four or sixteen where there are fewer than
+        // some eight waves for each CU (one row, us by 1 / 4 / 16: 131072 x 100
+        // 9.2 / 18.0 / -, 32768 x 1024 12.2 / 12.1 / 17.8, 16384 x 1024 7.9 / 6.9 /
+        // 8.9, 4096 x 4096 24.5 / 7.7 / 7.1)
+        const int64_t t = (c.N + 15) / 16;
+        if (c.M > 16) few<BF16, 2, 16>(c, al, st);
+        else if (t >= 8 * kCus) few<BF16, 1, 1>(c, al, st);
+        else if (t >= 2 * kCus) few<BF16, 1, 4>(c, al, st);
+        else few<BF16, 1, 16>(c, al, st);
         return hipGetLastError();
     }
     const int64_t n = splits_of(c.M, c.N, c.K);
@@ -474,9 +500,10 @@ hipError_t run(DenseCall& c, hipStream_t st) {
         c.splits = (int)((c.K + c.k_split - 1) / c.k_split);
     }
     if (c.splits == 1) c.part = nullptr;
-    if (c.splits > 1 || tiles_of(c.M, c.N, 128, 128) < kCus) tile<BF16, 64, 64, 2, 2, 3>(c, direct, st);
-    else if (!direct || tiles_of(c.M, c.N, 256, 256) < kCus) tile<BF16, 128, 128, 2, 2, 2>(c, direct, st);
-    else k_dense<BF16, 256, 256, 2, 4, 2><<<(unsigned)tiles_of(c.M, c.N, 256, 256), 8 * kWave, 0, st>>>(c);
+    const int side = c.splits > 1 ? 64 : best_tile(c.M, c.N, BF16, direct);
+    if (side == 256) k_dense<BF16, 256, 256, 2, 4, 2><<<(unsigned)tiles_of(c.M, c.N, 256, 256), 8 * kWave, 0, st>>>(c);
+    else if (side == 128) tile<BF16, 128, 128, 2, 2, 2>(c, direct, st);
+    else tile<BF16, 64, 64, 2, 2, 3>(c, direct, st);
     return hipGetLastError();
 }
 
