@@ -21,9 +21,6 @@ struct Stats {
     float m, s, w;
 };
 
-// Logits beyond this are taken by differences, since z c would overflow (rows
-// of a type's lowest value alone); below it by their scaled references.
-constexpr float kScHuge = 1e30f;
 // The scaled reference, rounded by itself everywhere (it is what the sums are
 // taken against: m c inside a fused operation would be another number).
 __device__ __forceinline__ float reference(float m, float c) {
@@ -31,12 +28,16 @@ __device__ __forceinline__ float reference(float m, float c) {
     const float r = m * c;
     return r;
 }
+// From 2^24 on R is off m c by more than 1/2, and by more than exp2 can take from 2^31
+// on: such logits are taken by differences, t = (z - m) c, against m c itself.
+__device__ __forceinline__ bool by_reference(float m, float c) { return fabsf(reference(m, c)) < 16777216.f; }
 __device__ __forceinline__ float scaled(float z, float m, float c) {
-    return fabsf(m) < kScHuge ? fmaf(z, c, -reference(m, c)) : (z - m) * c;
+    return by_reference(m, c) ? fmaf(z, c, -reference(m, c)) : (z - m) * c;
 }
 __device__ __forceinline__ float scaled_ref(float a, float m, float c) {   // of sums by a against those by m
 #pragma clang fp contract(off)
-    return fabsf(a) < kScHuge && fabsf(m) < kScHuge ? reference(a, c) - reference(m, c) : (a - m) * c;
+    if (by_reference(a, c)) return by_reference(m, c) ? reference(a, c) - reference(m, c) : fmaf(-m, c, reference(a, c));
+    return by_reference(m, c) ? fmaf(a, c, -reference(m, c)) : (a - m) * c;
 }
 
 __device__ __forceinline__ Stats join(Stats a, Stats b, float c) {
@@ -102,8 +103,9 @@ __device__ __forceinline__ void scores_out(const ScoresCall& a, int64_t r, Stats
     const float inf = __builtin_inff(), nan = __builtin_nanf("");
     const bool empty = x.s == 0.f, bad = !(x.s < inf);
     const float c = a.scale * kLog2e, l2 = log2f(x.s);
-    const auto log_p = [&](float z) {
-        return fabsf(z) < kScHuge ? (scaled(z, x.m, c) - l2) * kLn2 : fmaf(z - x.m, a.scale, -l2 * kLn2);
+    const auto log_p = [&](float z) {   // (a type's lowest value overflows in units of log2)
+        const float t = scaled(z, x.m, c);
+        return fabsf(t) < 1e30f ? (t - l2) * kLn2 : fmaf(z - x.m, a.scale, -l2 * kLn2);
     };
     if (lane < a.k) {
         float v = -inf;
@@ -112,7 +114,7 @@ __device__ __forceinline__ void scores_out(const ScoresCall& a, int64_t r, Stats
         a.top_id[r * a.k + lane] = bad || !alt ? -1 : (int64_t)(uint32_t)~alt;
     }
     if (lane) return;
-    if (a.lse) a.lse[r] = bad ? nan : empty ? -inf : fabsf(x.m) < kScHuge ? (reference(x.m, c) + l2) * kLn2 : fmaf(x.m, a.scale, l2 * kLn2);
+    if (a.lse) a.lse[r] = bad ? nan : empty ? -inf : by_reference(x.m, c) ? (reference(x.m, c) + l2) * kLn2 : fmaf(x.m, a.scale, l2 * kLn2);
     if (a.entropy) a.entropy[r] = empty ? 0.f : bad ? nan : (l2 - x.w / x.s) * kLn2;
     if (a.logprob) {
         float lp;
@@ -278,7 +280,7 @@ __global__ __launch_bounds__(kScThreads) void k_scores(ScoresCall a) {
                     x.w = fmaf(p, fmaxf(t, kScLow), x.w);   // -inf: 0 (-2^14)
                 }
         };
-        if (fabsf(x.m) < kScHuge) {
+        if (by_reference(x.m, c)) {
             const float ref = reference(x.m, c);
             sums([&](float z) { return fmaf(z, c, -ref); });
         } else sums([&](float z) { return (z - x.m) * c; });

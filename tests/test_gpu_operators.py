@@ -402,7 +402,8 @@ def check_scores(logits, targets, k, dtype, scale=1.0, pad=0, shift=0):
     def near(got, want, a, b, what):
         got, want = got.cpu().double(), want
         assert torch.equal(torch.isnan(got), torch.isnan(want)), what
-        f = torch.isfinite(want)
+        f = torch.isfinite(want.float())   # a value beyond fp32's range is infinite in an fp32 output
+        want = torch.where(f, want, want.float().double())
         assert torch.equal(got[~f & ~torch.isnan(want)], want[~f & ~torch.isnan(want)]), what
         assert bool(((got - want).abs()[f] <= a + b * want.abs()[f]).all()), (what, float((got - want).abs()[f].max()))
     near(lp, rlp, 8e-6, 1e-6, "logprob")
@@ -484,6 +485,26 @@ def test_scores_large_logits():
     z, t = logits_of(23, 4, 2500, spread=1.0)
     check_scores(z * 0.25 + 1.0e4, t, 9, "f32")
     check_scores(z * 40.0 - 3.0e4, t, 9, "f32")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V", [700, 40000])
+@pytest.mark.parametrize("size, scale", [(1.0e7, 1.0), (2.0e7, 1.0), (1.0e10, 1.0), (1.0e17, 1.0), (1.0e29, 1.0), (1.0e38, 1.0),
+                                         (100.0, 1.0e8), (1.0e-3, 1.0e20)])
+def test_scores_huge_logits(V, size, scale, dtype):
+    """Scaled logits beyond the whole numbers of fp32, up to its largest, of
+    either sign, with the largest three times in two of the rows; in the last
+    row only the part of the largest is huge."""
+    g = torch.Generator().manual_seed(77)
+    z = torch.randn(5, V, generator=g).clamp(-3.0, 3.0) * size
+    z[1] = -z[1].abs() - size / 8
+    for r in (0, 1):
+        z[r, [V // 3, V // 2, V - 2]] = z[r].max()
+    z[4] = torch.randn(V, generator=g) / scale
+    z[4, 2 * V // 3] = size
+    t = torch.randint(0, V, (5,), generator=g)
+    t[0], t[4] = V // 2, 2 * V // 3
+    check_scores(z, t, 6, dtype, scale=scale)
 
 
 def test_scores_left_out_outputs():
