@@ -370,10 +370,12 @@ __global__ __launch_bounds__((KW > 4 ? KW : 4) * kWave) void k_dense_few(DenseCa
         xin[i] = 16 * i + l16 < a.M;
         x[i] = static_cast<const T*>(a.x) + (xin[i] ? 16 * i + l16 : 0) * a.ldx;
     }
+    // whole units only: the one that K ends inside comes after the loop
+    using Loose = T __attribute__((ext_vector_type(M::E), aligned(sizeof(T))));
     const auto load = [&](const T* p, int64_t k, bool in) -> Frag {
-        if (!in) return Frag{};
-        if constexpr (ALIGNED) return k < a.K ? *gmem(reinterpret_cast<const Frag*>(p + k)) : Frag{};   // K is whole units
-        else return load_loose<BF16>(p, k, a.K);
+        using Unit = std::conditional_t<ALIGNED, Frag, Loose>;
+        if (in && k + M::E <= a.K) return *gmem(reinterpret_cast<const Unit*>(p + k));
+        return Frag{};
     };
     V4 acc[MT] = {};
     const int64_t steps = (a.K + M::KB - 1) / M::KB, s0 = steps * part / KW, s1 = steps * (part + 1) / KW;
@@ -392,6 +394,18 @@ __global__ __launch_bounds__((KW > 4 ? KW : 4) * kWave) void k_dense_few(DenseCa
 #pragma unroll
                 for (int i = 0; i < MT; ++i) acc[i] = M::mma(fw[u], fx[u][i], acc[i]);
         }
+    if (!ALIGNED && a.K % M::E && part == KW - 1 && n0 < a.N) {
+        const int64_t k = a.K / M::E * M::E;
+        const bool here = k % M::KB / M::E == g;   // the lanes whose unit it is
+        Frag fw = {};
+        if (here) fw = load_loose<BF16>(w, k, a.K);
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+            Frag fx = {};
+            if (here && xin[i]) fx = load_loose<BF16>(x[i], k, a.K);
+            acc[i] = M::mma(fw, fx, acc[i]);
+        }
+    }
     if constexpr (KW > 1) {
 #pragma unroll
         for (int i = 0; i < MT; ++i) red[wave][i][lane] = acc[i];
@@ -440,16 +454,18 @@ void tile(const DenseCall& c, bool direct, hipStream_t st) {
 bool few_rows(int64_t M, int64_t N, int64_t K) { return M <= 16 || (M <= 32 && N < 8192 && K <= 2048); }
 
 // Parts that K is split into, where tiles of 64 x 64 are fewer than half the
-// CUs: at least 1024 long each, as the join costs what 600 of K do (64 rows by
-// 4096, us whole / in two or four parts: K = 1024 7.5 / 12.5, 2048 11.1 / 11.1,
-// 8192 34 / 19.6; 256 rows by 1024, K = 4096, in parts of 512 14.8, 1024 12.8,
-// 2048 14.6).
-constexpr int64_t kMinSplitK = 1024;
-int64_t splits_of(int64_t M, int64_t N, int64_t K) {
+// CUs: at least 1024 long each (fp32, whose products take eight times as long,
+// 256), as the join costs as much as some 600 of bf16's K.  us, 64 rows by
+// 4096, bf16, whole / in parts: K = 1024 7.5 / 12.5, 2048 11.1 / 11.1, 8192 34 /
+// 19.6; 256 rows by 1024, bf16, K = 4096, parts of 512 / 1024 / 2048: 14.8 / 12.8 /
+// 14.6; 200 rows by 1000, fp32, K = 1000, parts of 128 / 256 / whole: 16.5 / 15.1 /
+// 25.2; 41 rows by 256, fp32, K = 3904, parts of 256 / 512 / 1024: 15.2 / 19.1 / 32.6.
+int64_t splits_of(int64_t M, int64_t N, int64_t K, bool io_bf16) {
     const int64_t t = tiles_of(M, N, 64, 64);
     if (few_rows(M, N, K) || 2 * t > kCus) return 1;
     int64_t n = 2 * kCus / t;
-    if (n > K / kMinSplitK) n = K / kMinSplitK;
+    const int64_t most = K / (io_bf16 ? 1024 : 256);
+    if (n > most) n = most;
     return n < 1 ? 1 : n;
 }
 
@@ -494,7 +510,7 @@ hipError_t run(DenseCall& c, hipStream_t st) {
         else few<BF16, 1, 16>(c, al, st);
         return hipGetLastError();
     }
-    const int64_t n = splits_of(c.M, c.N, c.K);
+    const int64_t n = splits_of(c.M, c.N, c.K, BF16);
     if (n > 1) {
         c.k_split = ((c.K + n - 1) / n + BK - 1) / BK * BK;
         c.splits = (int)((c.K + c.k_split - 1) / c.k_split);
@@ -509,10 +525,10 @@ hipError_t run(DenseCall& c, hipStream_t st) {
 
 }  // namespace
 
-size_t dense_ws_bytes(int64_t M, int64_t N, int64_t K) {
+size_t dense_ws_bytes(int64_t M, int64_t N, int64_t K, int io_bf16) {
     int64_t most = 0;
     for (int64_t m = 64; m - 63 <= M; m += 64) {   // the parts depend on the number of tile rows
-        const int64_t rows = m < M ? m : M, n = splits_of(rows, N, K);
+        const int64_t rows = m < M ? m : M, n = splits_of(rows, N, K, io_bf16);
         if (tiles_of(m, N, 64, 64) * 2 > kCus) break;
         if (n > 1 && n * rows > most) most = n * rows;
     }

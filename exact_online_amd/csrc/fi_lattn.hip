@@ -154,9 +154,9 @@ __global__ __launch_bounds__(la_threads(DVS), DK == 256 ? 2 : 4) void k_lattn_ch
 
     const int tid = threadIdx.x, lane = tid % kWave, wave = __builtin_amdgcn_readfirstlane(tid / kWave);
     uint32_t l16 = (uint32_t)lane % 16, g = (uint32_t)lane / 16;
-    const int slices = (a.dv + DVS - 1) / DVS, tasks = a.B * a.Hkv;
-    // the slices of one segment read the same Q and K: eight workgroups apart, on one XCD and its L2
-    const int unit = blockIdx.x / (8 * slices) * 8 + blockIdx.x % 8, slice = blockIdx.x / 8 % slices;
+    const int slices = (a.dv + DVS - 1) / DVS, tasks = a.B * a.Hkv, shares = OUT ? slices * a.hsplit : slices;
+    // the slices (and shares of query heads) of one segment read the same Q and K: eight workgroups apart, on one XCD and its L2
+    const int unit = blockIdx.x / (8 * shares) * 8 + blockIdx.x % 8, share = blockIdx.x / 8 % shares, slice = share % slices;
     if (unit >= tasks * a.nseg) return;
     const int seg = unit / tasks, task = unit % tasks, b = task / a.Hkv, n = task % a.Hkv, col0 = slice * DVS;
     const int dk = a.dk, dv = a.dv;
@@ -169,6 +169,8 @@ __global__ __launch_bounds__(la_threads(DVS), DK == 256 ? 2 : 4) void k_lattn_ch
     int c1 = c0 + a.seg_chunks;
     if (c1 > chunks) c1 = chunks;
     if (!OUT && c1 >= chunks) return;   // a row's last segment hands nothing on
+    const int per = OUT ? (a.G + a.hsplit - 1) / a.hsplit : 0, h0 = share / slices * per, h1 = h0 + per < a.G ? h0 + per : a.G;
+    if (OUT && h0 >= h1) return;
 
     if (OUT) {   // o is zero past the row's end
         const int64_t z1 = seg == a.nseg - 1 ? a.L : (int64_t)(c0 + a.seg_chunks) * C < a.L ? (c0 + a.seg_chunks) * C : a.L;
@@ -176,13 +178,13 @@ __global__ __launch_bounds__(la_threads(DVS), DK == 256 ? 2 : 4) void k_lattn_ch
         constexpr int Z = VEC ? E : 1, UNITS = DVS / Z;   // elements of a store, stores of a row
         const int col = col0 + tid % UNITS * Z;
         if (col < dv)
-            for (int h = n * a.G; h < (n + 1) * a.G; ++h)
+            for (int h = n * a.G + h0; h < n * a.G + h1; ++h)
                 for (int64_t t = z0 + tid / UNITS; t < z1; t += NTH / UNITS) {
                     T* const p = static_cast<T*>(a.o.p) + b * a.o.row + t * a.o.pos + h * a.o.head + col;
                     if constexpr (VEC) *gmem(reinterpret_cast<Frag*>(p)) = Frag{};
                     else *gmem(p) = (T)0.f;
                 }
-        if (c0 >= chunks && !(seg == 0 && in)) return;
+        if (c0 >= chunks && !(seg == 0 && in && h0 == 0)) return;
     }
 
     // the lane's part of S: rows 16 kt + row0 + r of column scol
@@ -192,6 +194,10 @@ __global__ __launch_bounds__(la_threads(DVS), DK == 256 ? 2 : 4) void k_lattn_ch
     float* const wp = a.nseg > 1 ? a.ws + ((int64_t)task * a.nseg + seg) * dk * dv : nullptr;
     const float* const from = !OUT ? nullptr : wp ? wp : a.fresh ? nullptr : sp;
     const bool full = dk == DK && col0 + DVS <= dv;   // no part of S lies outside
+    // Some of the wave's columns are there; a wave without any leaves the matrix
+    // cores to the others (38 -> 26 us, 12 heads of 192 x 32, fp32, 85 positions; in
+    // slices of 64 columns the question costs more than it gives).
+    const bool active = DVS <= 64 || col0 + 16 * wave < dv;
     if (from) {
         const int row0 = 4 * g, scol = col0 + 16 * wave + (int)l16;
         if (full) {
@@ -226,7 +232,7 @@ __global__ __launch_bounds__(la_threads(DVS), DK == 256 ? 2 : 4) void k_lattn_ch
     const int klcol = kin ? kcol : 0, vlcol = vin ? vcol : 0;
     const T* const kp = static_cast<const T*>(a.k.p) + b * a.k.row + n * a.k.head;
     const T* const vp = static_cast<const T*>(a.v.p) + b * a.v.row + n * a.v.head + col0;
-    const T* const qp = static_cast<const T*>(a.q.p) + b * a.q.row + (int64_t)n * a.G * a.q.head;
+    const T* const qp = static_cast<const T*>(a.q.p) + b * a.q.row + ((int64_t)n * a.G + h0) * a.q.head;
     Frag fk[UK], fv[UV], fq[UK];
     // VEC: a chunk of rows spans less than 2^31 bytes, so that a place is a
     // wave's own base and a lane's 32-bit offset
@@ -331,8 +337,8 @@ __global__ __launch_bounds__(la_threads(DVS), DK == 256 ? 2 : 4) void k_lattn_ch
         fetch(fk, kp, a.k.pos, ahead, krow, RK, klcol, kleft);
         if constexpr (!OUT) fetch(fv, vp, a.v.pos, ahead, vrow, RV, vlcol, vleft);
         if constexpr (OUT) {
-            for (int h = 0; h < a.G; ++h) {
-                const bool last = h + 1 == a.G;
+            for (int h = h0; h < h1; ++h) {
+                const bool last = h + 1 == h1;
                 asm volatile("" : "+v"(l16), "+v"(g));
                 // P^T, tiles of 16 keys x 16 queries, jt <= it, shared out among the waves
 #pragma unroll
@@ -343,9 +349,10 @@ __global__ __launch_bounds__(la_threads(DVS), DK == 256 ? 2 : 4) void k_lattn_ch
                     const uint32_t krow_ = BF16 ? 8 * (l16 / 8) + 2 * (l16 % 4) + l16 / 4 % 2 : l16;
                     V4 p = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                    for (int kb = 0; kb < DK / KB; ++kb)
+                    for (int kb = 0; kb < DK / KB; ++kb) {
                         p = M::mma(pair_frag(ks + (16 * jt + krow_) * PK + kb * KB + 4 * g),
                                    row_frag(qs + mixed(DK / E, 16 * it + l16, kb * 4 + g)), p);
+                    }
                     const auto to = [&](int tile) {   // of four of the wave's 16 keys
                         return smem_ptr(reinterpret_cast<Four*>(ps + mixed(C / E, 16 * it + l16, (16 * tile + 4 * g) / E) + 4 * g % E));
                     };
@@ -372,6 +379,7 @@ __global__ __launch_bounds__(la_threads(DVS), DK == 256 ? 2 : 4) void k_lattn_ch
                 V4 O[CT] = {};
 #pragma unroll
                 for (int kb = 0; kb < DK / KB; ++kb) {
+                    if (!active) break;
                     Frag fs;
 #pragma unroll
                     for (int e = 0; e < E; ++e) fs[e] = (T)S[kb * (KB / 16) + e / 4][e % 4];
@@ -382,7 +390,7 @@ __global__ __launch_bounds__(la_threads(DVS), DK == 256 ? 2 : 4) void k_lattn_ch
                     __builtin_amdgcn_sched_barrier(0);
                 }
                 // (loads in three places: each waits for the address path otherwise)
-                fetch(fq, qp + (last ? 0 : h + 1) * a.q.head, a.q.pos, last ? ahead : c, krow, RK, klcol, kleft);
+                fetch(fq, qp + (last ? 0 : h + 1 - h0) * a.q.head, a.q.pos, last ? ahead : c, krow, RK, klcol, kleft);
                 // lam^{i + 1}, counted from the row's first position in a first chunk
 #pragma unroll
                 for (int it = 0; it < CT; ++it) {
@@ -392,6 +400,7 @@ __global__ __launch_bounds__(la_threads(DVS), DK == 256 ? 2 : 4) void k_lattn_ch
                 __syncthreads();
 #pragma unroll
                 for (int kb = 0; kb < C / KB; ++kb) {
+                    if (!active) break;
                     const Frag v = transposed(vs, PV, kb * KB, 16 * wave);
 #pragma unroll
                     for (int it = kb * KB / 16; it < CT; ++it)   // queries before every key of the block: nothing
@@ -435,6 +444,7 @@ __global__ __launch_bounds__(la_threads(DVS), DK == 256 ? 2 : 4) void k_lattn_ch
             for (int r = 0; r < 4; ++r) S[kt][r] = fmaf(d, S[kt][r], S[kt][r]);
 #pragma unroll
         for (int kb = 0; kb < C / KB; ++kb) {
+            if (!active) break;
             __builtin_amdgcn_sched_barrier(0);
             const Frag v = transposed(vs, PV, kb * KB, 16 * wave);
             float w[E];   // of the operand's positions
@@ -472,12 +482,14 @@ __global__ __launch_bounds__(la_threads(DVS), DK == 256 ? 2 : 4) void k_lattn_ch
 #pragma unroll
                 for (int e = 0; e < E; ++e) x[e] = v[e] * w[e];
 #pragma unroll
-                for (int kt = 0; kt < KT; ++kt) S[kt] = M::mma(transposed(ks, PK, kb * KB, 16 * kt), x, S[kt]);
+                for (int kt = 0; kt < KT; ++kt) {
+                    S[kt] = M::mma(transposed(ks, PK, kb * KB, 16 * kt), x, S[kt]);
+                }
             }
         }
         __syncthreads();
     }
-    float* to = OUT ? (c1 == chunks ? sp : nullptr) : wp + (int64_t)dk * dv;
+    float* to = OUT ? (c1 == chunks && h0 == 0 ? sp : nullptr) : wp + (int64_t)dk * dv;
     if (!to) return;
     // the lane's place anew: nothing of the loads above is kept through the loop
     int row0 = 4 * g, scol = col0 + 16 * wave + (int)l16;
@@ -555,13 +567,20 @@ void chunk_launches(const LattnCall& c, hipStream_t st) {
         k_lattn_chunk<BF16, DK, DVS, false, VEC><<<grid, la_threads(DVS), 0, st>>>(c);
         k_lattn_scan<BF16><<<(unsigned)(c.B * c.Hkv * ((c.dk * c.dv + 255) / 256)), 256, 0, st>>>(c);
     }
-    k_lattn_chunk<BF16, DK, DVS, true, VEC><<<grid, la_threads(DVS), 0, st>>>(c);
+    k_lattn_chunk<BF16, DK, DVS, true, VEC><<<grid * c.hsplit, la_threads(DVS), 0, st>>>(c);
 }
 
 template <bool BF16>
 hipError_t chunk_dims(LattnCall& c, hipStream_t st) {
-    const int cols = slice_cols(c.dk);
-    c.nseg = segments(c.B * c.Hkv, (c.dv + cols - 1) / cols, (c.L + la_chunk(BF16) - 1) / la_chunk(BF16), &c.seg_chunks);
+    const int cols = slice_cols(c.dk), slices = (c.dv + cols - 1) / cols;
+    c.nseg = segments(c.B * c.Hkv, slices, (c.L + la_chunk(BF16) - 1) / la_chunk(BF16), &c.seg_chunks);
+    // A group's query heads go to workgroups of their own where the CUs are not
+    // full without: each forms the state for itself, and the first writes it (so
+    // not where the others may still read it: one segment from a given state).
+    // 32 heads on 8 of 128 x 128, one row, us without / with: 512 positions 62 / 32,
+    // 2048 65 / 37.
+    const int64_t wgs = c.B * c.Hkv * c.nseg * slices, n = c.fresh || c.nseg > 1 ? kLaWorkgroups / (wgs > 0 ? wgs : 1) : 1;
+    c.hsplit = n < 1 ? 1 : n < c.G ? (int)n : c.G;
     if (c.dk <= 64) c.vec ? chunk_launches<BF16, 64, 64, true>(c, st) : chunk_launches<BF16, 64, 64, false>(c, st);
     else if (c.dk <= 128) c.vec ? chunk_launches<BF16, 128, 128, true>(c, st) : chunk_launches<BF16, 128, 128, false>(c, st);
     else c.vec ? chunk_launches<BF16, 256, 128, true>(c, st) : chunk_launches<BF16, 256, 128, false>(c, st);

@@ -197,7 +197,7 @@ int fi_dense_create(const fi_dense_config *cfg, fi_dense **out) {
     s->cfg = *cfg;
     s->stream = static_cast<hipStream_t>(cfg->stream);
     s->part = nullptr;
-    const size_t ws = dense_ws_bytes(cfg->M, cfg->N, cfg->K);
+    const size_t ws = dense_ws_bytes(cfg->M, cfg->N, cfg->K, raw_int(cfg->io_dtype) == FI_BF16);
     const hipError_t e = ws > 0 ? dalloc(&s->part, ws) : hipSuccess;
     if (e != hipSuccess) {
         delete s;

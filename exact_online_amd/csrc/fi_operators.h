@@ -31,6 +31,7 @@ struct LattnCall {
     // ws[B Hkv][nseg][dk][dv] where there is more than one
     int nseg, seg_chunks;
     float *ws;
+    int hsplit;                 // workgroups that share out a group's query heads
 };
 
 // One position (L = 1), recurrent form.
@@ -57,7 +58,7 @@ struct DenseCall {
 
 // Chooses the kernel and the split; c.part holds dense_ws_bytes of the handle's M, N, K.
 hipError_t launch_dense(DenseCall c, hipStream_t st);
-size_t dense_ws_bytes(int64_t M, int64_t N, int64_t K);
+size_t dense_ws_bytes(int64_t M, int64_t N, int64_t K, int io_bf16);
 
 // ------------------------------------------------------------ token scores
 constexpr int kScoresMaxK = 32;

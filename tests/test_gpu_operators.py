@@ -487,6 +487,15 @@ def test_scores_large_logits():
     check_scores(z * 40.0 - 3.0e4, t, 9, "f32")
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("fresh", [True, False])
+@pytest.mark.parametrize("B,L,H,Hkv,dk,dv", [(2, 40, 320, 64, 8, 24), (3, 600, 14, 2, 24, 40), (2, 300, 15, 3, 96, 40), (1, 530, 7, 1, 200, 140)])
+def test_prompt_shared_heads(B, L, H, Hkv, dk, dv, fresh, dtype):
+    """Groups whose query heads go to several workgroups, also in shares that
+    are not equal; rows that end early or hold nothing."""
+    check_lattn(lattn_inputs(61, B, L, H, Hkv, dk, dv, dtype), dtype, lens=[L // 3, 0, L][:B], fresh=fresh)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("V", [700, 40000])
 @pytest.mark.parametrize("size, scale", [(1.0e7, 1.0), (2.0e7, 1.0), (1.0e10, 1.0), (1.0e17, 1.0), (1.0e29, 1.0), (1.0e38, 1.0),
