@@ -2,6 +2,7 @@
 //
 // Per row b, key/value head n and position t, lam = exp(ld[n]):
 //     S[t] = lam S[t-1] + k[t] v[t]^T,   o[t][h] = scale S[t]^T q[t][h].
+#include <algorithm>
 #include <type_traits>
 
 #include "fi_opdev.hpp"
@@ -191,7 +192,7 @@ __global__ __launch_bounds__(la_threads(DVS), DK == 256 ? 2 : 4) void k_lattn_ch
     const float ld = a.ld[n];
     V4 S[KT] = {};
     float* const sp = a.state && in ? a.state + (slot * a.Hkv + n) * dk * (int64_t)dv : nullptr;
-    float* const wp = a.nseg > 1 ? a.ws + ((int64_t)task * a.nseg + seg) * dk * dv : nullptr;
+    float* const wp = a.entries ? a.ws + ((int64_t)task * a.nseg + seg) * dk * dv : nullptr;
     const float* const from = !OUT ? nullptr : wp ? wp : a.fresh ? nullptr : sp;
     const bool full = dk == DK && col0 + DVS <= dv;   // no part of S lies outside
     // Some of the wave's columns are there; a wave without any leaves the matrix
@@ -544,29 +545,43 @@ __global__ __launch_bounds__(256) void k_lattn_scan(LattnCall a) {
 
 namespace {
 
-constexpr int kLaWorkgroups = 512;   // wanted of a launch: two for each CU
-constexpr int kLaMinChunks = 4;      // of a segment
+constexpr int kLaWorkgroups = 512;   // wanted of a launch: two for each CU (16 heads of 65536: 416 us, with 1024 447)
+constexpr int kLaWhole = 4;          // chunks of a row that is not split
+
+// Most segments of a row.  Each chunk of a segment takes its time twice (some 5 us
+// in all), each segment its part of the scan (0.15 us): chunks per segment near
+// the root of chunks / 32 (2 heads of 80 x 96, two rows of 2976, us with at least 4
+// / 2 / 1 chunks a segment: 40 / 30 / 26; 2 heads of 96 x 96, one row of 16384, 4 / 1:
+// 49 / 58).
+int64_t chunks_each(int64_t chunks) {
+    int64_t each = 1;
+    while (32 * each * each < chunks) ++each;
+    return each;
+}
+int64_t most_segments(int64_t chunks) { return chunks <= kLaWhole ? 1 : chunks / chunks_each(chunks); }
 
 int slice_cols(int dk) { return dk <= 64 ? 64 : 128; }
 
 // segments that a call of `tasks` rows and heads is split into
 int segments(int64_t tasks, int slices, int chunks, int* seg_chunks) {
     int64_t n = kLaWorkgroups / (tasks * slices);
-    if (n > chunks / kLaMinChunks) n = chunks / kLaMinChunks;
+    if (n > most_segments(chunks)) n = most_segments(chunks);
     if (n < 1) n = 1;
-    *seg_chunks = (int)((chunks + n - 1) / n);
+    *seg_chunks = chunks ? (int)((chunks + n - 1) / n) : 1;
     return chunks ? (chunks + *seg_chunks - 1) / *seg_chunks : 1;
 }
+
+// workgroups that share out a group's query heads in a launch of so many without
+int64_t head_shares(int64_t wgs) { return wgs < kLaWorkgroups ? kLaWorkgroups / (wgs > 0 ? wgs : 1) : 1; }
 
 template <bool BF16, int DK, int DVS, bool VEC>
 void chunk_launches(const LattnCall& c, hipStream_t st) {
     const int slices = (c.dv + DVS - 1) / DVS;
     const int64_t units = c.B * c.Hkv * c.nseg;
     const unsigned grid = (unsigned)((units + 7) / 8 * 8 * slices);
-    if (c.nseg > 1) {
-        k_lattn_chunk<BF16, DK, DVS, false, VEC><<<grid, la_threads(DVS), 0, st>>>(c);
+    if (c.nseg > 1) k_lattn_chunk<BF16, DK, DVS, false, VEC><<<grid, la_threads(DVS), 0, st>>>(c);
+    if (c.entries)
         k_lattn_scan<BF16><<<(unsigned)(c.B * c.Hkv * ((c.dk * c.dv + 255) / 256)), 256, 0, st>>>(c);
-    }
     k_lattn_chunk<BF16, DK, DVS, true, VEC><<<grid * c.hsplit, la_threads(DVS), 0, st>>>(c);
 }
 
@@ -575,12 +590,14 @@ hipError_t chunk_dims(LattnCall& c, hipStream_t st) {
     const int cols = slice_cols(c.dk), slices = (c.dv + cols - 1) / cols;
     c.nseg = segments(c.B * c.Hkv, slices, (c.L + la_chunk(BF16) - 1) / la_chunk(BF16), &c.seg_chunks);
     // A group's query heads go to workgroups of their own where the CUs are not
-    // full without: each forms the state for itself, and the first writes it (so
-    // not where the others may still read it: one segment from a given state).
-    // 32 heads on 8 of 128 x 128, one row, us without / with: 512 positions 62 / 32,
-    // 2048 65 / 37.
-    const int64_t wgs = c.B * c.Hkv * c.nseg * slices, n = c.fresh || c.nseg > 1 ? kLaWorkgroups / (wgs > 0 ? wgs : 1) : 1;
-    c.hsplit = n < 1 ? 1 : n < c.G ? (int)n : c.G;
+    // full without; each forms the state for itself, from the entry states' copy,
+    // and the first writes it.  (A copy for this alone pays where every head gets
+    // its own: 16 heads of 256 x 192 with 3 each, six given states, 16 positions: 33
+    // us without, 70 with.)  32 heads on 8 of 128 x 128, one row of 512: 62 us
+    // without, 32 with.
+    const int64_t n = head_shares(c.B * c.Hkv * c.nseg * slices);
+    c.hsplit = n >= c.G ? c.G : c.fresh || c.nseg > 1 ? (int)n : 1;
+    c.entries = c.nseg > 1 || (c.hsplit > 1 && !c.fresh);
     if (c.dk <= 64) c.vec ? chunk_launches<BF16, 64, 64, true>(c, st) : chunk_launches<BF16, 64, 64, false>(c, st);
     else if (c.dk <= 128) c.vec ? chunk_launches<BF16, 128, 128, true>(c, st) : chunk_launches<BF16, 128, 128, false>(c, st);
     else c.vec ? chunk_launches<BF16, 256, 128, true>(c, st) : chunk_launches<BF16, 256, 128, false>(c, st);
@@ -589,16 +606,14 @@ hipError_t chunk_dims(LattnCall& c, hipStream_t st) {
 
 }  // namespace
 
-size_t lattn_ws_bytes(int64_t B, int64_t L, int Hkv, int dk, int dv, int io_bf16) {
+size_t lattn_ws_bytes(int64_t B, int64_t L, int H, int Hkv, int dk, int dv, int io_bf16) {
     const int C = la_chunk(io_bf16), cols = slice_cols(dk), slices = (dv + cols - 1) / cols;
-    int64_t most = 0;   // states of any call's segments; a call of n rows is split into at most kLaWorkgroups / n
+    // most segments of any row: the longest's, or those of the longest with fewer chunks in each
+    const int64_t chunks = (L + C - 1) / C, split = std::max(most_segments(chunks), 32 * (chunks_each(chunks) - 1));
+    int64_t most = 0;   // states of any call: one of b rows has at most cap segments a row
     for (int64_t b = 1; b <= B && b * Hkv * slices <= kLaWorkgroups; ++b) {
-        int sc;
-        // a shorter call has no more segments than its chunks give
-        int64_t n = segments(b * Hkv, slices, (int)((L + C - 1) / C), &sc);
-        const int64_t cap = kLaWorkgroups / (b * Hkv * slices);
-        if (n > 1 || L >= 2 * kLaMinChunks * C) n = cap < L / (kLaMinChunks * C) + 1 ? cap : L / (kLaMinChunks * C) + 1;
-        if (n > 1 && b * Hkv * n > most) most = b * Hkv * n;
+        const int64_t cap = kLaWorkgroups / (b * Hkv * slices), n = std::min(cap, split);
+        if ((n > 1 || (H > Hkv && head_shares(b * Hkv * slices) > 1)) && b * Hkv * n > most) most = b * Hkv * n;
     }
     return (size_t)most * dk * dv * sizeof(float);
 }

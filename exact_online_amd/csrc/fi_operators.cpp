@@ -88,7 +88,7 @@ int fi_lattn_create(const fi_lattn_config *cfg, const float *log_decay, fi_lattn
     if (e == hipSuccess) e = hipMemcpyAsync(s->ld, log_decay, bytes, hipMemcpyDeviceToDevice, s->stream);
     if (e == hipSuccess) e = hipMemcpyAsync(host, log_decay, bytes, hipMemcpyDeviceToHost, s->stream);
     if (e == hipSuccess) e = hipStreamSynchronize(s->stream);
-    const size_t ws = lattn_ws_bytes(cfg->B, cfg->L, (int)cfg->Hkv, (int)cfg->dk, (int)cfg->dv,
+    const size_t ws = lattn_ws_bytes(cfg->B, cfg->L, (int)cfg->H, (int)cfg->Hkv, (int)cfg->dk, (int)cfg->dv,
                                      raw_int(cfg->io_dtype) == FI_BF16);
     if (e == hipSuccess && ws > 0) e = dalloc(&s->ws, ws);
     bool ok = e == hipSuccess;

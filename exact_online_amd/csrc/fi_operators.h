@@ -27,9 +27,9 @@ struct LattnCall {
     View q, k, v, o;
     const int32_t *lens, *slots;
     float *state;
-    // the chunked form: segments of seg_chunks chunks, and their entry states
-    // ws[B Hkv][nseg][dk][dv] where there is more than one
-    int nseg, seg_chunks;
+    // the chunked form: segments of seg_chunks chunks, and (`entries`) their entry
+    // states ws[B Hkv][nseg][dk][dv]
+    int nseg, seg_chunks, entries;
     float *ws;
     int hsplit;                 // workgroups that share out a group's query heads
 };
@@ -38,7 +38,7 @@ struct LattnCall {
 hipError_t launch_lattn_step(const LattnCall &c, hipStream_t st);
 // Chunked form; sets the call's segments.  ws holds lattn_ws_bytes.
 hipError_t launch_lattn_chunk(LattnCall c, hipStream_t st);
-size_t lattn_ws_bytes(int64_t B, int64_t L, int Hkv, int dk, int dv, int io_bf16);
+size_t lattn_ws_bytes(int64_t B, int64_t L, int H, int Hkv, int dk, int dv, int io_bf16);
 
 // ------------------------------------------------------------ dense product
 // most M and N: a launch has at most 2^32 threads

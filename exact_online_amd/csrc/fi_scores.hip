@@ -348,16 +348,19 @@ __global__ __launch_bounds__(kScThreads) void k_scores_join(ScoresCall a) {
         }
         x = join_wave(x, c);
     } else if (wave == 1) {
-        // the k-th best of the lanes' best ones bounds what can be among the row's k
+        // With the parts' j-th best keys, j = ceil(k / parts), the ceil(k / j)-th of
+        // them bounds what can be among the row's k: that many parts have j keys
+        // as large (95 rows of 54733, k = 32: 37 us, with the best keys alone 39).
         if (lane < kScoresMaxK) out[lane] = 0;
         if (lane == 0) count = 0;
         if (k) {
             uint32_t head = 0;
+            const int j = (k + a.parts - 1) / a.parts;
             for (int p = lane; p < a.parts; p += kWave) {
-                const uint32_t h = (uint32_t)(keys[p * k] >> 32);
+                const uint32_t h = (uint32_t)(keys[p * k + j - 1] >> 32);
                 head = head > h ? head : h;
             }
-            const uint32_t o = reached_by(head, k);
+            const uint32_t o = reached_by(head, (k + j - 1) / j);
             if (lane == 0) least = o;
         }
     } else if (wave == 2) {
@@ -389,7 +392,10 @@ __global__ __launch_bounds__(kScThreads) void k_scores_join(ScoresCall a) {
 
 namespace {
 
-constexpr int kScPartsWanted = 4096;   // of a launch: four waves for each SIMD
+// Waves wanted of a launch: two for each SIMD.  us with 4096 / 2048 / 1024, bf16: 1099
+// rows of 9067, k = 5: 18.1 / 17.0 / 16.5; 333 of 100003: 28.8 / 30.9 / 38.3, and with
+// k = 32 54.6 / 46.9 / 52.6; 95 of 54733, k = 0: 10.0 / 9.0 / 8.5.
+constexpr int kScPartsWanted = 2048;
 
 // Parts that a row of V logits is split into in a call of `rows`: each at
 // least a batch of loads of one wave.
