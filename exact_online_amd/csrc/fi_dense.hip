@@ -130,6 +130,16 @@ __device__ __forceinline__ void dense_mma(V16 (&acc)[TN][TM], const typename Mm<
 // are read during the products of the one before.  A row's eight units are
 // stored at u ^ (row / 2 % 8): the lanes that read one unit of 16 rows then
 // meet every bank once.
+//
+// bf16, 256 x 256: 8192^3 888 us (1240 TFLOP/s, the library's 1411), 16384 x 4096
+// x 1024 157 us, and 180 to 192 with bias and GELU.  The product itself keeps the
+// matrix cores as busy as the power limit leaves them (clock 1.5 to 1.9 GHz);
+// then a tile's end, which the next tile of the CU waits for: stores (128 KB of
+// every CU at once: 7 us), GELU (14 operations and two transcendental ones for each
+// output: 9 us a tile).  256 x 128 with steps of 64 bytes in three stages: 990
+// TFLOP/s at 8192^3; 128 x 128, two on a CU: 1065, and 207 us (216 with GELU, which
+// it hides) at 16384 x 4096 x 1024.  64 x 64 takes three stages, as its steps are
+// short against the loads' way (1000^3: 9.2 us with two, 8.3 with three).
 template <bool BF16, int BM, int BN, int WM, int WN, int STAGES>
 __global__ __launch_bounds__(WM* WN * kWave, 2) void k_dense(DenseCall a) {
     using M = Mm<BF16>;
@@ -249,7 +259,10 @@ __global__ __launch_bounds__(WM* WN * kWave, 2) void k_dense(DenseCall a) {
 }
 
 // Rows at any alignment: K in steps of 128 bytes through registers into two
-// LDS buffers (a row's eight units at u ^ (row / 2 % 8)).
+// LDS buffers (a row's eight units at u ^ (row / 2 % 8)).  Two steps are in flight
+// in registers (one: 53 us where this takes 41 to 47, 1777 x 1025 x 999, fp32, with bias and
+// residual; 88 of fp32's 154 TFLOP/s: with 476 tiles a CU has one or two, and
+// their start and end show).
 template <bool BF16, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(WM* WN * kWave) void k_dense_loose(DenseCall a) {
     using M = Mm<BF16>;
@@ -350,7 +363,10 @@ __global__ __launch_bounds__(256) void k_dense_join(DenseCall a) {
 
 // ------------------------------------------------------------ few rows
 // Up to 16 MT rows of x: w goes by once, from memory to the matrix cores'
-// operands; KW waves of a workgroup split K of 16 outputs between them.
+// operands; KW waves of a workgroup split K of 16 outputs between them.  Bound
+// by w: one row, 32768 x 1024, bf16: 11.9 us (5.6 TB/s: some of w is still in the
+// last-level cache), 131072 x 1024: 40 us (6.7 TB/s).  Eight steps' loads (four with
+// sixteen waves) are in flight at once.
 template <bool BF16, int MT, int KW, bool ALIGNED>
 __global__ __launch_bounds__((KW > 4 ? KW : 4) * kWave) void k_dense_few(DenseCall a) {
     using M = Mm<BF16>;

@@ -14,6 +14,11 @@ namespace fi {
 // c) = (tid / 8, tid % 8) the columns 4c .. 4c+3 of the slice and the rows r,
 // r + 32, ...: columns of S never meet, so slices need no exchange, and rows
 // of the slice are whole lines of memory.
+// Bound by the state, read and written once: 200 rows x 8 heads of 128 x 128
+// (214 MB with q, k, v and o, 32 query heads) take 41 to 47 us, 4.6 to 5.3 TB/s,
+// what a large copy reaches (4.9); 71 us before the state's loads were 16 bytes
+// each and all asked for before the position's own arrive.  One row: 3.8 us, a
+// launch and two trips to memory.
 constexpr int kRecThreads = 256;
 constexpr int kRecCols = 32;
 constexpr int kRecRows = kRecThreads / (kRecCols / 4);   // rows in one sweep
@@ -138,6 +143,30 @@ hipError_t launch_lattn_step(const LattnCall& c, hipStream_t st) {
 //     S = lam^C E + K^T diag(lam^{C-1-j}) V
 // A row's first chunk is filled from the back (zero rows in front), so that
 // every later one is whole and ends on the row's last position.
+//
+// Long rows of few heads are split into segments: OUT = false forms every
+// segment's state from zero, k_lattn_scan joins them into the states before the
+// segments, OUT = true starts from those.  That reads K and V twice; carrying
+// the state from segment to segment instead would leave a row to its slices.
+//
+// Split: a wave's columns of S stay in its registers from chunk to chunk, and
+// S is the operand of both of its products as it lies there; the waves meet
+// only in P, whose tiles they share out.  Waves with 32 columns (operands used
+// twice, half the waves) took 303 us where these take 297, and 132 where these
+// take 91 (ragged rows, four heads a group).
+//
+// Roundings (bf16): P and, as operand of Q E, E are rounded to bf16 once;
+// o is then off by 0.0026 of its norm, of which its own rounding is 0.0017.
+// (Both in two parts: 0.0017, for 20% of the time.)  V's decayed rows go into
+// S in three parts, exactly, so that S keeps fp32's precision over any number
+// of chunks.
+//
+// Measured: 16 heads of 128 x 128, 65536 positions, bf16: 400 us (1.07 GB once:
+// 2.7 TB/s): local states 130, scan 15, outputs 255 to 297.  The outputs keep
+// the vector units busy 42%, LDS 35% and the matrix cores 28% of the time with 3.2
+// waves a SIMD: bound by the chain of a chunk (operands to LDS, P, O, S, four
+// barriers), which two workgroups on a CU overlap.  fp32, two rows of 4001, 16
+// heads of 64 x 64: 60 us, outputs 41, bound by the same chain (matrix cores 40%).
 constexpr int la_chunk(bool bf16) { return bf16 ? 64 : 32; }   // positions of a chunk
 constexpr int la_threads(int dvs) { return dvs / 16 * kWave; }
 

@@ -224,7 +224,16 @@ struct Best {
 };
 
 // A wave takes one part of one row (four of them make a workgroup, and meet
-// nowhere); one part: the whole row, and the results go out at once.
+// nowhere); one part: the whole row, and the results go out at once.  A row's
+// reductions then cost one wave's steps, once: with a workgroup to a row 4096 x
+// 32768 took 76 us.
+//
+// Measured, bf16: 4096 x 32768, k = 5: 62 us (268 MB, 4.3 TB/s; a copy's 4.9 would take
+// 55), the vector units 64% busy with an exponential, two fused operations and
+// a maximum for each logit; 333 x 100003, nine in ten masked, k = 8: 31 us (67 MB), 26 in
+// this kernel, where some ten batches a wave do not hide its beginning
+// (threshold, first ranking) and end.  fp32, one row of 131072, k = 20: 6.4 us here,
+// 4.7 in the join: two launches and their trips to memory.
 template <bool BF16>
 __global__ __launch_bounds__(kScThreads) void k_scores(ScoresCall a) {
     using M = Mm<BF16>;
@@ -319,7 +328,9 @@ __global__ __launch_bounds__(kScThreads) void k_scores(ScoresCall a) {
     }
 }
 
-// Joins a row's parts (at most two for each lane of a wave).
+// Joins a row's parts (at most two for each lane of a wave): 4.6 us, a launch
+// and its trips to memory; all keys are asked for before the bound on them is
+// known.
 constexpr int kScMaxParts = 2 * kWave;
 
 template <bool BF16>
