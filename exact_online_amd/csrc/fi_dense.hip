@@ -488,21 +488,34 @@ int64_t splits_of(int64_t M, int64_t N, int64_t K, bool io_bf16) {
 // The time of a launch in rounds over the CUs, which hold at most `at_once`
 // workgroups each: a round with i on a CU costs cost[i], measured with K =
 // 1024, in hundredths of bf16's round of 256 x 256 tiles (36 us) and of fp32's
-// two 128 x 128 tiles on a CU (150 us; fp32 keeps the matrix cores busy with one
-// workgroup on a CU).  So bf16's 4096 x 4096 goes by 256 (us by 256 / 128 /
-// 64: 37.6 / 41.7 / 61.0), 2048 x 4096 by 128 (35.0 / 22.5 / 37.4), 1024 x 1024 by
-// 64 (25.7 / 12.7 / 8.3), 3000 x 3000 by 256 (36.6 / 46.4 / 50.3), and fp32's
-// 2048 x 2048 by 128 (240 / 78 / 100), 1777 x 1025 by 64 (242 / 74 / 45).
-int64_t rounds(int64_t tiles, int at_once, const int* cost) {
-    const int64_t round = at_once * kCus, over = tiles % round;
-    return tiles / round * cost[at_once] + cost[(over + kCus - 1) / kCus];
-}
-int best_tile(int64_t M, int64_t N, bool io_bf16, bool direct) {
-    static constexpr int c64[2][4] = {{0, 16, 30, 45}, {0, 22, 26, 34}}, c128[2][3] = {{0, 50, 95}, {0, 42, 58}}, c256[2][2] = {{0, 156}, {0, 100}};
-    const int64_t by64 = rounds(tiles_of(M, N, 64, 64), 3, c64[io_bf16]), by128 = rounds(tiles_of(M, N, 128, 128), 2, c128[io_bf16]),
-                  by256 = rounds(tiles_of(M, N, 256, 256), 1, c256[io_bf16]);
-    if (direct && by256 <= by128 && by256 <= by64) return 256;
-    return by128 <= by64 ? 128 : 64;
+// two 128 x 128 tiles on a CU (150 us; fp32 keeps the matrix cores busy with
+// fewer).  us by 256 x 256 / 128 x 128 / 128 x 64 / 64 x 64: bf16 4096 x 4096 37.6 / 41.7 /
+// - / 61.0, 2048 x 4096 35.0 / 22.5 / 32.0 / 37.4, 2048 x 2048 27.7 / 15.1 / 13.6 / 19.0, 1024 x
+// 1024 25.7 / 12.7 / 12.1 / 8.8, 3000 x 3000 36.6 / 46.4 / 42.1 / 50.3; fp32 2048 x 2048 240 / 74.5 /
+// 77.8 / 92.8, 2500 x 1500 245 / 75.6 / 71.7 / 88.3, 1777 x 1025 241 / 71.3 / 44.8 / 44.2.
+// (Unaligned rows go by 128 x 128 and 64 x 64 only: bf16's 2048 x 2048 x 1023 28.0 /
+// 33.1 / 43.9 from 128 x 128 on.)
+struct TileSize {
+    int m, n, at_once, cost[2][4];   // of fp32, of bf16
+};
+constexpr TileSize kTiles[] = {{64, 64, 3, {{0, 17, 28, 40}, {0, 22, 27, 38}}},
+                               {128, 128, 2, {{0, 50, 93}, {0, 42, 58}}},
+                               {128, 64, 3, {{0, 29, 52, 70}, {0, 30, 38, 62}}},
+                               {256, 256, 1, {{0, 156}, {0, 100}}}};
+int best_tile(int64_t M, int64_t N, bool io_bf16, bool direct) {   // the largest of the cheapest
+    int best = 0;
+    int64_t least = INT64_MAX;
+    for (int i = 0; i < (direct ? 4 : 2); ++i) {
+        const TileSize& t = kTiles[i];
+        const int* cost = t.cost[io_bf16];
+        const int64_t tiles = tiles_of(M, N, t.m, t.n), round = t.at_once * kCus;
+        const int64_t all = tiles / round * cost[t.at_once] + cost[(tiles % round + kCus - 1) / kCus];
+        if (all <= least) {
+            least = all;
+            best = i;
+        }
+    }
+    return best;
 }
 
 template <bool BF16>
@@ -532,10 +545,12 @@ hipError_t run(DenseCall& c, hipStream_t st) {
         c.splits = (int)((c.K + c.k_split - 1) / c.k_split);
     }
     if (c.splits == 1) c.part = nullptr;
-    const int side = c.splits > 1 ? 64 : best_tile(c.M, c.N, BF16, direct);
-    if (side == 256) k_dense<BF16, 256, 256, 2, 4, 2><<<(unsigned)tiles_of(c.M, c.N, 256, 256), 8 * kWave, 0, st>>>(c);
-    else if (side == 128) tile<BF16, 128, 128, 2, 2, 2>(c, direct, st);
-    else tile<BF16, 64, 64, 2, 2, 3>(c, direct, st);
+    switch (c.splits > 1 ? 0 : best_tile(c.M, c.N, BF16, direct)) {
+        case 0: tile<BF16, 64, 64, 2, 2, 3>(c, direct, st); break;
+        case 1: tile<BF16, 128, 128, 2, 2, 2>(c, direct, st); break;
+        case 2: k_dense<BF16, 128, 64, 2, 2, 2><<<(unsigned)tiles_of(c.M, c.N, 128, 64), 4 * kWave, 0, st>>>(c); break;
+        default: k_dense<BF16, 256, 256, 2, 4, 2><<<(unsigned)tiles_of(c.M, c.N, 256, 256), 8 * kWave, 0, st>>>(c);
+    }
     return hipGetLastError();
 }
 

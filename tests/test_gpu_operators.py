@@ -354,6 +354,15 @@ def test_dense_strides(M, N, K, pad, shift, io, out):
     check_dense(M * pad, M, N, K, io, out, "gelu", bias=True, res=True, pad=pad, shift=shift)
 
 
+@pytest.mark.parametrize("io,M,N,K", [
+    ("bf16", 4090, 4050, 72), ("f32", 4090, 4050, 36), ("bf16", 2048, 4090, 200), ("f32", 2040, 2048, 100),      # tiles of 256, of 128
+    ("bf16", 1024, 4090, 136), ("f32", 3606, 1071, 68), ("bf16", 2047, 4100, 75), ("f32", 2047, 2050, 37),       # 128 x 64; unaligned
+    ("bf16", 64, 512, 4160), ("bf16", 200, 300, 3071), ("f32", 64, 260, 2100), ("f32", 40, 1000, 1027),          # parts of K
+    ("bf16", 17, 9000, 264), ("bf16", 32, 500, 2056), ("f32", 25, 8200, 101), ("bf16", 16, 33000, 71)])          # few rows, either way
+def test_dense_every_route(io, M, N, K):
+    check_dense(M + K, M, N, K, io, io, "gelu", bias=True, res=True)
+
+
 def test_dense_fewer_rows_than_the_config():
     x, w = torch.randn(4, 32, device="cuda"), torch.randn(16, 32, device="cuda")
     y = torch.full((4, 16), 9.0, device="cuda")
@@ -494,6 +503,13 @@ def test_prompt_shared_heads(B, L, H, Hkv, dk, dv, fresh, dtype):
     """Groups whose query heads go to several workgroups, also in shares that
     are not equal; rows that end early or hold nothing."""
     check_lattn(lattn_inputs(61, B, L, H, Hkv, dk, dv, dtype), dtype, lens=[L // 3, 0, L][:B], fresh=fresh)
+
+
+@pytest.mark.parametrize("dtype,L", [("bf16", 2049), ("bf16", 2600), ("f32", 1025), ("f32", 4200)])
+@pytest.mark.parametrize("dk,dv,fresh", [(40, 72, True), (136, 24, False)])
+def test_prompt_many_segments(dtype, L, dk, dv, fresh):
+    """Rows of so many chunks that a segment has several, and the last fewer."""
+    check_lattn(lattn_inputs(62, 2, L, 2, 1, dk, dv, dtype), dtype, lens=[L - 70, L], fresh=fresh)
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
