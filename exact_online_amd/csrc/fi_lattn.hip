@@ -36,6 +36,7 @@ __global__ __launch_bounds__(kRecThreads) void k_lattn_step(LattnCall a) {
     const int dk = a.dk, dv = a.dv, G = a.G;
     const int64_t slot = a.slots ? a.slots[b] : b;
     const bool in = slot >= 0 && slot < a.n_slots;
+    const bool here = in && (!a.lens || a.lens[b] > 0);   // (a prompt's row may be empty)
     const int col = col0 + 4 * c, left = dv - col;   // columns of the state from the thread's first on
 
     // everything that the position reads is asked for at once
@@ -58,12 +59,13 @@ __global__ __launch_bounds__(kRecThreads) void k_lattn_step(LattnCall a) {
     const auto load_q = [&](int g0) {
         const int gn = G - g0 < kRecHeads ? G - g0 : kRecHeads;
         for (int i = tid; i < gn * ROWS; i += kRecThreads)
-            qs[i / ROWS][i % ROWS] = in && i % ROWS < dk ? get_io<BF16>(a.q.p, qb + (g0 + i / ROWS) * a.q.head + i % ROWS) : 0.f;
+            qs[i / ROWS][i % ROWS] = here && i % ROWS < dk ? get_io<BF16>(a.q.p, qb + (g0 + i / ROWS) * a.q.head + i % ROWS) : 0.f;
     };
-    for (int i = tid; i < ROWS; i += kRecThreads) ks[i] = in && i < dk ? get_io<BF16>(a.k.p, kb + i) : 0.f;
-    if (tid < kRecCols) vs[tid] = in && col0 + tid < dv ? get_io<BF16>(a.v.p, vb + col0 + tid) : 0.f;
+    for (int i = tid; i < ROWS; i += kRecThreads) ks[i] = here && i < dk ? get_io<BF16>(a.k.p, kb + i) : 0.f;
+    if (tid < kRecCols) vs[tid] = here && col0 + tid < dv ? get_io<BF16>(a.v.p, vb + col0 + tid) : 0.f;
     load_q(0);
-    const float em1 = expm1f(a.ld[n]);   // lam - 1
+    const float em1 = here ? expm1f(a.ld[n]) : 0.f;   // lam - 1
+    const bool kept = here || (in && a.fresh);        // the state changes
     __syncthreads();
 
     // S + (lam - 1) S rather than lam S: the rounding of lam (up to 2^-25 of S
@@ -74,7 +76,7 @@ __global__ __launch_bounds__(kRecThreads) void k_lattn_step(LattnCall a) {
         const float k = ks[r + i * kRecRows];
 #pragma unroll
         for (int j = 0; j < 4; ++j) S[i][j] = fmaf(k, v[j], fmaf(em1, S[i][j], S[i][j]));
-        if (in && r + i * kRecRows < dk) {
+        if (kept && r + i * kRecRows < dk) {
             FI_GLOBAL float* p = gmem(sp + i * kRecRows * dv);
             if constexpr (VEC) {
                 if (left > 0) *reinterpret_cast<FI_GLOBAL V4*>(p) = S[i];
@@ -113,7 +115,7 @@ __global__ __launch_bounds__(kRecThreads) void k_lattn_step(LattnCall a) {
             float o = 0.f;
 #pragma unroll
             for (int w = 0; w < WAVES; ++w) o += red[w][g][j];
-            if (col0 + j < dv) put_io<BF16>(a.o.p, b * a.o.row + (n * G + g0 + g) * a.o.head + col0 + j, in ? a.scale * o : 0.f);
+            if (col0 + j < dv) put_io<BF16>(a.o.p, b * a.o.row + (n * G + g0 + g) * a.o.head + col0 + j, here ? a.scale * o : 0.f);
         }
     }
 }

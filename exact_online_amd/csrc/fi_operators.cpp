@@ -167,7 +167,8 @@ int fi_lattn_prompt(fi_lattn *s, const fi_lattn_args *a) {
     LattnCall c;
     const int rc = lattn_call(s, a, c);
     if (rc != FI_OK || c.B == 0) return rc;
-    FI_HIP(launch_lattn_chunk(c, s->stream));
+    // a single position: the recurrent form, which needs no chunk (5 us for 7 to 12)
+    FI_HIP(c.L == 1 && c.state ? launch_lattn_step(c, s->stream) : launch_lattn_chunk(c, s->stream));
     return FI_OK;
 }
 

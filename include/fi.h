@@ -313,8 +313,8 @@ typedef struct {
 int fi_lattn_create(const fi_lattn_config *cfg, const float *log_decay, fi_lattn **out);
 
 /* fi_lattn_prompt: L given positions of every row in the chunked form (matrix
- * products over chunks of positions), from the row's state, which is left
- * after its last position.  B = 0 and L = 0 are allowed.  FI_ERR_INVALID for
+ * products over chunks of positions; one position with states: the recurrent
+ * form), from the row's state, which is left after its last position.  B = 0 and L = 0 are allowed.  FI_ERR_INVALID for
  * a NULL pointer, sizes beyond the config's, fewer than B states without
  * slots, or a pointer that is not aligned to its element.  A NaN or infinity
  * in k or v at t makes every later output and the state not finite, and can

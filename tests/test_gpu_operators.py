@@ -505,6 +505,17 @@ def test_prompt_shared_heads(B, L, H, Hkv, dk, dv, fresh, dtype):
     check_lattn(lattn_inputs(61, B, L, H, Hkv, dk, dv, dtype), dtype, lens=[L // 3, 0, L][:B], fresh=fresh)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("fresh", [True, False])
+def test_prompt_of_one_position(fresh, dtype):
+    """Rows with one position, with none and without a state of the array."""
+    inputs = lattn_inputs(63, 4, 1, 6, 2, 70, 33, dtype, slots=5)
+    check_lattn(inputs, dtype, lens=[1, 0, 3, 1], slots=[4, 0, 2, 9], fresh=fresh)
+    q, k, v, ld, state = inputs
+    q[1], k[1], v[1] = float("nan"), float("nan"), float("inf")    # past the end of a row: not read as numbers
+    check_lattn((q, k, v, ld, state), dtype, lens=[1, 0, 3, 1], slots=[4, 0, 2, 9], fresh=fresh)
+
+
 @pytest.mark.parametrize("dtype,L", [("bf16", 2049), ("bf16", 2600), ("f32", 1025), ("f32", 4200)])
 @pytest.mark.parametrize("dk,dv,fresh", [(40, 72, True), (136, 24, False)])
 def test_prompt_many_segments(dtype, L, dk, dv, fresh):
