@@ -386,16 +386,9 @@ __global__ __launch_bounds__((KW > 4 ? KW : 4) * kWave) void k_dense_few(DenseCa
         xin[i] = 16 * i + l16 < a.M;
         x[i] = static_cast<const T*>(a.x) + (xin[i] ? 16 * i + l16 : 0) * a.ldx;
     }
-    // whole units only: the one that K ends inside comes after the loop
-    using Loose = T __attribute__((ext_vector_type(M::E), aligned(sizeof(T))));
-    const auto load = [&](const T* p, int64_t k, bool in) -> Frag {
-        using Unit = std::conditional_t<ALIGNED, Frag, Loose>;
-        if (in && k + M::E <= a.K) return *gmem(reinterpret_cast<const Unit*>(p + k));
-        return Frag{};
-    };
     V4 acc[MT] = {};
     const int64_t steps = (a.K + M::KB - 1) / M::KB, s0 = steps * part / KW, s1 = steps * (part + 1) / KW;
-    if (n0 < a.N)
+    const auto sweep = [&](auto load) {
         for (int64_t s = s0; s < s1; s += UNROLL) {
             Frag fw[UNROLL], fx[UNROLL][MT];
 #pragma unroll
@@ -410,8 +403,21 @@ __global__ __launch_bounds__((KW > 4 ? KW : 4) * kWave) void k_dense_few(DenseCa
 #pragma unroll
                 for (int i = 0; i < MT; ++i) acc[i] = M::mma(fw[u], fx[u][i], acc[i]);
         }
-    if (!ALIGNED && a.K % M::E && part == KW - 1 && n0 < a.N) {
-        const int64_t k = a.K / M::E * M::E;
+    };
+    if (n0 < a.N) {
+        using Words = T __attribute__((ext_vector_type(M::E), aligned(4)));
+        uintptr_t low = reinterpret_cast<uintptr_t>(w);
+#pragma unroll
+        for (int i = 0; i < MT; ++i) low |= reinterpret_cast<uintptr_t>(x[i]);
+        if constexpr (ALIGNED)   // K is whole units
+            sweep([&](const T* p, int64_t k, bool in) { return in && k < a.K ? *gmem(reinterpret_cast<const Frag*>(p + k)) : Frag{}; });
+        // otherwise the last unit comes after the loop
+        else if (!BF16 || !__any(low % 4 != 0))
+            sweep([&](const T* p, int64_t k, bool in) -> Frag { return in && k + M::E < a.K ? Frag(*gmem(reinterpret_cast<const Words*>(p + k))) : Frag{}; });
+        else sweep([&](const T* p, int64_t k, bool in) { return in && k + M::E < a.K ? load_by_words<BF16>(p + k) : Frag{}; });
+    }
+    if (!ALIGNED && part == KW - 1 && n0 < a.N) {
+        const int64_t k = (a.K - 1) / M::E * M::E;
         const bool here = k % M::KB / M::E == g;   // the lanes whose unit it is
         Frag fw = {};
         if (here) fw = load_loose<BF16>(w, k, a.K);
