@@ -67,16 +67,16 @@ __device__ __forceinline__ uint32_t ordered(float v) {
 __device__ __forceinline__ float value_of(uint32_t o) { return __uint_as_float(o >> 31 ? o & 0x7FFFFFFFu : ~o); }
 __device__ __forceinline__ Key key_of(float v, uint32_t id) { return (Key)ordered(v) << 32 | ~id; }
 
-// A threshold that at least k of a wave's values reach and, where a few steps
-// of bisection find one, at most 3/2 k + 8.
-__device__ __forceinline__ uint32_t reached_by(uint32_t o, int k) {
+// A threshold that at least k of a wave's values reach and, where ties leave
+// one, at most `most`: the more may, the fewer steps of bisection.
+__device__ __forceinline__ uint32_t reached_by(uint32_t o, int k, int most) {
     uint32_t lo = 0, hi = 0xFFFFFFFFu;   // lo is reached by k of them, hi + 1 is not
     while (lo < hi) {
         const uint32_t mid = lo + (hi - lo) / 2 + 1;
         const int n = __popcll(__ballot(o >= mid));
         if (n >= k) {
             lo = mid;
-            if (n <= k + k / 2 + 8) break;
+            if (n <= most) break;
         } else hi = mid - 1;
     }
     return lo;
@@ -295,8 +295,9 @@ __global__ __launch_bounds__(kScThreads) void k_scores(ScoresCall a) {
         } else sums([&](float z) { return (z - x.m) * c; });
         if (k) {
             if (v == v0) {
-                // of the first batch, only what reaches the k-th largest lane or so
-                const uint32_t o = reached_by(ordered(most), k);
+                // of the first batch, only what reaches the k-th largest lane or so (95 rows
+                // of 54733, k = 32: 19.0 us; up to 3/2 k + 8 lanes 22.8, k exactly 20.1)
+                const uint32_t o = reached_by(ordered(most), k, k + k / 8 + 2);
                 const float f = value_of(o - (o == 0x80000000u ? 2 : 1));   // the next value below; -0 is 0
                 if (o && f > -inf) {                                        // false for NaN bits too
                     best.thr = f;
@@ -361,7 +362,7 @@ __global__ __launch_bounds__(kScThreads) void k_scores_join(ScoresCall a) {
     } else if (wave == 1) {
         // With the parts' j-th best keys, j = ceil(k / parts), the ceil(k / j)-th of
         // them bounds what can be among the row's k: that many parts have j keys
-        // as large (95 rows of 54733, k = 32: 37 us, with the best keys alone 39).
+        // as large (95 rows of 54733, k = 32: 23 us; 37 where half as many more might reach it).
         if (lane < kScoresMaxK) out[lane] = 0;
         if (lane == 0) count = 0;
         if (k) {
@@ -371,7 +372,8 @@ __global__ __launch_bounds__(kScThreads) void k_scores_join(ScoresCall a) {
                 const uint32_t h = (uint32_t)(keys[p * k + j - 1] >> 32);
                 head = head > h ? head : h;
             }
-            const uint32_t o = reached_by(head, (k + j - 1) / j);
+            const int m = (k + j - 1) / j;
+            const uint32_t o = reached_by(head, m, m);
             if (lane == 0) least = o;
         }
     } else if (wave == 2) {
