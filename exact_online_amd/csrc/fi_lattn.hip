@@ -230,6 +230,10 @@ __global__ __launch_bounds__(la_threads(DVS), DK == 256 ? 2 : 4) void k_lattn_ch
     // cores to the others (38 -> 26 us, 12 heads of 192 x 32, fp32, 85 positions; in
     // slices of 64 columns the question costs more than it gives).
     const bool active = DVS <= 64 || col0 + 16 * wave < dv;
+    // fp32's wide heads, whose products take most of the time, also leave out the
+    // tiles beyond dk (us, 7 rows of 11096, 6 heads on 3, dk = 192 / 256, dv = 192: 1143 / 1396,
+    // with all tiles 1343 / 1329; bf16, 3 of 31068, 10 on 5: 787 / 821 and 802 / 751).
+    constexpr bool SHORT = !BF16 && DK > 128;
     if (from) {
         const int row0 = 4 * g, scol = col0 + 16 * wave + (int)l16;
         if (full) {
@@ -382,6 +386,7 @@ __global__ __launch_bounds__(la_threads(DVS), DK == 256 ? 2 : 4) void k_lattn_ch
                     V4 p = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                     for (int kb = 0; kb < DK / KB; ++kb) {
+                        if (SHORT && kb * KB >= dk) break;
                         p = M::mma(pair_frag(ks + (16 * jt + krow_) * PK + kb * KB + 4 * g),
                                    row_frag(qs + mixed(DK / E, 16 * it + l16, kb * 4 + g)), p);
                     }
@@ -411,7 +416,7 @@ __global__ __launch_bounds__(la_threads(DVS), DK == 256 ? 2 : 4) void k_lattn_ch
                 V4 O[CT] = {};
 #pragma unroll
                 for (int kb = 0; kb < DK / KB; ++kb) {
-                    if (!active) break;
+                    if (!active || (SHORT && kb * KB >= dk)) break;
                     Frag fs;
 #pragma unroll
                     for (int e = 0; e < E; ++e) fs[e] = (T)S[kb * (KB / 16) + e / 4][e % 4];
@@ -505,6 +510,7 @@ __global__ __launch_bounds__(la_threads(DVS), DK == 256 ? 2 : 4) void k_lattn_ch
                            lo = __builtin_bit_cast(Frag, part[2]);
 #pragma unroll
                 for (int kt = 0; kt < KT; ++kt) {
+                    if (SHORT && kt % 4 == 0 && 16 * kt >= dk) break;
                     const Frag k = transposed(ks, PK, kb * KB, 16 * kt);
                     S[kt] = M::mma(k, hi, M::mma(k, mid, M::mma(k, lo, S[kt])));
                     if (kt % 4 == 3) __builtin_amdgcn_sched_barrier(0);
@@ -515,6 +521,7 @@ __global__ __launch_bounds__(la_threads(DVS), DK == 256 ? 2 : 4) void k_lattn_ch
                 for (int e = 0; e < E; ++e) x[e] = v[e] * w[e];
 #pragma unroll
                 for (int kt = 0; kt < KT; ++kt) {
+                    if (SHORT && kt % 4 == 0 && 16 * kt >= dk) break;
                     S[kt] = M::mma(transposed(ks, PK, kb * KB, 16 * kt), x, S[kt]);
                 }
             }
