@@ -157,11 +157,13 @@ hipError_t launch_lattn_step(const LattnCall& c, hipStream_t st) {
 // twice, half the waves) took 303 us where these take 297, and 132 where these
 // take 91 (ragged rows, four heads a group).
 //
-// Roundings (bf16): P and, as operand of Q E, E are rounded to bf16 once;
-// o is then off by 0.0026 of its norm, of which its own rounding is 0.0017.
-// (Both in two parts: 0.0017, for 20% of the time.)  V's decayed rows go into
-// S in three parts, exactly, so that S keeps fp32's precision over any number
-// of chunks.
+// Roundings (bf16): the operands of the products are bf16, so P and, in Q E, E
+// enter as two bf16 parts each, off by 2^-16 of them at most: o is the formula's value
+// rounded once (0.0001 of its norm from that; with one part each 0.0025, which is more
+// than the rounding itself, and what the step does to the same state would be another
+// number; 64K x 16 heads 397 -> 445 us, ragged rows 122 -> 133, one row of 77 8.3 -> 9.0).
+// V's decayed rows go into S in three parts, exactly, so that S keeps fp32's
+// precision over any number of chunks.
 //
 // Measured: 16 heads of 128 x 128, 65536 positions, bf16: 400 us (1.07 GB once:
 // 2.7 TB/s): local states 130, scan 15, outputs 255 to 297.  The outputs keep
@@ -182,7 +184,8 @@ __global__ __launch_bounds__(la_threads(DVS), DK == 256 ? 2 : 4) void k_lattn_ch
     constexpr int PK = DK + E, PV = DVS + E;                     // K's and V's LDS rows, 16 bytes longer
     constexpr int KT = DK / 16, CT = C / 16;                     // tiles of dk and of C
     constexpr int UK = C * DK / E / NTH, UV = C * DVS / E / NTH; // 16-byte units of a thread
-    __shared__ __align__(16) T ks[C * PK], vs[C * PV], qs[OUT ? C * DK : 1], ps[OUT ? C * C : 1];
+    constexpr int PARTS = BF16 ? 2 : 1;                          // of an fp32 factor as an operand
+    __shared__ __align__(16) T ks[C * PK], vs[C * PV], qs[OUT ? C * DK : 1], ps[OUT ? PARTS * C * C : 1];
 
     const int tid = threadIdx.x, lane = tid % kWave, wave = __builtin_amdgcn_readfirstlane(tid / kWave);
     uint32_t l16 = (uint32_t)lane % 16, g = (uint32_t)lane / 16;
@@ -390,8 +393,8 @@ __global__ __launch_bounds__(la_threads(DVS), DK == 256 ? 2 : 4) void k_lattn_ch
                         p = M::mma(pair_frag(ks + (16 * jt + krow_) * PK + kb * KB + 4 * g),
                                    row_frag(qs + mixed(DK / E, 16 * it + l16, kb * 4 + g)), p);
                     }
-                    const auto to = [&](int tile) {   // of four of the wave's 16 keys
-                        return smem_ptr(reinterpret_cast<Four*>(ps + mixed(C / E, 16 * it + l16, (16 * tile + 4 * g) / E) + 4 * g % E));
+                    const auto to = [&](int tile, int part) {   // of four of the wave's 16 keys
+                        return smem_ptr(reinterpret_cast<Four*>(ps + part * C * C + mixed(C / E, 16 * it + l16, (16 * tile + 4 * g) / E) + 4 * g % E));
                     };
                     const auto key = [&](int r) { return (int)(BF16 ? 8 * (g / 2) + 2 * r + g % 2 : 4 * g + r); };   // its place in its tile
                     if (it == jt) {
@@ -401,15 +404,21 @@ __global__ __launch_bounds__(la_threads(DVS), DK == 256 ? 2 : 4) void k_lattn_ch
                             p[r] = (i >= 0 ? p[r] : 0.f) * lam[i >= 0 ? i : 0];
                         }
                         // the rest of the block of keys that the product below takes whole
-                        if (BF16 && it % 2 == 0) *to(jt + 1) = Four{};
+                        if (BF16 && it % 2 == 0) *to(jt + 1, 0) = *to(jt + 1, 1) = Four{};
                     } else {
 #pragma unroll
                         for (int r = 0; r < 4; ++r) p[r] *= lam[16 * (it - jt) + (int)l16 - key(r)];
                     }
-                    Four y;
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) y[r] = (T)p[r];
-                    *to(jt) = y;
+                    for (int i = 0; i < PARTS; ++i) {
+                        Four y;
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            y[r] = (T)p[r];
+                            p[r] -= (float)y[r];
+                        }
+                        *to(jt, i) = y;
+                    }
                 }
                 __builtin_amdgcn_sched_barrier(0);
                 // O^T = E^T Q^T: columns are positions
@@ -417,12 +426,21 @@ __global__ __launch_bounds__(la_threads(DVS), DK == 256 ? 2 : 4) void k_lattn_ch
 #pragma unroll
                 for (int kb = 0; kb < DK / KB; ++kb) {
                     if (!active || (SHORT && kb * KB >= dk)) break;
-                    Frag fs;
+                    Frag fs[PARTS];
 #pragma unroll
-                    for (int e = 0; e < E; ++e) fs[e] = (T)S[kb * (KB / 16) + e / 4][e % 4];
+                    for (int e = 0; e < E; ++e) {
+                        float x = S[kb * (KB / 16) + e / 4][e % 4];
+#pragma unroll
+                        for (int i = 0; i < PARTS; ++i) {
+                            fs[i][e] = (T)x;
+                            x -= (float)fs[i][e];
+                        }
+                    }
 #pragma unroll
                     for (int it = 0; it < CT; ++it) {
-                        O[it] = M::mma(fs, row_frag(qs + mixed(DK / E, 16 * it + l16, kb * 4 + g)), O[it]);
+                        const Frag q = row_frag(qs + mixed(DK / E, 16 * it + l16, kb * 4 + g));
+#pragma unroll
+                        for (int i = PARTS - 1; i >= 0; --i) O[it] = M::mma(fs[i], q, O[it]);
                     }
                     __builtin_amdgcn_sched_barrier(0);
                 }
@@ -441,7 +459,9 @@ __global__ __launch_bounds__(la_threads(DVS), DK == 256 ? 2 : 4) void k_lattn_ch
                     const Frag v = transposed(vs, PV, kb * KB, 16 * wave);
 #pragma unroll
                     for (int it = kb * KB / 16; it < CT; ++it)   // queries before every key of the block: nothing
-                        O[it] = M::mma(v, row_frag(ps + mixed(C / E, 16 * it + l16, kb * 4 + g)), O[it]);
+#pragma unroll
+                        for (int i = PARTS - 1; i >= 0; --i)
+                            O[it] = M::mma(v, row_frag(ps + i * C * C + mixed(C / E, 16 * it + l16, kb * 4 + g)), O[it]);
                 }
                 __builtin_amdgcn_sched_barrier(0);
                 T* const op = static_cast<T*>(a.o.p) + b * a.o.row + (n * a.G + h) * a.o.head + (int64_t)(c * C - pad) * a.o.pos + col0 + 16 * wave;

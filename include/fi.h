@@ -274,8 +274,10 @@ typedef struct {
  *     o[t][h] = scale * S[t]^T q[t][h]            for the H/Hkv query heads h of
  *                                                 group n (h / (H/Hkv) == n)
  *
- * q, k, v and o are of io_dtype; S is held, summed and stored in fp32.  A
- * state array is state[n_slots][Hkv][dk][dv] (fp32, dense, the caller's); row
+ * q, k, v and o are of io_dtype; S is held, summed and stored in fp32, and o
+ * is rounded to io_dtype once.  (bf16 prompts: the fp32 factors of the matrix
+ * products, S and the weights of the values, enter as two bf16 parts each, which
+ * hold them to 2^-16.)  A state array is state[n_slots][Hkv][dk][dv] (fp32, dense, the caller's); row
  * b uses slot slots[b], or slot b where slots is NULL.  A row whose slot is
  * outside [0, n_slots) takes no part: its o is zero and no state changes.
  * Two rows of one call must not share a slot (their updates would race).
