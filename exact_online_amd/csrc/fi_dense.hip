@@ -135,8 +135,8 @@ __device__ __forceinline__ void dense_mma(V16 (&acc)[TN][TM], const typename Mm<
 // x 1024 157 us, and 180 to 192 with bias and GELU.  The product itself keeps the
 // matrix cores as busy as the power limit leaves them (clock 1.5 to 1.9 GHz);
 // then a tile's end, which the next tile of the CU waits for: stores (128 KB of
-// every CU at once: 7 us), GELU (14 operations and two transcendental ones for each
-// output: 9 us a tile).  256 x 128 with steps of 64 bytes in three stages: 990
+// every CU at once: 7 us), GELU (17 operations and two transcendental ones for each
+// output: 10 us a tile).  256 x 128 with steps of 64 bytes in three stages: 990
 // TFLOP/s at 8192^3; 128 x 128, two on a CU: 1065, and 207 us (216 with GELU, which
 // it hides) at 16384 x 4096 x 1024.  64 x 64 takes three stages, as its steps are
 // short against the loads' way (1000^3: 9.2 us with two, 8.3 with three).

@@ -62,3 +62,29 @@ def test_prompt_bf16_is_rounded_once(H, Hkv, dk, dv, L, fresh):
     log("largest distance of a row and head %.3g" % max(far))
     assert max(far) <= 2.0 ** -9.5
     assert max(ref.rel_l2(st[b, n], rs[b, n]) for b in range(B) for n in range(Hkv)) <= 5e-6
+
+
+# ------------------------------------------------------------ dense product
+@pytest.mark.parametrize("rows", ["one", "many"])
+def test_dense_gelu_keeps_its_tails(rows):
+    """GELU v Phi(v) of fp32 at v = x w, K = 1: relative in Phi(-|v|), which
+    every value on the negative side is made of.
+
+    Phi(-|v|) = e^{-v^2/2} times a polynomial: the polynomial's fit, its
+    evaluation, a reciprocal and an exponential, a unit of 2^-23 each and two for the
+    products, and the exponent's three roundings, 2^-24 each of v^2 / 2 log2 e:
+    (6 + v^2) 2^-23; then one rounding of y.  Below 2^-125 results may be flushed."""
+    v = torch.cat([torch.linspace(-14, 14, 2 * 8191 + 1), torch.tensor([0.0, -1e-6, 1e-6, 50.0, -50.0, 3e4, -3e4])])
+    x, w = (torch.ones(1, 1), v[:, None]) if rows == "one" else (v[:, None], torch.ones(65, 1))
+    z = x @ w.t()
+    y = torch.empty_like(z, device="cuda")
+    with fi.Dense(z.shape[0], z.shape[1], 1, fi.FI_F32, fi.FI_F32, fi.FI_ACT_GELU, stream()) as op:
+        op.run(x.cuda(), w.cuda(), y)
+        torch.cuda.synchronize()
+    z = z.double()
+    phi = torch.special.erfc(z.abs() / math.sqrt(2.0)) / 2   # (ndtr takes 1 + erf: 0 below -8.3)
+    want = z.clamp(min=0) - z.abs() * phi
+    bound = 2.0 ** -24 * want.abs() + z.abs() * phi * (6 + z * z) * 2.0 ** -23 + 2.0 ** -125 * z.abs().clamp(min=1)
+    over = (y.cpu().double() - want).abs() / bound.clamp(min=1e-300)
+    log("gelu, largest share of its bound %.3g at %.4g" % (over.max(), z.flatten()[over.argmax()]))
+    assert float(over.max()) <= 1.0
