@@ -52,6 +52,15 @@ __device__ __forceinline__ Stats moved_to(Stats a, float m, float c) {
     const float t = fmaxf(scaled_ref(a.m, m, c), kScLow), e = exp2f(t);
     return {m, a.s * e, e * (a.w + t * a.s)};
 }
+
+// sum + x, less what the additions before lost, which this one's loss replaces.
+// (One after the other the terms of many equal logits all round the same way:
+// 131072 of them in one row put lse off by 3e-5 and the entropy by 2e-4.)
+__device__ __forceinline__ void add_to(float& sum, float& lost, float x) {
+    const float y = x - lost, t = sum + y;
+    lost = (t - sum) - y;
+    sum = t;
+}
 __device__ __forceinline__ Stats join_wave(Stats x, float c) {
     x = moved_to(x, wave_max(x.m), c);
     return {x.m, wave_sum(x.s), wave_sum(x.w)};
@@ -251,7 +260,7 @@ __global__ __launch_bounds__(kScThreads) void k_scores(ScoresCall a) {
     const T* row = static_cast<const T*>(a.logits) + r * a.ld;
     const int64_t v0 = (int64_t)part * a.per, v1 = v0 + a.per < a.V ? v0 + a.per : a.V;
 
-    Stats x = {-__FLT_MAX__, 0.f, 0.f};   // m is the wave's, s and w the lane's
+    Stats x = {-__FLT_MAX__, 0.f, 0.f}, lost = x;   // m is the wave's, s and w the lane's; in the additions to them
     Best<BF16> best = {smem_ptr(wk[wave]), smem_ptr(wq[wave]), smem_ptr(wi[wave]), k, lane, 0, 0, 0, 0, -inf};
     const auto load = [&](Frag* f, int64_t v) {
 #pragma unroll
@@ -277,22 +286,27 @@ __global__ __launch_bounds__(kScThreads) void k_scores(ScoresCall a) {
             most = fmaxf(most, big[u]);
         }
         if (v == v0 || __ballot(scaled(most, x.m, c) > kScHigh)) {
-            x = moved_to(x, fmaxf(wave_max(most), x.m), c);
+            const float m = fmaxf(wave_max(most), x.m);
+            x = moved_to(x, m, c);
+            lost = moved_to(lost, m, c);
         }
+        float s[kScUnroll] = {}, w[kScUnroll] = {};   // the batch's sums
         const auto sums = [&](auto t_of) {
 #pragma unroll
             for (int u = 0; u < kScUnroll; ++u)
 #pragma unroll
                 for (int e = 0; e < E; ++e) {
                     const float t = t_of((float)now[u][e]), p = __builtin_amdgcn_exp2f(t);
-                    x.s += p;
-                    x.w = fmaf(p, fmaxf(t, kScLow), x.w);   // -inf: 0 (-2^14)
+                    s[u] += p;
+                    w[u] = fmaf(p, fmaxf(t, kScLow), w[u]);   // -inf: 0 (-2^14)
                 }
         };
         if (by_reference(x.m, c)) {
             const float ref = reference(x.m, c);
             sums([&](float z) { return fmaf(z, c, -ref); });
         } else sums([&](float z) { return (z - x.m) * c; });
+        add_to(x.s, lost.s, (s[0] + s[1]) + (s[2] + s[3]));
+        add_to(x.w, lost.w, (w[0] + w[1]) + (w[2] + w[3]));
         if (k) {
             if (v == v0) {
                 // of the first batch, only what reaches the k-th largest lane or so (95 rows
@@ -315,8 +329,8 @@ __global__ __launch_bounds__(kScThreads) void k_scores(ScoresCall a) {
         for (int u = 0; u < kScUnroll; ++u) now[u] = next[u];
     }
     best.rank();
-    x.s = wave_sum(x.s);
-    x.w = wave_sum(x.w);
+    x.s = wave_sum(x.s - lost.s);
+    x.w = wave_sum(x.w - lost.w);
     const Key alt = lane < best.size ? wk[wave][lane] : 0;
     if (a.parts == 1) scores_out(a, r, x, alt, target_of<BF16>(a, r, lane), lane);
     else {

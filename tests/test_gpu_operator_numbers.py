@@ -88,3 +88,42 @@ def test_dense_gelu_keeps_its_tails(rows):
     over = (y.cpu().double() - want).abs() / bound.clamp(min=1e-300)
     log("gelu, largest share of its bound %.3g at %.4g" % (over.max(), z.flatten()[over.argmax()]))
     assert float(over.max()) <= 1.0
+
+
+# ------------------------------------------------------------ token scores
+def run_scores(z, t, k, dtype, scale=1.0):
+    R, V = z.shape
+    lp, H, lse = (torch.full((R,), 9.0, device="cuda") for _ in range(3))
+    top, ids = torch.empty(R, k, device="cuda"), torch.empty(R, k, dtype=torch.int64, device="cuda")
+    with fi.TokenScores(R, V, k, DT[dtype][1], scale, stream()) as op:
+        op.run(z, t, lp, H, top, ids, lse)
+        torch.cuda.synchronize()
+    return [x.cpu() for x in (lp, H, lse, top, ids)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("R,V", [(1100, 131072), (1030, 200000), (1, 1 << 26)])
+def test_scores_of_many_equal_logits(R, V, dtype):
+    """One peak at 0 over a floor of equal logits -d, a row for each of several d:
+    every term of a sum rounds the same way, so sums of n terms one after the other
+    would be off by up to n 2^-25 of their value (n = V / 64: 6e-5).
+
+    Bounds as for any row: 2^t is off by |t| 2^-23, log probabilities by
+    1e-6 (8 + |lp|), lse by 1e-6 (4 + |lse|), entropies by 1e-6 (4 + H)."""
+    depth = [1.5, 2.5, 5.0, 5.25, 3.3125, 9.0, 11.5] if R > 1 else [2.5]
+    d = torch.tensor([depth[r % len(depth)] for r in range(R)])
+    z = (-d[:, None]).expand(R, V).to("cuda", DT[dtype][0]).contiguous()
+    z[:, V // 3] = 0.0
+    t = torch.full((R,), V - 1, dtype=torch.int64, device="cuda")
+    t[::2] = V // 3
+    lp, H, lse, top, ids = run_scores(z, t, 2, dtype)
+    d = d.double()      # (all of them are bf16 numbers)
+    rlse = torch.log1p((V - 1) * torch.exp(-d))
+    rlp = torch.where(t.cpu() == V // 3, 0.0, -d) - rlse
+    rH = rlse * torch.exp(-rlse) + (V - 1) * (d + rlse) * torch.exp(-d - rlse)
+    for what, got, want, a in (("lse", lse, rlse, 4e-6), ("logprob", lp, rlp, 8e-6), ("entropy", H, rH, 4e-6)):
+        e = (got.double() - want).abs()
+        log(what, R, V, dtype, "off by %.3g" % e.max())
+        assert bool((e <= a + 1e-6 * want.abs()).all()), what
+    assert ids[0].tolist() == [V // 3, 0]
+    assert bool(((top[:, 0].double() + rlse).abs() <= 8e-6 + 1e-6 * rlse).all())
