@@ -21,35 +21,43 @@ struct Stats {
     float m, s, w;
 };
 
+// The scale, and with log2 e: that is infinite for the largest scales, and then no
+// reference is within bounds.
+struct Scale {
+    float s, c;
+};
+__device__ __forceinline__ Scale scale_of(const ScoresCall& a) { return {a.scale, a.scale * kLog2e}; }
+
 // The scaled reference, rounded by itself everywhere (it is what the sums are
 // taken against: m c inside a fused operation would be another number).
-__device__ __forceinline__ float reference(float m, float c) {
+__device__ __forceinline__ float reference(float m, Scale k) {
 #pragma clang fp contract(off)
-    const float r = m * c;
+    const float r = m * k.c;
     return r;
 }
 // From 2^24 on R is off m c by more than 1/2, and by more than exp2 can take from 2^31
-// on: such logits are taken by differences, t = (z - m) c, against m c itself.
-__device__ __forceinline__ bool by_reference(float m, float c) { return fabsf(reference(m, c)) < 16777216.f; }
-__device__ __forceinline__ float scaled(float z, float m, float c) {
-    return by_reference(m, c) ? fmaf(z, c, -reference(m, c)) : (z - m) * c;
+// on: such logits are taken by differences, t = (z - m) scale log2 e, against m c itself.
+__device__ __forceinline__ bool by_reference(float m, Scale k) { return fabsf(reference(m, k)) < 16777216.f; }   // false for NaN
+__device__ __forceinline__ float by_difference(float z, float m, Scale k) { return (z - m) * k.s * kLog2e; }
+__device__ __forceinline__ float scaled(float z, float m, Scale k) {
+    return by_reference(m, k) ? fmaf(z, k.c, -reference(m, k)) : by_difference(z, m, k);
 }
-__device__ __forceinline__ float scaled_ref(float a, float m, float c) {   // of sums by a against those by m
+__device__ __forceinline__ float scaled_ref(float a, float m, Scale k) {   // of sums by a against those by m
 #pragma clang fp contract(off)
-    if (by_reference(a, c)) return by_reference(m, c) ? reference(a, c) - reference(m, c) : fmaf(-m, c, reference(a, c));
-    return by_reference(m, c) ? fmaf(a, c, -reference(m, c)) : (a - m) * c;
+    if (by_reference(a, k)) return by_reference(m, k) ? reference(a, k) - reference(m, k) : fmaf(-m, k.c, reference(a, k));
+    return by_reference(m, k) ? fmaf(a, k.c, -reference(m, k)) : by_difference(a, m, k);
 }
 
-__device__ __forceinline__ Stats join(Stats a, Stats b, float c) {
+__device__ __forceinline__ Stats join(Stats a, Stats b, Scale k) {
     const float m = fmaxf(a.m, b.m);
-    const float da = fmaxf(scaled_ref(a.m, m, c), kScLow), db = fmaxf(scaled_ref(b.m, m, c), kScLow);
+    const float da = fmaxf(scaled_ref(a.m, m, k), kScLow), db = fmaxf(scaled_ref(b.m, m, k), kScLow);
     const float ea = exp2f(da), eb = exp2f(db);
     return {m, a.s * ea + b.s * eb, ea * (a.w + da * a.s) + eb * (b.w + db * b.s)};
 }
 
 // the same sums by another reference
-__device__ __forceinline__ Stats moved_to(Stats a, float m, float c) {
-    const float t = fmaxf(scaled_ref(a.m, m, c), kScLow), e = exp2f(t);
+__device__ __forceinline__ Stats moved_to(Stats a, float m, Scale k) {
+    const float t = fmaxf(scaled_ref(a.m, m, k), kScLow), e = exp2f(t);
     return {m, a.s * e, e * (a.w + t * a.s)};
 }
 
@@ -61,8 +69,8 @@ __device__ __forceinline__ void add_to(float& sum, float& lost, float x) {
     lost = (t - sum) - y;
     sum = t;
 }
-__device__ __forceinline__ Stats join_wave(Stats x, float c) {
-    x = moved_to(x, wave_max(x.m), c);
+__device__ __forceinline__ Stats join_wave(Stats x, Scale k) {
+    x = moved_to(x, wave_max(x.m), k);
     return {x.m, wave_sum(x.s), wave_sum(x.w)};
 }
 
@@ -111,7 +119,8 @@ __device__ __forceinline__ Target target_of(const ScoresCall& a, int64_t r, int 
 __device__ __forceinline__ void scores_out(const ScoresCall& a, int64_t r, Stats x, Key alt, Target t, int lane) {
     const float inf = __builtin_inff(), nan = __builtin_nanf("");
     const bool empty = x.s == 0.f, bad = !(x.s < inf);
-    const float c = a.scale * kLog2e, l2 = log2f(x.s);
+    const Scale c = scale_of(a);
+    const float l2 = log2f(x.s);
     const auto log_p = [&](float z) {   // (a type's lowest value overflows in units of log2)
         const float t = scaled(z, x.m, c);
         return fabsf(t) < 1e30f ? (t - l2) * kLn2 : fmaf(z - x.m, a.scale, -l2 * kLn2);
@@ -253,7 +262,8 @@ __global__ __launch_bounds__(kScThreads) void k_scores(ScoresCall a) {
     __shared__ __align__(16) Frag wq[kScWaves][kWave];
     __shared__ uint32_t wi[kScWaves][kWave];
     const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), k = a.k;
-    const float c = a.scale * kLog2e, inf = __builtin_inff();
+    const Scale c = scale_of(a);
+    const float inf = __builtin_inff();
     const int64_t unit = (int64_t)blockIdx.x * kScWaves + wave, r = unit / a.parts;
     if (r >= a.rows) return;
     const int part = (int)(unit - r * a.parts);
@@ -303,8 +313,8 @@ __global__ __launch_bounds__(kScThreads) void k_scores(ScoresCall a) {
         };
         if (by_reference(x.m, c)) {
             const float ref = reference(x.m, c);
-            sums([&](float z) { return fmaf(z, c, -ref); });
-        } else sums([&](float z) { return (z - x.m) * c; });
+            sums([&](float z) { return fmaf(z, c.c, -ref); });
+        } else sums([&](float z) { return by_difference(z, x.m, c); });
         add_to(x.s, lost.s, (s[0] + s[1]) + (s[2] + s[3]));
         add_to(x.w, lost.w, (w[0] + w[1]) + (w[2] + w[3]));
         if (k) {
@@ -358,7 +368,7 @@ __global__ __launch_bounds__(kScThreads) void k_scores_join(ScoresCall a) {
     __shared__ Target given;
     const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave, k = a.k, all = a.parts * k;
     const int64_t r = blockIdx.x;
-    const float c = a.scale * kLog2e;
+    const Scale c = scale_of(a);
     const Key* const keys = a.pkey + r * all;
     // one wave joins the sums and writes the results, another bounds the
     // alternatives, a third gets the given token's logit

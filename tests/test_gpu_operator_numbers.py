@@ -127,3 +127,28 @@ def test_scores_of_many_equal_logits(R, V, dtype):
         assert bool((e <= a + 1e-6 * want.abs()).all()), what
     assert ids[0].tolist() == [V // 3, 0]
     assert bool(((top[:, 0].double() + rlse).abs() <= 8e-6 + 1e-6 * rlse).all())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("V", [700, 40000])
+@pytest.mark.parametrize("scale", [2.0e38, 3.0e38, 3.4e38])
+def test_scores_of_the_largest_scales(V, scale, dtype):
+    """Finite scales whose product with log2 e is not: logits that
+    lie some 1e-38 apart, and ordinary ones, where all of the probability is with the
+    largest.  The bounds of ordinary rows (logits below 2^-126 are whole
+    multiples of 2^-149, so their differences are exact)."""
+    g = gen(V)
+    z = torch.randn(5, V, generator=g).to(DT[dtype][0])
+    z[0] = (torch.randn(V, generator=g) * 1.5e-38).to(DT[dtype][0])
+    z[1] = (torch.randn(V, generator=g) * 2.0 ** -126).to(DT[dtype][0])
+    z[2] = 0.0
+    z[3, V // 2] = 7.0
+    t = torch.randint(0, V, (5,), generator=g)
+    lp, H, lse, top, ids = run_scores(z.cuda(), t.cuda(), 6, dtype, scale)
+    rlp, rH, rlse, rtop, rids = ref.scores(z, t, 6, torch.tensor(scale).item())
+    assert torch.equal(ids, rids)
+    for got, want, a in ((lp, rlp, 8e-6), (H, rH, 4e-6), (lse, rlse, 4e-6), (top, rtop, 8e-6)):
+        f = torch.isfinite(want.float())
+        assert torch.equal(torch.isnan(got), torch.isnan(want))
+        assert torch.equal(got[~f], want.float()[~f])
+        assert bool(((got.double() - want).abs()[f] <= a + 1e-6 * want.abs()[f]).all())
