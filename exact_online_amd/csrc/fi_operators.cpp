@@ -178,6 +178,7 @@ int fi_lattn_step(fi_lattn *s, const fi_lattn_args *a) {
     if (rc != FI_OK) return rc;
     if (a->L != 1 || a->lens) return FI_ERR_INVALID;
     if (c.B == 0) return FI_OK;
+    if (!c.state) return FI_ERR_INVALID;   // every step leaves its state behind
     FI_HIP(launch_lattn_step(c, s->stream));
     return FI_OK;
 }

@@ -323,8 +323,9 @@ int fi_lattn_create(const fi_lattn_config *cfg, const float *log_decay, fi_lattn
  * make outputs of up to 63 positions before t of its row and head NaN. */
 int fi_lattn_prompt(fi_lattn *s, const fi_lattn_args *a);
 
-/* fi_lattn_step: one new position of every row in the recurrent form; L is 1
- * and lens NULL (else FI_ERR_INVALID).  Errors as fi_lattn_prompt. */
+/* fi_lattn_step: one new position of every row in the recurrent form; L is 1,
+ * lens NULL and state not NULL, also where fresh (else FI_ERR_INVALID).  Errors
+ * as fi_lattn_prompt. */
 int fi_lattn_step(fi_lattn *s, const fi_lattn_args *a);
 
 /* fi_lattn_destroy: synchronise the stream and free everything; NULL is a no-op. */
