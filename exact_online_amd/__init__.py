@@ -360,6 +360,28 @@ def _refuse(where: str):
     raise FiError(FI_ERR_INVALID, where)
 
 
+def _torch(name):
+    import torch   # the callers' tensors are its, so it is there
+    return getattr(torch, name)
+
+
+def _io_type(dtype):
+    """The tensors' type of an FI_* type (the create call refuses others)."""
+    return {FI_F32: _torch("float32"), FI_BF16: _torch("bfloat16")}.get(int(dtype))
+
+
+def _dense(x, dtype, n, where) -> int:
+    """The address of an array of at least n elements; a tensor has to be dense, of this type and on the device.
+    None and addresses are taken as they are."""
+    if x is None:
+        return 0
+    if not hasattr(x, "data_ptr"):
+        return int(x)
+    if x.dtype is not dtype or not x.is_cuda or not x.is_contiguous() or x.numel() < n:
+        _refuse(where)
+    return x.data_ptr()
+
+
 _LATTN_ARGS = struct.Struct("@2q" + "P3q" * 4 + "2PqPi4x")   # 4x: the trailing padding
 
 
@@ -368,32 +390,43 @@ class LinearAttention(_Owner):
     (marshalling only).  q, k, v and o are tensors [B, L, heads, size] of the
     io type, of any strides as long as a head's elements are adjacent; state
     is [slots, Hkv, dk, dv], fp32 and contiguous, updated in place; lens and
-    slots are int32 tensors [B] on the device."""
+    slots are int32 tensors [B] on the device, log_decay is fp32 [Hkv].  Other
+    shapes, types, strides and tensors on the host are refused."""
 
     _destroy = staticmethod(fi_lattn_destroy)
 
     def __init__(self, B, L, H, Hkv, dk, dv, log_decay, scale=1.0, io_dtype=FI_BF16, stream=None):
         self.cfg = fi_lattn_config(B=int(B), L=int(L), H=int(H), Hkv=int(Hkv), dk=int(dk), dv=int(dv),
                                    scale=float(scale), io_dtype=int(io_dtype), stream=_stream(stream))
-        self._heads = int(H), int(Hkv), int(dk), int(dv)
+        self._is = (int(H), int(Hkv), int(dk), int(dv), _io_type(io_dtype), _torch("float32"), _torch("int32"))
         self._args = fi_lattn_args()
-        self.handle = fi_lattn_create(self.cfg, log_decay)
+        self.handle = fi_lattn_create(self.cfg, _dense(log_decay, _torch("float32"), int(Hkv), "fi_lattn_create"))
 
     def _call(self, fn, where, q, k, v, o, state, lens, slots, fresh):
         shape = q.shape
         B, L = shape[0], shape[1]
-        H, Hkv, dk, dv = self._heads
+        H, Hkv, dk, dv, io, f32, i32 = self._is
         qs, ks, vs, os_ = q.stride(), k.stride(), v.stride(), o.stride()
         if (shape != (B, L, H, dk) or k.shape != (B, L, Hkv, dk) or v.shape != (B, L, Hkv, dv)
                 or o.shape != (B, L, H, dv) or (dk > 1 and (qs[3] != 1 or ks[3] != 1))
-                or (dv > 1 and (vs[3] != 1 or os_[3] != 1))):
+                or (dv > 1 and (vs[3] != 1 or os_[3] != 1))
+                or q.dtype is not io or k.dtype is not io or v.dtype is not io or o.dtype is not io
+                or not (q.is_cuda and k.is_cuda and v.is_cuda and o.is_cuda)):
             _refuse(where)
+        n_slots = states = 0
+        if state is not None:
+            shape = state.shape
+            n_slots = shape[0] if shape else 0
+            if (shape != (n_slots, Hkv, dk, dv) or state.dtype is not f32 or not state.is_cuda
+                    or not state.is_contiguous()):
+                _refuse(where)
+            states = state.data_ptr()
         # the struct's fields in their order (fi_lattn_args, native layout)
         _LATTN_ARGS.pack_into(
             self._args, 0, B, L, q.data_ptr(), qs[0], qs[1], qs[2], k.data_ptr(), ks[0], ks[1], ks[2],
             v.data_ptr(), vs[0], vs[1], vs[2], o.data_ptr(), os_[0], os_[1], os_[2],
-            0 if lens is None else lens.data_ptr(), 0 if slots is None else slots.data_ptr(),
-            0 if state is None else state.shape[0], 0 if state is None else state.data_ptr(), 1 if fresh else 0)
+            0 if lens is None else _dense(lens, i32, B, where), 0 if slots is None else _dense(slots, i32, B, where),
+            n_slots, states, 1 if fresh else 0)
         status = fn(self.handle, self._args)
         if status < 0:
             raise FiError(status, where)
@@ -407,7 +440,8 @@ class LinearAttention(_Owner):
 
 class Dense(_Owner):
     """y = act(x w^T + bias) + res over rows (marshalling only): x [M, K],
-    w [N, K], bias [N], res and y [M, N], rows of any stride."""
+    w [N, K] and bias [N] of io_dtype, res and y [M, N] of out_dtype, rows of
+    any stride.  Other shapes, types and tensors on the host are refused."""
 
     _destroy = staticmethod(fi_dense_destroy)
 
@@ -415,6 +449,7 @@ class Dense(_Owner):
         self.cfg = fi_dense_config(M=int(M), N=int(N), K=int(K), io_dtype=int(io_dtype), out_dtype=int(out_dtype),
                                    act=int(act), stream=_stream(stream))
         self.N, self.K = int(N), int(K)
+        self._io, self._out = _io_type(io_dtype), _io_type(out_dtype)
         self.handle = fi_dense_create(self.cfg)
 
     def run(self, x, w, y, bias=None, res=None):
@@ -422,14 +457,18 @@ class Dense(_Owner):
         where = "fi_dense_run"
         xs, ws, ys = x.stride(), w.stride(), y.stride()
         if (x.shape != (M, K) or w.shape != (N, K) or y.shape != (M, N) or (K > 1 and (xs[1] != 1 or ws[1] != 1))
-                or (N > 1 and ys[1] != 1)):
+                or (N > 1 and ys[1] != 1) or x.dtype is not self._io or w.dtype is not self._io
+                or y.dtype is not self._out or not (x.is_cuda and w.is_cuda and y.is_cuda)):
             _refuse(where)
         ldr = 0
         if res is not None:
-            ldr, inner = res.stride()
-            if res.shape != (M, N) or (N > 1 and inner != 1):
+            if res.shape != (M, N) or res.dtype is not self._out or not res.is_cuda:
                 _refuse(where)
-        a = fi_dense_args(M, x.data_ptr(), xs[0], w.data_ptr(), ws[0], _ptr(bias), _ptr(res), ldr, y.data_ptr(), ys[0])
+            ldr, inner = res.stride()
+            if N > 1 and inner != 1:
+                _refuse(where)
+        a = fi_dense_args(M, x.data_ptr(), xs[0], w.data_ptr(), ws[0], _dense(bias, self._io, N, where), _ptr(res), ldr,
+                          y.data_ptr(), ys[0])
         _check(lib.fi_dense_run(self.handle, a), where)
 
 
@@ -437,23 +476,28 @@ class TokenScores(_Owner):
     """Log probabilities of given tokens, entropies and the most probable
     tokens (marshalling only): logits [rows, V] with rows of any stride;
     targets int64 [rows]; logprob, entropy, lse fp32 [rows]; top fp32 and
-    top_id int64 [rows, k], contiguous.  Outputs that are None are left out."""
+    top_id int64 [rows, k], contiguous (or longer).  Outputs that are None are
+    left out; other shapes, types, strides and tensors on the host are refused."""
 
     _destroy = staticmethod(fi_scores_destroy)
 
     def __init__(self, rows, V, k=0, io_dtype=FI_BF16, scale=1.0, stream=None):
         self.cfg = fi_scores_config(rows=int(rows), V=int(V), k=int(k), io_dtype=int(io_dtype), scale=float(scale),
                                     stream=_stream(stream))
-        self.V = int(V)
+        self.V, self.k = int(V), int(k)
+        self._io, self._f32, self._i64 = _io_type(io_dtype), _torch("float32"), _torch("int64")
         self.handle = fi_scores_create(self.cfg)
 
     def run(self, logits, targets=None, logprob=None, entropy=None, top=None, top_id=None, lse=None):
+        where, f32, i64 = "fi_scores_run", self._f32, self._i64
         rows, ld = logits.shape[0], logits.stride(0)
-        if logits.shape != (rows, self.V) or (self.V > 1 and logits.stride(1) != 1):
-            _refuse("fi_scores_run")
-        a = fi_scores_args(rows, logits.data_ptr(), ld, _ptr(targets), _ptr(logprob), _ptr(entropy), _ptr(lse),
-                           _ptr(top), _ptr(top_id))
-        _check(lib.fi_scores_run(self.handle, a), "fi_scores_run")
+        if (logits.shape != (rows, self.V) or (self.V > 1 and logits.stride(1) != 1) or logits.dtype is not self._io
+                or not logits.is_cuda):
+            _refuse(where)
+        a = fi_scores_args(rows, logits.data_ptr(), ld, _dense(targets, i64, rows, where),
+                           *(_dense(x, f32, rows, where) for x in (logprob, entropy, lse)),
+                           _dense(top, f32, rows * self.k, where), _dense(top_id, i64, rows * self.k, where))
+        _check(lib.fi_scores_run(self.handle, a), where)
 
 
 def fi_profile_read(s: int):

@@ -41,3 +41,110 @@ def test_step_needs_states(lattn, fresh, slots):
     assert lattn("prompt", **kw) == want
     assert lattn("step", **{**kw, "B": 0, "fresh": 1}) == fi.FI_OK      # no rows, no states
     assert lattn("step", L=1, fresh=fresh) == fi.FI_ERR_HIP             # with states it would launch
+
+
+# ------------------------------------------------------------ the binding
+class OnDevice:
+    """A tensor that says it lies on the device."""
+    is_cuda = True
+
+    def __init__(self, t):
+        self.t = t
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+
+class Calls:
+    """Stands in for the library: says FI_OK and counts the calls that run something."""
+
+    def __init__(self):
+        self.n = 0
+
+    def __getattr__(self, name):
+        def call(*a):
+            if name == "fi_strerror":
+                return b""
+            if name.endswith("_create"):
+                a[-1]._obj.value = 1
+            elif not name.endswith("_destroy"):
+                self.n += 1
+            return fi.FI_OK
+        return call
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    c = Calls()
+    monkeypatch.setattr(fi, "lib", c)
+    return c
+
+
+def zeros(*shape, t=torch.float32):
+    return torch.zeros(*shape, dtype=t)
+
+
+BF, F32, I32, I64 = torch.bfloat16, torch.float32, torch.int32, torch.int64
+LATTN_OK = dict(q=zeros(3, 4, 4, 8, t=BF), k=zeros(3, 4, 2, 8, t=BF), v=zeros(3, 4, 2, 6, t=BF), o=zeros(3, 4, 4, 6, t=BF),
+                state=zeros(5, 2, 8, 6), lens=zeros(3, t=I32), slots=zeros(3, t=I32))
+DENSE_OK = dict(x=zeros(3, 8, t=BF), w=zeros(6, 8, t=BF), y=zeros(3, 6), bias=zeros(6, t=BF), res=zeros(3, 6))
+SCORES_OK = dict(logits=zeros(3, 50, t=BF), targets=zeros(3, t=I64), logprob=zeros(3), entropy=zeros(3), lse=zeros(3),
+                 top=zeros(3, 4), top_id=zeros(3, 4, t=I64))
+
+
+def wrong(ok, strided):
+    """(name, tensor): of another type each, too short, on the host, and (`strided`: dense arrays) with gaps."""
+    for name, t in ok.items():
+        other = {BF: F32, F32: BF, I32: I64, I64: I32}[t.dtype]
+        yield name, OnDevice(t.to(other))
+        yield name, OnDevice(t[..., :-1].contiguous())
+        yield name, t
+        if name in strided:
+            wide = zeros(*t.shape[:-1], 2 * t.shape[-1], t=t.dtype)
+            yield name, OnDevice(wide[..., ::2])
+
+
+def check_binding(calls, op, ok, strided):
+    ok = {n: OnDevice(t) for n, t in ok.items()}
+    n = calls.n
+    op(**ok)
+    assert calls.n == n + 1
+    for name, bad in wrong({n: t.t for n, t in ok.items()}, strided):
+        with pytest.raises(fi.FiError) as e:
+            op(**{**ok, name: bad})
+        assert e.value.status == fi.FI_ERR_INVALID, name
+        assert calls.n == n + 1, (name, bad.dtype, bad.shape)
+
+
+def test_linear_attention_checks_its_tensors(calls):
+    for bad in (zeros(2), OnDevice(zeros(1)), OnDevice(zeros(2, t=BF)), OnDevice(zeros(4)[::2])):
+        with pytest.raises(fi.FiError):
+            fi.LinearAttention(3, 4, 4, 2, 8, 6, bad, 1.0, fi.FI_BF16).close()
+    with fi.LinearAttention(3, 4, 4, 2, 8, 6, OnDevice(zeros(2)), 1.0, fi.FI_BF16) as op:
+        check_binding(calls, op.prompt, LATTN_OK, ("q", "k", "v", "o", "state", "lens", "slots"))
+        op.prompt(**{n: OnDevice(LATTN_OK[n]) for n in "qkvo"}, fresh=True)
+        for state in (zeros(5, 2, 6, 8), zeros(5, 2, 8, 5), zeros(5, 96), zeros(5, 2, 6, 8).transpose(2, 3), zeros(96),
+                      zeros(5, 4, 8, 6)[:, ::2], zeros(1, 2, 8, 6).expand(5, -1, -1, -1), torch.tensor(0.0)):
+            n = calls.n
+            with pytest.raises(fi.FiError):
+                op.step(*(OnDevice(LATTN_OK[x][:, :1]) for x in "qkvo"), state=OnDevice(state))
+            assert calls.n == n
+
+
+def test_dense_checks_its_tensors(calls):
+    with fi.Dense(3, 6, 8, fi.FI_BF16, fi.FI_F32) as op:
+        check_binding(calls, op.run, DENSE_OK, ("x", "w", "y", "res", "bias"))
+        op.run(*(OnDevice(DENSE_OK[n]) for n in "xwy"))
+
+
+def test_token_scores_checks_its_tensors(calls):
+    with fi.TokenScores(3, 50, 4, fi.FI_BF16) as op:
+        check_binding(calls, op.run, SCORES_OK, ("logits", "targets", "logprob", "entropy", "lse", "top", "top_id"))
+        op.run(OnDevice(SCORES_OK["logits"]), top=OnDevice(zeros(12)), top_id=OnDevice(zeros(20, t=I64)))   # as long or longer
+
+
+def test_addresses_are_taken_as_they_are(calls):
+    with fi.Dense(3, 6, 8, fi.FI_BF16, fi.FI_F32) as op, fi.TokenScores(3, 50, 0, fi.FI_BF16) as sc:
+        op.run(*(OnDevice(DENSE_OK[n]) for n in "xwy"), bias=P)
+        sc.run(OnDevice(SCORES_OK["logits"]), targets=P, logprob=P, entropy=P)
+    assert calls.n == 2
