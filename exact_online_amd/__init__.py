@@ -467,8 +467,13 @@ class Dense(_Owner):
             ldr, inner = res.stride()
             if N > 1 and inner != 1:
                 _refuse(where)
-        a = fi_dense_args(M, x.data_ptr(), xs[0], w.data_ptr(), ws[0], _dense(bias, self._io, N, where), _ptr(res), ldr,
-                          y.data_ptr(), ys[0])
+        ldx, ldw, ldy = xs[0], ws[0], ys[0]
+        if M == 1:   # the stride of a single row is any number
+            ldx, ldr, ldy = K, N, N
+        if N == 1:
+            ldw = K
+        a = fi_dense_args(M, x.data_ptr(), ldx, w.data_ptr(), ldw, _dense(bias, self._io, N, where), _ptr(res), ldr,
+                          y.data_ptr(), ldy)
         _check(lib.fi_dense_run(self.handle, a), where)
 
 
@@ -490,7 +495,8 @@ class TokenScores(_Owner):
 
     def run(self, logits, targets=None, logprob=None, entropy=None, top=None, top_id=None, lse=None):
         where, f32, i64 = "fi_scores_run", self._f32, self._i64
-        rows, ld = logits.shape[0], logits.stride(0)
+        rows = logits.shape[0]
+        ld = logits.stride(0) if rows > 1 else self.V   # the stride of a single row is any number
         if (logits.shape != (rows, self.V) or (self.V > 1 and logits.stride(1) != 1) or logits.dtype is not self._io
                 or not logits.is_cuda):
             _refuse(where)

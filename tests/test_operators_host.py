@@ -69,6 +69,7 @@ class Calls:
                 a[-1]._obj.value = 1
             elif not name.endswith("_destroy"):
                 self.n += 1
+                self.args = a[-1]
             return fi.FI_OK
         return call
 
@@ -148,3 +149,21 @@ def test_addresses_are_taken_as_they_are(calls):
         op.run(*(OnDevice(DENSE_OK[n]) for n in "xwy"), bias=P)
         sc.run(OnDevice(SCORES_OK["logits"]), targets=P, logprob=P, entropy=P)
     assert calls.n == 2
+
+
+def test_the_stride_of_a_single_row_says_nothing(calls):
+    """torch gives a dimension of size one any stride (a transposed column: 1), and the
+    library wants rows at least their length apart."""
+    def row(n, t):
+        return OnDevice(zeros(n, 1, t=t).T)
+    with fi.Dense(4, 6, 8, fi.FI_BF16, fi.FI_F32) as op, fi.Dense(4, 1, 8, fi.FI_BF16, fi.FI_F32) as one, \
+            fi.TokenScores(4, 50, 0, fi.FI_BF16) as sc:
+        op.run(row(8, BF), OnDevice(zeros(6, 8, t=BF)), row(6, F32), res=row(6, F32))
+        a = calls.args
+        assert (a.M, a.ldx, a.ldw, a.ldr, a.ldy) == (1, 8, 8, 6, 6)
+        one.run(OnDevice(zeros(3, 8, t=BF)), row(8, BF), OnDevice(zeros(3, 1)))
+        assert (calls.args.ldx, calls.args.ldw, calls.args.ldy) == (8, 8, 1)
+        sc.run(row(50, BF), entropy=OnDevice(zeros(1)))
+        assert (calls.args.rows, calls.args.ld) == (1, 50)
+        op.run(OnDevice(zeros(2, 9, t=BF)[:, 1:]), OnDevice(zeros(6, 12, t=BF)[:, :8]), OnDevice(zeros(2, 7)[:, 1:]))
+        assert (calls.args.ldx, calls.args.ldw, calls.args.ldy) == (9, 12, 7)      # of several rows it does
