@@ -16,7 +16,7 @@ PROFILE_LIB = PKG / "libfi_prof.so"   # the phase-timing build (-DFI_PROFILE=1),
 SOURCES = [CSRC / "fi_kernels.hip", CSRC / "fi_lattn.hip", CSRC / "fi_dense.hip", CSRC / "fi_scores.hip",
            CSRC / "fi_api.cpp", CSRC / "fi_operators.cpp"]
 HEADERS = [ROOT / "include" / "fi.h", ROOT / "include" / "fi_profile.h", CSRC / "fi_internal.h",
-           CSRC / "fi_device.hpp", CSRC / "fi_operators.h", CSRC / "fi_opdev.hpp"]
+           CSRC / "fi_device.hpp", CSRC / "fi_host.h", CSRC / "fi_operators.h", CSRC / "fi_opdev.hpp"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

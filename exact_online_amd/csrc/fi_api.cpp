@@ -13,6 +13,7 @@
 #include <new>
 
 #include "fi.h"
+#include "fi_host.h"
 #include "fi_internal.h"
 #if FI_PROFILE
 #include "fi_profile.h"

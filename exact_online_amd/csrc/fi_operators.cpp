@@ -10,7 +10,7 @@
 #include <vector>
 
 #include "fi.h"
-#include "fi_internal.h"
+#include "fi_host.h"
 
 using namespace fi;
 
