@@ -174,8 +174,11 @@ hipError_t launch_lattn_step(const LattnCall& c, hipStream_t st) {
 constexpr int la_chunk(bool bf16) { return bf16 ? 64 : 32; }   // positions of a chunk
 constexpr int la_threads(int dvs) { return dvs / 16 * kWave; }
 
+// waves of a SIMD that registers are kept for (LDS holds three workgroups of bf16's 64 x 64 outputs)
+constexpr int la_waves(bool bf16, int dk, bool out) { return dk == 256 ? 2 : bf16 && dk == 64 && out ? 3 : 4; }
+
 template <bool BF16, int DK, int DVS, bool OUT, bool VEC>
-__global__ __launch_bounds__(la_threads(DVS), DK == 256 ? 2 : 4) void k_lattn_chunk(LattnCall a) {
+__global__ __launch_bounds__(la_threads(DVS), la_waves(BF16, DK, OUT)) void k_lattn_chunk(LattnCall a) {
     using M = Mm<BF16>;
     using T = typename M::T;
     using Frag = typename M::Frag;
