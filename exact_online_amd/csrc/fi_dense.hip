@@ -525,14 +525,11 @@ int best_tile(int64_t M, int64_t N, bool io_bf16, bool direct) {   // the larges
 }
 
 template <bool BF16>
-hipError_t run(DenseCall& c, hipStream_t st) {
-    constexpr int E = BF16 ? 8 : 4, BK = 8 * E;
+hipError_t run(const DenseCall& c, hipStream_t st) {
+    constexpr int E = BF16 ? 8 : 4;
     const auto whole = [](const void* p, int64_t ld) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % E == 0 && ld < (1 << 21); };
     const bool direct = whole(c.x, c.ldx) && whole(c.w, c.ldw);
-    c.splits = 1;
-    c.k_split = c.K;
     if (few_rows(c.M, c.N, c.K)) {
-        c.part = nullptr;
         const bool al = direct && c.K % E == 0;
         // 16 outputs for one wave, or for four or sixteen where there are fewer than
         // some eight waves for each CU (one row, us by 1 / 4 / 16: 131072 x 100
@@ -545,12 +542,6 @@ hipError_t run(DenseCall& c, hipStream_t st) {
         else few<BF16, 1, 16>(c, al, st);
         return hipGetLastError();
     }
-    const int64_t n = splits_of(c.M, c.N, c.K, BF16);
-    if (n > 1) {
-        c.k_split = ((c.K + n - 1) / n + BK - 1) / BK * BK;
-        c.splits = (int)((c.K + c.k_split - 1) / c.k_split);
-    }
-    if (c.splits == 1) c.part = nullptr;
     switch (c.splits > 1 ? 0 : best_tile(c.M, c.N, BF16, direct)) {
         case 0: tile<BF16, 64, 64, 2, 2, 3>(c, direct, st); break;
         case 1: tile<BF16, 128, 128, 2, 2, 2>(c, direct, st); break;
@@ -561,6 +552,16 @@ hipError_t run(DenseCall& c, hipStream_t st) {
 }
 
 }  // namespace
+
+void plan_dense(DenseCall& c) {
+    const int64_t n = splits_of(c.M, c.N, c.K, c.io_bf16), step = c.io_bf16 ? 64 : 32;   // K in whole steps of 128 bytes
+    c.ldp = (c.N + 7) / 8 * 8;
+    c.k_split = n > 1 ? ((c.K + n - 1) / n + step - 1) / step * step : c.K;
+    c.splits = (int)((c.K + c.k_split - 1) / c.k_split);
+    if (c.splits == 1) c.part = nullptr;
+}
+
+size_t dense_ws_used(const DenseCall& c) { return c.splits > 1 ? (size_t)c.splits * c.M * c.ldp * sizeof(float) : 0; }
 
 size_t dense_ws_bytes(int64_t M, int64_t N, int64_t K, int io_bf16) {
     int64_t most = 0;
@@ -573,7 +574,7 @@ size_t dense_ws_bytes(int64_t M, int64_t N, int64_t K, int io_bf16) {
 }
 
 hipError_t launch_dense(DenseCall c, hipStream_t st) {
-    c.ldp = (c.N + 7) / 8 * 8;
+    plan_dense(c);
     return c.io_bf16 ? run<true>(c, st) : run<false>(c, st);
 }
 

@@ -647,9 +647,18 @@ void chunk_launches(const LattnCall& c, hipStream_t st) {
 }
 
 template <bool BF16>
-hipError_t chunk_dims(LattnCall& c, hipStream_t st) {
-    const int cols = slice_cols(c.dk), slices = (c.dv + cols - 1) / cols;
-    c.nseg = segments(c.B * c.Hkv, slices, (c.L + la_chunk(BF16) - 1) / la_chunk(BF16), &c.seg_chunks);
+hipError_t chunk_dims(const LattnCall& c, hipStream_t st) {
+    if (c.dk <= 64) c.vec ? chunk_launches<BF16, 64, 64, true>(c, st) : chunk_launches<BF16, 64, 64, false>(c, st);
+    else if (c.dk <= 128) c.vec ? chunk_launches<BF16, 128, 128, true>(c, st) : chunk_launches<BF16, 128, 128, false>(c, st);
+    else c.vec ? chunk_launches<BF16, 256, 128, true>(c, st) : chunk_launches<BF16, 256, 128, false>(c, st);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+void plan_lattn(LattnCall& c) {
+    const int cols = slice_cols(c.dk), slices = (c.dv + cols - 1) / cols, C = la_chunk(c.io_bf16);
+    c.nseg = segments(c.B * c.Hkv, slices, (c.L + C - 1) / C, &c.seg_chunks);
     // A group's query heads go to workgroups of their own where the CUs are not
     // full without; each forms the state for itself, from the entry states' copy,
     // and the first writes it.  (A copy for this alone pays where every head gets
@@ -659,13 +668,9 @@ hipError_t chunk_dims(LattnCall& c, hipStream_t st) {
     const int64_t n = head_shares(c.B * c.Hkv * c.nseg * slices);
     c.hsplit = n >= c.G ? c.G : c.fresh || c.nseg > 1 ? (int)n : 1;
     c.entries = c.nseg > 1 || (c.hsplit > 1 && !c.fresh);
-    if (c.dk <= 64) c.vec ? chunk_launches<BF16, 64, 64, true>(c, st) : chunk_launches<BF16, 64, 64, false>(c, st);
-    else if (c.dk <= 128) c.vec ? chunk_launches<BF16, 128, 128, true>(c, st) : chunk_launches<BF16, 128, 128, false>(c, st);
-    else c.vec ? chunk_launches<BF16, 256, 128, true>(c, st) : chunk_launches<BF16, 256, 128, false>(c, st);
-    return hipGetLastError();
 }
 
-}  // namespace
+size_t lattn_ws_used(const LattnCall& c) { return c.entries ? (size_t)c.B * c.Hkv * c.nseg * c.dk * c.dv * sizeof(float) : 0; }
 
 size_t lattn_ws_bytes(int64_t B, int64_t L, int H, int Hkv, int dk, int dv, int io_bf16) {
     const int C = la_chunk(io_bf16), cols = slice_cols(dk), slices = (dv + cols - 1) / cols;
@@ -680,6 +685,7 @@ size_t lattn_ws_bytes(int64_t B, int64_t L, int H, int Hkv, int dk, int dv, int 
 }
 
 hipError_t launch_lattn_chunk(LattnCall c, hipStream_t st) {
+    plan_lattn(c);
     return c.io_bf16 ? chunk_dims<true>(c, st) : chunk_dims<false>(c, st);
 }
 

@@ -36,8 +36,11 @@ struct LattnCall {
 
 // One position (L = 1), recurrent form.
 hipError_t launch_lattn_step(const LattnCall &c, hipStream_t st);
-// Chunked form; sets the call's segments.  ws holds lattn_ws_bytes.
+// Chunked form; ws holds lattn_ws_bytes, which is the most that plan_lattn makes any
+// call of these sizes and smaller ones use.
 hipError_t launch_lattn_chunk(LattnCall c, hipStream_t st);
+void plan_lattn(LattnCall &c);   // segments, entry states, shares of query heads
+size_t lattn_ws_used(const LattnCall &c);
 size_t lattn_ws_bytes(int64_t B, int64_t L, int H, int Hkv, int dk, int dv, int io_bf16);
 
 // ------------------------------------------------------------ dense product
@@ -56,8 +59,11 @@ struct DenseCall {
     int splits;
 };
 
-// Chooses the kernel and the split; c.part holds dense_ws_bytes of the handle's M, N, K.
+// Chooses the kernel; c.part holds dense_ws_bytes of the handle's M, N, K, the most
+// that plan_dense makes a call of M rows or fewer use.
 hipError_t launch_dense(DenseCall c, hipStream_t st);
+void plan_dense(DenseCall &c);   // parts of K
+size_t dense_ws_used(const DenseCall &c);
 size_t dense_ws_bytes(int64_t M, int64_t N, int64_t K, int io_bf16);
 
 // ------------------------------------------------------------ token scores
@@ -79,6 +85,8 @@ struct ScoresCall {
 };
 
 hipError_t launch_scores(ScoresCall c, hipStream_t st);
-size_t scores_ws_parts(int64_t rows, int64_t V, int io_bf16);   // most rows x parts of a call
+void plan_scores(ScoresCall &c);   // a row's parts
+size_t scores_ws_used(const ScoresCall &c);                      // rows x parts of a call
+size_t scores_ws_parts(int64_t rows, int64_t V, int io_bf16);   // the most of any call of so many rows or fewer
 
 }  // namespace fi

@@ -457,8 +457,12 @@ size_t scores_ws_parts(int64_t rows, int64_t V, int io_bf16) {
     return (size_t)most;
 }
 
+void plan_scores(ScoresCall& c) { c.parts = parts_of(c.rows, c.V, c.io_bf16, &c.per); }
+
+size_t scores_ws_used(const ScoresCall& c) { return c.parts > 1 ? (size_t)c.rows * c.parts : 0; }
+
 hipError_t launch_scores(ScoresCall c, hipStream_t st) {
-    c.parts = parts_of(c.rows, c.V, c.io_bf16, &c.per);
+    plan_scores(c);
     const ScoresCall all = c;
     constexpr int64_t kRows = (int64_t)1 << 23;   // of one launch, which has at most 2^32 threads
     for (int64_t r = 0; r < all.rows; r += kRows) {
