@@ -27,8 +27,8 @@ constexpr int kRecHeads = 4;                             // query heads at a tim
 template <bool BF16, int RPT, bool VEC>
 __global__ __launch_bounds__(kRecThreads) void k_lattn_step(LattnCall a) {
     constexpr int ROWS = kRecRows * RPT, WAVES = kRecThreads / kWave;
-    __shared__ float ks[ROWS], vs[kRecCols], qs[kRecHeads][ROWS];
-    __shared__ __align__(16) float red[WAVES][kRecHeads][kRecCols];
+    __shared__ float ks[ROWS], qs[kRecHeads][ROWS];
+    __shared__ __align__(16) float vs[kRecCols], red[WAVES][kRecHeads][kRecCols];   // read in 16-byte units
     const int tid = threadIdx.x, c = tid % (kRecCols / 4), r = tid / (kRecCols / 4);
     const int slices = (a.dv + kRecCols - 1) / kRecCols;
     const int64_t b = blockIdx.x / slices / a.Hkv;
