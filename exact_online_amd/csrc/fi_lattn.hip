@@ -161,7 +161,7 @@ hipError_t launch_lattn_step(const LattnCall& c, hipStream_t st) {
 // enter as two bf16 parts each, off by 2^-16 of them at most: o is the formula's value
 // rounded once (0.0001 of its norm from that; with one part each 0.0025, which is more
 // than the rounding itself, and what the step does to the same state would be another
-// number; 64K x 16 heads 397 -> 445 us, ragged rows 122 -> 133, one row of 77 8.3 -> 9.0).
+// number; 64K x 16 heads 397 -> 429 us, ragged rows 122 -> 130, one row of 77 8.3 -> 8.7).
 // V's decayed rows go into S in three parts, exactly, so that S keeps fp32's
 // precision over any number of chunks.
 //
@@ -376,7 +376,10 @@ __global__ __launch_bounds__(la_threads(DVS), la_waves(BF16, DK, OUT)) void k_la
         // the next chunk's rows (the last one's again at the end: no branch,
         // so that nothing waits for them before their use)
         const int ahead = c + 1 < c1 ? c + 1 : c;
-        fetch(fk, kp, a.k.pos, ahead, krow, RK, klcol, kleft);
+        // (K's rows beside V's where registers are short: of 128 columns they went to
+        // scratch as soon as they came, 64K x 16 heads 446 us, 429 so; of 256 1% the other way)
+        constexpr bool LATE = OUT && DK <= 128;
+        if constexpr (!LATE) fetch(fk, kp, a.k.pos, ahead, krow, RK, klcol, kleft);
         if constexpr (!OUT) fetch(fv, vp, a.v.pos, ahead, vrow, RV, vlcol, vleft);
         if constexpr (OUT) {
             for (int h = h0; h < h1; ++h) {
@@ -494,6 +497,7 @@ __global__ __launch_bounds__(la_threads(DVS), la_waves(BF16, DK, OUT)) void k_la
                 }
             }
         }
+        if constexpr (LATE) fetch(fk, kp, a.k.pos, ahead, krow, RK, klcol, kleft);
         if constexpr (OUT) fetch(fv, vp, a.v.pos, ahead, vrow, RV, vlcol, vleft);
         // S: its decay as S + (lam^C - 1) S (lam^C's rounding would add up
         // over the chunks of a long memory), then the chunk's own products
