@@ -132,7 +132,7 @@ __device__ __forceinline__ void dense_mma(V16 (&acc)[TN][TM], const typename Mm<
 // meet every bank once.
 //
 // bf16, 256 x 256: 8192^3 888 us (1240 TFLOP/s, the library's 1411), 16384 x 4096
-// x 1024 157 us, and 180 to 192 with bias and GELU.  The product itself keeps the
+// x 1024 157 us, and 181 to 186 with bias and GELU.  The product itself keeps the
 // matrix cores as busy as the power limit leaves them (clock 1.5 to 1.9 GHz);
 // then a tile's end, which the next tile of the CU waits for: stores (128 KB of
 // every CU at once: 7 us), GELU (17 operations and two transcendental ones for each
@@ -366,7 +366,9 @@ __global__ __launch_bounds__(256) void k_dense_join(DenseCall a) {
 // operands; KW waves of a workgroup split K of 16 outputs between them.  Bound
 // by w: one row, 32768 x 1024, bf16: 11.9 us (5.6 TB/s: some of w is still in the
 // last-level cache), 131072 x 1024: 40 us (6.7 TB/s).  Eight steps' loads (four with
-// sixteen waves) are in flight at once.
+// sixteen waves) are in flight at once.  (For 17 to 32 rows that is more than the 128
+// registers of a lane of sixteen waves: 22 of them go to scratch, and the figures at
+// few_rows are measured so.)
 template <bool BF16, int MT, int KW, bool ALIGNED>
 __global__ __launch_bounds__((KW > 4 ? KW : 4) * kWave) void k_dense_few(DenseCall a) {
     using M = Mm<BF16>;

@@ -154,8 +154,8 @@ hipError_t launch_lattn_step(const LattnCall& c, hipStream_t st) {
 // Split: a wave's columns of S stay in its registers from chunk to chunk, and
 // S is the operand of both of its products as it lies there; the waves meet
 // only in P, whose tiles they share out.  Waves with 32 columns (operands used
-// twice, half the waves) took 303 us where these take 297, and 132 where these
-// take 91 (ragged rows, four heads a group).
+// twice, half the waves) took 303 us where these took 297, and 132 where these
+// took 91 (ragged rows, four heads a group; both with one part of P and E).
 //
 // Roundings (bf16): the operands of the products are bf16, so P and, in Q E, E
 // enter as two bf16 parts each, off by 2^-16 of them at most: o is the formula's value
@@ -165,12 +165,13 @@ hipError_t launch_lattn_step(const LattnCall& c, hipStream_t st) {
 // V's decayed rows go into S in three parts, exactly, so that S keeps fp32's
 // precision over any number of chunks.
 //
-// Measured: 16 heads of 128 x 128, 65536 positions, bf16: 400 us (1.07 GB once:
-// 2.7 TB/s): local states 130, scan 15, outputs 255 to 297.  The outputs keep
-// the vector units busy 42%, LDS 35% and the matrix cores 28% of the time with 3.2
-// waves a SIMD: bound by the chain of a chunk (operands to LDS, P, O, S, four
-// barriers), which two workgroups on a CU overlap.  fp32, two rows of 4001, 16
-// heads of 64 x 64: 60 us, outputs 41, bound by the same chain (matrix cores 40%).
+// Measured: 16 heads of 128 x 128, 65536 positions, bf16: 429 us (1.07 GB once:
+// 2.5 TB/s): local states 115 to 135, scan 15, outputs 293 to 350.  The outputs keep
+// the vector units busy 51%, LDS 35% and the matrix cores 32% of the time with 3.1
+// waves a SIMD: none of them is full, and a wave goes through a chunk one phase after
+// the other (operands to LDS, P, O, S, four barriers), which two workgroups on a CU
+// overlap in part.  fp32, two rows of 4001, 16 heads of 64 x 64: 61 us, outputs 41
+// (matrix cores 41%).
 constexpr int la_chunk(bool bf16) { return bf16 ? 64 : 32; }   // positions of a chunk
 constexpr int la_threads(int dvs) { return dvs / 16 * kWave; }
 

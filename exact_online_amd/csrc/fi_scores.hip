@@ -246,12 +246,12 @@ struct Best {
 // reductions then cost one wave's steps, once: with a workgroup to a row 4096 x
 // 32768 took 76 us.
 //
-// Measured, bf16: 4096 x 32768, k = 5: 62 us (268 MB, 4.3 TB/s; a copy's 4.9 would take
-// 55), the vector units 64% busy with an exponential, two fused operations and
-// a maximum for each logit; 333 x 100003, nine in ten masked, k = 8: 31 us (67 MB), 26 in
+// Measured, bf16: 4096 x 32768, k = 5: 63.6 us (268 MB, 4.2 TB/s; a copy's 4.9 would take
+// 55), the vector units 65% busy with an exponential, two fused operations and
+// a maximum for each logit; 333 x 100003, nine in ten masked, k = 8: 31.8 us (67 MB), 27 in
 // this kernel, where some ten batches a wave do not hide its beginning
-// (threshold, first ranking) and end.  fp32, one row of 131072, k = 20: 6.4 us here,
-// 4.7 in the join: two launches and their trips to memory.
+// (threshold, first ranking) and end.  fp32, one row of 131072, k = 20: 6.3 us here,
+// 4.5 in the join: two launches and their trips to memory.
 template <bool BF16>
 __global__ __launch_bounds__(kScThreads) void k_scores(ScoresCall a) {
     using M = Mm<BF16>;
@@ -429,7 +429,8 @@ __global__ __launch_bounds__(kScThreads) void k_scores_join(ScoresCall a) {
 
 namespace {
 
-// Waves wanted of a launch: two for each SIMD.  us with 4096 / 2048 / 1024, bf16: 1099
+// Waves wanted of a launch: two for each SIMD, at most (whole parts of a row: 1025 rows and
+// more are one each).  us with 4096 / 2048 / 1024, bf16: 1099
 // rows of 9067, k = 5: 18.1 / 17.0 / 16.5; 333 of 100003: 28.8 / 30.9 / 38.3, and with
 // k = 32 54.6 / 46.9 / 52.6; 95 of 54733, k = 0: 10.0 / 9.0 / 8.5.
 constexpr int kScPartsWanted = 2048;
