@@ -26,6 +26,10 @@ __all__ = [
     "fi_lattn_destroy", "LinearAttention", "fi_dense_config", "fi_dense_args", "fi_dense_create", "fi_dense_run",
     "fi_dense_destroy", "Dense", "fi_scores_config", "fi_scores_args", "fi_scores_create", "fi_scores_run",
     "fi_scores_destroy", "TokenScores",
+    "fi_delta_config", "fi_delta_args", "fi_delta_create", "fi_delta_prompt", "fi_delta_step", "fi_delta_destroy",
+    "DeltaRule", "FI_NORM_NONE", "FI_NORM_RMS", "FI_NORM_L2", "FI_PAIRS_HALVES", "FI_PAIRS_ADJACENT",
+    "fi_rotary_config", "fi_rotary_args", "fi_rotary_create", "fi_rotary_run", "fi_rotary_destroy", "Rotary",
+    "fi_verify_config", "fi_verify_args", "fi_verify_create", "fi_verify_run", "fi_verify_destroy", "DraftCheck",
 ]
 
 FI_F32, FI_BF16 = 0, 1
@@ -57,8 +61,12 @@ EXPORTS = ("fi_create", "fi_step", "fi_run_closed_loop", "fi_run_prompted", "fi_
            "fi_position", "fi_strerror", "fi_tile_at", "fi_conv_static", "fi_stack_create", "fi_stack_run",
            "fi_stack_destroy", "fi_lattn_create", "fi_lattn_prompt", "fi_lattn_step", "fi_lattn_destroy",
            "fi_dense_create", "fi_dense_run", "fi_dense_destroy", "fi_scores_create", "fi_scores_run",
-           "fi_scores_destroy")
+           "fi_scores_destroy", "fi_delta_create", "fi_delta_prompt", "fi_delta_step", "fi_delta_destroy",
+           "fi_rotary_create", "fi_rotary_run", "fi_rotary_destroy", "fi_verify_create", "fi_verify_run",
+           "fi_verify_destroy")
 FI_ACT_GELU, FI_ACT_TANH, FI_ACT_IDENTITY = 0, 1, 2
+FI_NORM_NONE, FI_NORM_RMS, FI_NORM_L2 = 0, 1, 2
+FI_PAIRS_HALVES, FI_PAIRS_ADJACENT = 0, 1
 FI_STATIC_WORKSPACE_BYTES = 64 << 20
 
 
@@ -118,6 +126,44 @@ class fi_scores_args(ctypes.Structure):
                 ("lse", ctypes.c_void_p), ("top", ctypes.c_void_p), ("top_id", ctypes.c_void_p)]
 
 
+class fi_delta_config(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int64), ("L", ctypes.c_int64), ("Hk", ctypes.c_int64), ("Hv", ctypes.c_int64),
+                ("dk", ctypes.c_int64), ("dv", ctypes.c_int64), ("scale", ctypes.c_float),
+                ("io_dtype", ctypes.c_int32), ("stream", ctypes.c_void_p)]
+
+
+class fi_delta_args(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int64), ("L", ctypes.c_int64), ("q", fi_view), ("k", fi_view), ("v", fi_view),
+                ("o", fi_view), ("log_decay", fi_view), ("beta", fi_view), ("lens", ctypes.c_void_p),
+                ("slots", ctypes.c_void_p), ("n_slots", ctypes.c_int64), ("state", ctypes.c_void_p),
+                ("fresh", ctypes.c_int32), ("hold", ctypes.c_int32)]
+
+
+class fi_rotary_config(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int64), ("L", ctypes.c_int64), ("Hq", ctypes.c_int64), ("Hk", ctypes.c_int64),
+                ("d", ctypes.c_int64), ("rot", ctypes.c_int64), ("norm", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("pairs", ctypes.c_int32), ("io_dtype", ctypes.c_int32), ("stream", ctypes.c_void_p)]
+
+
+class fi_rotary_args(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int64), ("L", ctypes.c_int64), ("q", fi_view), ("k", fi_view), ("qo", fi_view),
+                ("ko", fi_view), ("wq", ctypes.c_void_p), ("wk", ctypes.c_void_p), ("first", ctypes.c_void_p),
+                ("positions", ctypes.c_void_p)]
+
+
+class fi_verify_config(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int64), ("N", ctypes.c_int64), ("V", ctypes.c_int64), ("io_dtype", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("draft_scale", ctypes.c_float), ("stream", ctypes.c_void_p)]
+
+
+class fi_verify_args(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int64), ("N", ctypes.c_int64), ("target", ctypes.c_void_p),
+                ("target_row", ctypes.c_int64), ("target_ld", ctypes.c_int64), ("draft", ctypes.c_void_p),
+                ("draft_row", ctypes.c_int64), ("draft_ld", ctypes.c_int64), ("tokens", ctypes.c_void_p),
+                ("lens", ctypes.c_void_p), ("u", ctypes.c_void_p), ("r", ctypes.c_void_p), ("out", ctypes.c_void_p),
+                ("kept", ctypes.c_void_p), ("logprob", ctypes.c_void_p)]
+
+
 _H = ctypes.c_void_p
 lib.fi_create.argtypes = [ctypes.POINTER(fi_config), ctypes.c_void_p, ctypes.POINTER(_H)]
 lib.fi_create.restype = ctypes.c_int
@@ -159,7 +205,20 @@ lib.fi_scores_create.argtypes = [ctypes.POINTER(fi_scores_config), ctypes.POINTE
 lib.fi_scores_create.restype = ctypes.c_int
 lib.fi_scores_run.argtypes = [_H, ctypes.POINTER(fi_scores_args)]
 lib.fi_scores_run.restype = ctypes.c_int
-for _f in (lib.fi_lattn_destroy, lib.fi_dense_destroy, lib.fi_scores_destroy):
+lib.fi_delta_create.argtypes = [ctypes.POINTER(fi_delta_config), ctypes.POINTER(_H)]
+lib.fi_delta_create.restype = ctypes.c_int
+lib.fi_delta_prompt.argtypes = lib.fi_delta_step.argtypes = [_H, ctypes.POINTER(fi_delta_args)]
+lib.fi_delta_prompt.restype = lib.fi_delta_step.restype = ctypes.c_int
+lib.fi_rotary_create.argtypes = [ctypes.POINTER(fi_rotary_config), ctypes.c_void_p, ctypes.POINTER(_H)]
+lib.fi_rotary_create.restype = ctypes.c_int
+lib.fi_rotary_run.argtypes = [_H, ctypes.POINTER(fi_rotary_args)]
+lib.fi_rotary_run.restype = ctypes.c_int
+lib.fi_verify_create.argtypes = [ctypes.POINTER(fi_verify_config), ctypes.POINTER(_H)]
+lib.fi_verify_create.restype = ctypes.c_int
+lib.fi_verify_run.argtypes = [_H, ctypes.POINTER(fi_verify_args)]
+lib.fi_verify_run.restype = ctypes.c_int
+for _f in (lib.fi_lattn_destroy, lib.fi_dense_destroy, lib.fi_scores_destroy, lib.fi_delta_destroy,
+           lib.fi_rotary_destroy, lib.fi_verify_destroy):
     _f.argtypes, _f.restype = [_H], None
 # only in the phase-timing build (include/fi_profile.h)
 HAS_PROFILE = hasattr(lib, "fi_profile_read")
@@ -333,6 +392,46 @@ def fi_scores_destroy(s) -> None:
     lib.fi_scores_destroy(s)
 
 
+def fi_delta_create(cfg: fi_delta_config) -> int:
+    return _create(lib.fi_delta_create, "fi_delta_create", ctypes.byref(cfg))
+
+
+def fi_delta_prompt(s: int, args: fi_delta_args) -> None:
+    _check(lib.fi_delta_prompt(s, args), "fi_delta_prompt")
+
+
+def fi_delta_step(s: int, args: fi_delta_args) -> None:
+    _check(lib.fi_delta_step(s, args), "fi_delta_step")
+
+
+def fi_delta_destroy(s) -> None:
+    lib.fi_delta_destroy(s)
+
+
+def fi_rotary_create(cfg: fi_rotary_config, inv_freq) -> int:
+    return _create(lib.fi_rotary_create, "fi_rotary_create", ctypes.byref(cfg), _ptr(inv_freq))
+
+
+def fi_rotary_run(s: int, args: fi_rotary_args) -> None:
+    _check(lib.fi_rotary_run(s, args), "fi_rotary_run")
+
+
+def fi_rotary_destroy(s) -> None:
+    lib.fi_rotary_destroy(s)
+
+
+def fi_verify_create(cfg: fi_verify_config) -> int:
+    return _create(lib.fi_verify_create, "fi_verify_create", ctypes.byref(cfg))
+
+
+def fi_verify_run(s: int, args: fi_verify_args) -> None:
+    _check(lib.fi_verify_run(s, args), "fi_verify_run")
+
+
+def fi_verify_destroy(s) -> None:
+    lib.fi_verify_destroy(s)
+
+
 class _Owner:
     """Owns one handle; `_destroy` frees it."""
 
@@ -504,6 +603,169 @@ class TokenScores(_Owner):
                            *(_dense(x, f32, rows, where) for x in (logprob, entropy, lse)),
                            _dense(top, f32, rows * self.k, where), _dense(top_id, i64, rows * self.k, where))
         _check(lib.fi_scores_run(self.handle, a), where)
+
+
+def _device() -> int:
+    """The device that a handle made now runs on (0 where there is none: the create calls refuse then)."""
+    cuda = _torch("cuda")
+    return cuda.current_device() if cuda.is_available() else 0
+
+
+def _on(x, dtype, n, device, where) -> int:
+    """The address of a dense tensor of at least n elements of this type on the device, or 0 for None."""
+    if x is None:
+        return 0
+    if x.dtype is not dtype or x.get_device() != device or not x.is_contiguous() or x.numel() < n:
+        _refuse(where)
+    return x.data_ptr()
+
+
+_DELTA_ARGS = struct.Struct("@2q" + "P3q" * 6 + "2PqP2i")
+
+
+class DeltaRule(_Owner):
+    """The gated delta rule over the caller's states (marshalling only).  q and
+    k are tensors [B, L, Hk, dk], v and o [B, L, Hv, dv] of the io type, of any
+    strides as long as a head's elements are adjacent; log_decay and beta are
+    fp32 [B, L, Hv] of any strides; state is [slots, Hv, dk, dv], fp32 and
+    contiguous, updated in place (with hold: read only); lens and slots are int32
+    tensors [B].  All are on the handle's device, the one that was current when it was made;
+    other shapes, types, strides and devices are refused."""
+
+    _destroy = staticmethod(fi_delta_destroy)
+
+    def __init__(self, B, L, Hk, Hv, dk, dv, scale=1.0, io_dtype=FI_BF16, stream=None):
+        self.cfg = fi_delta_config(B=int(B), L=int(L), Hk=int(Hk), Hv=int(Hv), dk=int(dk), dv=int(dv),
+                                   scale=float(scale), io_dtype=int(io_dtype), stream=_stream(stream))
+        self._is = (int(Hk), int(Hv), int(dk), int(dv), _io_type(io_dtype), _torch("float32"), _torch("int32"), _device())
+        self._args = fi_delta_args()
+        self.handle = fi_delta_create(self.cfg)
+
+    def _call(self, fn, where, q, k, v, log_decay, beta, o, state, lens, slots, fresh, hold):
+        shape = q.shape
+        B, L = shape[0], shape[1]
+        Hk, Hv, dk, dv, io, f32, i32, dev = self._is
+        qs, ks, vs, os_, gs, bs = q.stride(), k.stride(), v.stride(), o.stride(), log_decay.stride(), beta.stride()
+        values, gates = (B, L, Hv, dv), (B, L, Hv)
+        if (shape != (B, L, Hk, dk) or k.shape != shape or v.shape != values or o.shape != values
+                or log_decay.shape != gates or beta.shape != gates
+                or (dk > 1 and (qs[3] != 1 or ks[3] != 1)) or (dv > 1 and (vs[3] != 1 or os_[3] != 1))
+                or q.dtype is not io or k.dtype is not io or v.dtype is not io or o.dtype is not io
+                or log_decay.dtype is not f32 or beta.dtype is not f32
+                or q.get_device() != dev or k.get_device() != dev or v.get_device() != dev or o.get_device() != dev
+                or log_decay.get_device() != dev or beta.get_device() != dev):
+            _refuse(where)
+        n_slots = states = 0
+        if state is not None:
+            shape = state.shape
+            n_slots = shape[0] if shape else 0
+            if (shape != (n_slots, Hv, dk, dv) or state.dtype is not f32 or state.get_device() != dev
+                    or not state.is_contiguous()):
+                _refuse(where)
+            states = state.data_ptr()
+        # the struct's fields in their order (fi_delta_args, native layout)
+        _DELTA_ARGS.pack_into(
+            self._args, 0, B, L, q.data_ptr(), qs[0], qs[1], qs[2], k.data_ptr(), ks[0], ks[1], ks[2],
+            v.data_ptr(), vs[0], vs[1], vs[2], o.data_ptr(), os_[0], os_[1], os_[2],
+            log_decay.data_ptr(), gs[0], gs[1], gs[2], beta.data_ptr(), bs[0], bs[1], bs[2],
+            0 if lens is None else _on(lens, i32, B, dev, where), 0 if slots is None else _on(slots, i32, B, dev, where),
+            n_slots, states, 1 if fresh else 0, 1 if hold else 0)
+        status = fn(self.handle, self._args)
+        if status < 0:
+            raise FiError(status, where)
+
+    def prompt(self, q, k, v, log_decay, beta, o, state=None, lens=None, slots=None, fresh=False, hold=False):
+        self._call(lib.fi_delta_prompt, "fi_delta_prompt", q, k, v, log_decay, beta, o, state, lens, slots, fresh, hold)
+
+    def step(self, q, k, v, log_decay, beta, o, state, slots=None, hold=False):
+        self._call(lib.fi_delta_step, "fi_delta_step", q, k, v, log_decay, beta, o, state, None, slots, False, hold)
+
+
+_ROTARY_ARGS = struct.Struct("@2q" + "P3q" * 4 + "4P")
+
+
+class Rotary(_Owner):
+    """Queries and keys normed for each head and turned by their position, in
+    one pass (marshalling only).  q and qo are tensors [B, L, Hq, d], k and ko [B, L,
+    Hk, d] of the io type, of any strides as long as a head's elements are adjacent;
+    qo and ko may be q and k themselves.  inv_freq is fp32 [rot / 2], its length says how much of a
+    head is turned (None: nothing is); wq and wk are [d] of the io type; first
+    is int32 [B] or positions int32 [B, L].  All are on the handle's device, the
+    one that was current when it was made; others are refused."""
+
+    _destroy = staticmethod(fi_rotary_destroy)
+
+    def __init__(self, B, L, Hq, Hk, d, inv_freq, norm=FI_NORM_RMS, eps=1e-6, pairs=FI_PAIRS_HALVES, io_dtype=FI_BF16, stream=None):
+        n = 0 if inv_freq is None else inv_freq.numel()
+        self.cfg = fi_rotary_config(B=int(B), L=int(L), Hq=int(Hq), Hk=int(Hk), d=int(d), rot=2 * n, norm=int(norm),
+                                    eps=float(eps), pairs=int(pairs), io_dtype=int(io_dtype), stream=_stream(stream))
+        dev = _device()
+        self._is = (int(Hq), int(Hk), int(d), _io_type(io_dtype), _torch("int32"), dev)
+        self._args = fi_rotary_args()
+        self.handle = fi_rotary_create(self.cfg, _on(inv_freq, _torch("float32"), n, dev, "fi_rotary_create") if n else None)
+
+    def run(self, q, k, qo, ko, wq=None, wk=None, first=None, positions=None):
+        where = "fi_rotary_run"
+        Hq, Hk, d, io, i32, dev = self._is
+        shape = q.shape
+        B, L = shape[0], shape[1]
+        qs, qos = q.stride(), qo.stride()
+        if (shape != (B, L, Hq, d) or qo.shape != shape or (d > 1 and (qs[3] != 1 or qos[3] != 1))
+                or q.dtype is not io or qo.dtype is not io or q.get_device() != dev or qo.get_device() != dev):
+            _refuse(where)
+        kp = kop = 0
+        ks = kos = (0, 0, 0)
+        if Hk:
+            ks, kos, shape = k.stride(), ko.stride(), (B, L, Hk, d)
+            if (k.shape != shape or ko.shape != shape or (d > 1 and (ks[3] != 1 or kos[3] != 1))
+                    or k.dtype is not io or ko.dtype is not io or k.get_device() != dev or ko.get_device() != dev):
+                _refuse(where)
+            kp, kop = k.data_ptr(), ko.data_ptr()
+        # the struct's fields in their order (fi_rotary_args, native layout)
+        _ROTARY_ARGS.pack_into(
+            self._args, 0, B, L, q.data_ptr(), qs[0], qs[1], qs[2], kp, ks[0], ks[1], ks[2],
+            qo.data_ptr(), qos[0], qos[1], qos[2], kop, kos[0], kos[1], kos[2],
+            0 if wq is None else _on(wq, io, d, dev, where), 0 if wk is None else _on(wk, io, d, dev, where),
+            0 if first is None else _on(first, i32, B, dev, where),
+            0 if positions is None else _on(positions, i32, B * L, dev, where))
+        status = lib.fi_rotary_run(self.handle, self._args)
+        if status < 0:
+            raise FiError(status, where)
+
+
+class DraftCheck(_Owner):
+    """Drafted tokens against the target's probabilities (marshalling only):
+    target [B, N + 1, V] and draft [B, N, V] (or None: certain drafts), logits of the
+    io type, rows of any strides; tokens int64 [B, N], u fp32 [B, N], r fp32 [B];
+    out int64 [B, N + 1], kept int32 [B], logprob fp32 [B, N + 1] or None; lens int32 [B] or None.
+    All but the logits are contiguous, and all are on the handle's device, the one that was
+    current when it was made; others are refused."""
+
+    _destroy = staticmethod(fi_verify_destroy)
+
+    def __init__(self, B, N, V, io_dtype=FI_BF16, scale=1.0, draft_scale=None, stream=None):
+        self.cfg = fi_verify_config(B=int(B), N=int(N), V=int(V), io_dtype=int(io_dtype), scale=float(scale),
+                                    draft_scale=float(scale if draft_scale is None else draft_scale), stream=_stream(stream))
+        self._is = (int(V), _io_type(io_dtype), _torch("float32"), _torch("int32"), _torch("int64"), _device())
+        self.handle = fi_verify_create(self.cfg)
+
+    def run(self, target, tokens, u, r, out, kept, logprob=None, draft=None, lens=None):
+        where = "fi_verify_run"
+        V, io, f32, i32, i64, dev = self._is
+        B, N = target.shape[0], target.shape[1] - 1
+
+        def logits(x, n):
+            s = x.stride()
+            if (x.shape != (B, n, V) or (V > 1 and s[2] != 1) or x.dtype is not io or x.get_device() != dev):
+                _refuse(where)
+            return x.data_ptr(), s[0], s[1]
+        if tokens.shape != (B, N) or u.shape != (B, N) or out.shape != (B, N + 1):
+            _refuse(where)
+        a = fi_verify_args(B, N, *logits(target, N + 1), *((0, 0, 0) if draft is None else logits(draft, N)),
+                           _on(tokens, i64, B * N, dev, where), _on(lens, i32, B, dev, where), _on(u, f32, B * N, dev, where),
+                           _on(r, f32, B, dev, where), _on(out, i64, B * (N + 1), dev, where), _on(kept, i32, B, dev, where),
+                           _on(logprob, f32, B * (N + 1), dev, where))
+        _check(lib.fi_verify_run(self.handle, a), where)
 
 
 def fi_profile_read(s: int):

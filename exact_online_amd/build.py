@@ -14,7 +14,7 @@ CSRC = PKG / "csrc"
 LIB = PKG / "libfi.so"
 PROFILE_LIB = PKG / "libfi_prof.so"   # the phase-timing build (-DFI_PROFILE=1), for bench.py --phases
 SOURCES = [CSRC / "fi_kernels.hip", CSRC / "fi_lattn.hip", CSRC / "fi_dense.hip", CSRC / "fi_scores.hip",
-           CSRC / "fi_api.cpp", CSRC / "fi_operators.cpp"]
+           CSRC / "fi_delta.hip", CSRC / "fi_rotary.hip", CSRC / "fi_verify.hip", CSRC / "fi_api.cpp", CSRC / "fi_operators.cpp"]
 HEADERS = [ROOT / "include" / "fi.h", ROOT / "include" / "fi_profile.h", CSRC / "fi_internal.h",
            CSRC / "fi_device.hpp", CSRC / "fi_host.h", CSRC / "fi_operators.h", CSRC / "fi_opdev.hpp"]
 
@@ -47,7 +47,7 @@ def build(verbose: bool = False, out: Path | None = None, extra: list | None = N
                 sys.stderr.write("\n".join(rest) + "\n")
 
     # one object per source, side by side, then the link
-    with tempfile.TemporaryDirectory() as d, ThreadPoolExecutor(max_workers=4) as ex:
+    with tempfile.TemporaryDirectory() as d, ThreadPoolExecutor(max_workers=8) as ex:
         objs = [str(Path(d) / (p.name + ".o")) for p in SOURCES]
         list(ex.map(run, [[HIPCC, *flags, "-c", str(p), "-o", o] for p, o in zip(SOURCES, objs)]))
         run([HIPCC, *flags, "-shared", "-o", str(tmp), *objs])

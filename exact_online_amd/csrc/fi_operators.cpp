@@ -1,6 +1,6 @@
 // fi_operators.cpp -- host side of the operators around the mixers
-// (fi_lattn_*, fi_dense_*, fi_scores_* of include/fi.h): argument checks,
-// workspaces and launches.
+// (fi_lattn_*, fi_dense_*, fi_scores_*, fi_delta_*, fi_rotary_*, fi_verify_* of
+// include/fi.h): argument checks, workspaces and launches.
 #include "fi_operators.h"
 
 #include <hip/hip_runtime_api.h>
@@ -34,6 +34,26 @@ struct fi_scores {
     unsigned long long *pkey;
 };
 
+struct fi_delta {
+    fi_delta_config cfg;
+    hipStream_t stream;
+    int device;
+};
+
+struct fi_rotary {
+    fi_rotary_config cfg;
+    hipStream_t stream;
+    int device;
+    double *turns;   // [rot / 2], device
+};
+
+struct fi_verify {
+    fi_verify_config cfg;
+    hipStream_t stream;
+    int device;
+    double *ws;      // sums of rows' parts
+};
+
 namespace {
 
 constexpr int64_t kLim = (int64_t)1 << 31;
@@ -59,6 +79,20 @@ bool fits(std::initializer_list<int64_t> f, int64_t most) {
     }
     return true;
 }
+
+// The handle's device is the current one as long as this lives.
+struct OnDevice {
+    int before = -1;
+    hipError_t error;
+    explicit OnDevice(int device) {
+        error = hipGetDevice(&before);
+        if (error != hipSuccess || before == device) before = -1;
+        else error = hipSetDevice(device);
+    }
+    ~OnDevice() {
+        if (before >= 0) (void)hipSetDevice(before);
+    }
+};
 
 }  // namespace
 
@@ -284,6 +318,276 @@ void fi_scores_destroy(fi_scores *s) {
     if (s->pst) (void)hipFree(s->pst);
     if (s->pkey) (void)hipFree(s->pkey);
     delete s;
+}
+
+// ------------------------------------------------------------ gated delta rule
+int fi_delta_create(const fi_delta_config *cfg, fi_delta **out) {
+    if (out) *out = nullptr;
+    if (!cfg || !out) return FI_ERR_INVALID;
+    if (cfg->B < 1 || cfg->L < 1 || cfg->Hk < 1 || cfg->Hv < 1 || cfg->dk < 1 || cfg->dv < 1) return FI_ERR_INVALID;
+    if (cfg->B >= kLim || cfg->L >= kLim || cfg->Hv >= kLim) return FI_ERR_INVALID;
+    if (cfg->Hv % cfg->Hk != 0 || !std::isfinite(cfg->scale) || !dtype_ok(raw_int(cfg->io_dtype))) return FI_ERR_INVALID;
+    if (!fits({cfg->B, cfg->L, cfg->Hv, cfg->dk}, kMaxCount) || !fits({cfg->B, cfg->L, cfg->Hv, cfg->dv}, kMaxCount))
+        return FI_ERR_INVALID;
+    if (cfg->dk > kMaxHead || cfg->dv > kMaxHead || cfg->L > FI_MAX_L || cfg->B > kLattnMaxRows / cfg->Hv)
+        return FI_ERR_UNSUPPORTED;
+    const int rc = check_device();
+    if (rc != FI_OK) return rc;
+    fi_delta *s = new (std::nothrow) fi_delta();
+    if (!s) return FI_ERR_NOMEM;
+    s->cfg = *cfg;
+    s->stream = static_cast<hipStream_t>(cfg->stream);
+    const hipError_t e = hipGetDevice(&s->device);
+    if (e != hipSuccess) {
+        delete s;
+        return hip_fail(e);
+    }
+    *out = s;
+    return FI_OK;
+}
+
+void fi_delta_destroy(fi_delta *s) {
+    if (!s) return;
+    const OnDevice here(s->device);
+    (void)hipStreamSynchronize(s->stream);
+    delete s;
+}
+
+}  // extern "C"
+
+namespace {
+
+int delta_call(const fi_delta *s, const fi_delta_args *a, DeltaCall &c) {
+    if (!s || !a) return FI_ERR_INVALID;
+    const fi_delta_config &f = s->cfg;
+    if (a->B < 0 || a->B > f.B || a->L < 0 || a->L > f.L) return FI_ERR_INVALID;
+    const int dt = raw_int(f.io_dtype), es = esize(dt);
+    const bool some = a->B > 0 && a->L > 0;   // an empty call's arrays may be NULL
+    for (const fi_view *v : {&a->q, &a->k, &a->v, &a->o})
+        if ((some && !v->p) || !aligned(v->p, es)) return FI_ERR_INVALID;
+    for (const fi_view *v : {&a->log_decay, &a->beta})
+        if ((some && !v->p) || !aligned(v->p, 4)) return FI_ERR_INVALID;
+    if ((!a->state && !a->fresh) || !aligned(a->state, 16) || !aligned(a->lens, 4) || !aligned(a->slots, 4))
+        return FI_ERR_INVALID;
+    if (a->n_slots < 0 || a->n_slots >= kLim || (!a->slots && a->state && a->n_slots < a->B)) return FI_ERR_INVALID;
+    c = {};
+    c.B = a->B;
+    c.L = (int)a->L;
+    c.Hk = (int)f.Hk;
+    c.Hv = (int)f.Hv;
+    c.G = (int)(f.Hv / f.Hk);
+    c.dk = (int)f.dk;
+    c.dv = (int)f.dv;
+    c.scale = f.scale;
+    c.io_bf16 = dt == FI_BF16;
+    c.fresh = a->fresh != 0;
+    c.hold = a->hold != 0;
+    c.vec = view_vec(a->q, f.dk, es) && view_vec(a->k, f.dk, es) && view_vec(a->v, f.dv, es) && view_vec(a->o, f.dv, es);
+    auto view = [](const fi_view &v) { return View{v.p, v.row, v.pos, v.head}; };
+    c.q = view(a->q);
+    c.k = view(a->k);
+    c.v = view(a->v);
+    c.o = view(a->o);
+    c.ld = view(a->log_decay);
+    c.beta = view(a->beta);
+    c.lens = a->lens;
+    c.slots = a->slots;
+    c.n_slots = a->state ? a->n_slots : kLim;   // without states every slot is fine
+    c.state = a->state;
+    return FI_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int fi_delta_prompt(fi_delta *s, const fi_delta_args *a) {
+    DeltaCall c;
+    const int rc = delta_call(s, a, c);
+    if (rc != FI_OK || c.B == 0) return rc;
+    const OnDevice here(s->device);
+    FI_HIP(here.error);
+    FI_HIP(launch_delta_step(c, s->stream));
+    return FI_OK;
+}
+
+int fi_delta_step(fi_delta *s, const fi_delta_args *a) {
+    DeltaCall c;
+    const int rc = delta_call(s, a, c);
+    if (rc != FI_OK) return rc;
+    if (a->L != 1 || a->lens) return FI_ERR_INVALID;
+    if (c.B == 0) return FI_OK;
+    if (!c.state) return FI_ERR_INVALID;   // every step leaves its state behind
+    const OnDevice here(s->device);
+    FI_HIP(here.error);
+    FI_HIP(launch_delta_step(c, s->stream));
+    return FI_OK;
+}
+
+// ------------------------------------------------------------ normed and turned heads
+int fi_rotary_create(const fi_rotary_config *cfg, const float *inv_freq, fi_rotary **out) {
+    if (out) *out = nullptr;
+    if (!cfg || !out || (!inv_freq && cfg->rot > 0)) return FI_ERR_INVALID;
+    if (cfg->B < 1 || cfg->L < 1 || cfg->Hq < 1 || cfg->Hk < 0 || cfg->d < 1) return FI_ERR_INVALID;
+    if (cfg->B >= kLim || cfg->L >= kLim || cfg->Hq >= kLim || cfg->Hk >= kLim) return FI_ERR_INVALID;
+    if (cfg->rot < 0 || cfg->rot > cfg->d || cfg->rot % 2 != 0 || !(cfg->eps >= 0.f) || !std::isfinite(cfg->eps)) return FI_ERR_INVALID;
+    const int norm = raw_int(cfg->norm), pairs = raw_int(cfg->pairs);
+    if (norm != FI_NORM_NONE && norm != FI_NORM_RMS && norm != FI_NORM_L2) return FI_ERR_INVALID;
+    if (pairs != FI_PAIRS_HALVES && pairs != FI_PAIRS_ADJACENT) return FI_ERR_INVALID;
+    if (!dtype_ok(raw_int(cfg->io_dtype)) || !fits({cfg->B, cfg->L, cfg->Hq + cfg->Hk, cfg->d}, kMaxCount)) return FI_ERR_INVALID;
+    if (cfg->d > kMaxHead) return FI_ERR_UNSUPPORTED;
+    const int rc = check_device();
+    if (rc != FI_OK) return rc;
+    fi_rotary *s = new (std::nothrow) fi_rotary();
+    if (!s) return FI_ERR_NOMEM;
+    s->cfg = *cfg;
+    s->stream = static_cast<hipStream_t>(cfg->stream);
+    s->turns = nullptr;
+    hipError_t e = hipGetDevice(&s->device);
+    bool ok = true;
+    if (cfg->rot > 0 && e == hipSuccess) {
+        float freq[kMaxHead / 2];
+        double turns[kMaxHead / 2];
+        const int n = (int)cfg->rot / 2;
+        e = hipMemcpyAsync(freq, inv_freq, n * sizeof(float), hipMemcpyDeviceToHost, s->stream);
+        if (e == hipSuccess) e = hipStreamSynchronize(s->stream);
+        for (int i = 0; e == hipSuccess && i < n; ++i) {
+            ok = ok && std::isfinite(freq[i]);
+            turns[i] = (double)freq[i] / 6.283185307179586476925;
+        }
+        if (e == hipSuccess) e = dalloc(&s->turns, n * sizeof(double));
+        if (e == hipSuccess) e = hipMemcpyAsync(s->turns, turns, n * sizeof(double), hipMemcpyHostToDevice, s->stream);
+        if (e == hipSuccess) e = hipStreamSynchronize(s->stream);
+    }
+    if (e != hipSuccess || !ok) {
+        fi_rotary_destroy(s);
+        return e != hipSuccess ? hip_fail(e) : FI_ERR_INVALID;
+    }
+    *out = s;
+    return FI_OK;
+}
+
+void fi_rotary_destroy(fi_rotary *s) {
+    if (!s) return;
+    const OnDevice here(s->device);
+    (void)hipStreamSynchronize(s->stream);
+    if (s->turns) (void)hipFree(s->turns);
+    delete s;
+}
+
+int fi_rotary_run(fi_rotary *s, const fi_rotary_args *a) {
+    if (!s || !a) return FI_ERR_INVALID;
+    const fi_rotary_config &f = s->cfg;
+    if (a->B < 0 || a->B > f.B || a->L < 0 || a->L > f.L) return FI_ERR_INVALID;
+    if (a->B == 0 || a->L == 0) return FI_OK;   // their arrays may be NULL
+    const int dt = raw_int(f.io_dtype), es = esize(dt);
+    if (!a->q.p || !a->qo.p || (f.Hk > 0 && (!a->k.p || !a->ko.p)) || (a->first && a->positions)) return FI_ERR_INVALID;
+    const bool keys = f.Hk > 0;
+    int unit = 16 / es;   // elements that load at once
+    const auto narrow = [&](int64_t n) {
+        while (n % unit) unit /= 2;
+    };
+    for (const fi_view *v : {&a->q, &a->qo, &a->k, &a->ko}) {
+        if (!keys && (v == &a->k || v == &a->ko)) continue;
+        if (!aligned(v->p, es)) return FI_ERR_INVALID;
+        while (!aligned(v->p, (int64_t)unit * es)) unit /= 2;
+        narrow(v->row);
+        narrow(v->pos);
+        narrow(v->head);
+    }
+    for (const void *w : {a->wq, keys ? a->wk : nullptr}) {
+        if (!aligned(w, es)) return FI_ERR_INVALID;
+        while (!aligned(w, (int64_t)unit * es)) unit /= 2;
+    }
+    if (!aligned(a->first, 4) || !aligned(a->positions, 4)) return FI_ERR_INVALID;
+    narrow(f.d);
+    if (raw_int(f.pairs) == FI_PAIRS_HALVES) narrow(f.rot / 2);
+    auto view = [](const fi_view &v) { return View{v.p, v.row, v.pos, v.head}; };
+    const RotaryCall c{a->B, (int)a->L, (int)f.Hq, (int)f.Hk, (int)f.d, (int)f.rot, raw_int(f.norm), raw_int(f.pairs), dt == FI_BF16,
+                       f.eps, s->turns, view(a->q), view(a->k), view(a->qo), view(a->ko), a->wq, a->wk, a->first, a->positions,
+                       unit, 1};
+    const OnDevice here(s->device);
+    FI_HIP(here.error);
+    FI_HIP(launch_rotary(c, s->stream));
+    return FI_OK;
+}
+
+// ------------------------------------------------------------ drafted tokens
+int fi_verify_create(const fi_verify_config *cfg, fi_verify **out) {
+    if (out) *out = nullptr;
+    if (!cfg || !out) return FI_ERR_INVALID;
+    if (cfg->B < 1 || cfg->N < 0 || cfg->V < 1 || cfg->B >= kLim || cfg->N > FI_VERIFY_MAX_DRAFTS || cfg->V >= kLim) return FI_ERR_INVALID;
+    if (!dtype_ok(raw_int(cfg->io_dtype))) return FI_ERR_INVALID;
+    for (float x : {cfg->scale, cfg->draft_scale})
+        if (!(x > 0.f) || !std::isfinite(x)) return FI_ERR_INVALID;
+    if (cfg->B > kVerifyMaxRows / (2 * cfg->N + 1)) return FI_ERR_UNSUPPORTED;
+    const int rc = check_device();
+    if (rc != FI_OK) return rc;
+    fi_verify *s = new (std::nothrow) fi_verify();
+    if (!s) return FI_ERR_NOMEM;
+    s->cfg = *cfg;
+    s->stream = static_cast<hipStream_t>(cfg->stream);
+    s->ws = nullptr;
+    hipError_t e = hipGetDevice(&s->device);
+    const size_t n = verify_ws_doubles(cfg->B, (int)cfg->N, cfg->V, raw_int(cfg->io_dtype) == FI_BF16);
+    if (e == hipSuccess) e = dalloc(&s->ws, n * sizeof(double));
+    if (e != hipSuccess) {
+        fi_verify_destroy(s);
+        return hip_fail(e);
+    }
+    *out = s;
+    return FI_OK;
+}
+
+void fi_verify_destroy(fi_verify *s) {
+    if (!s) return;
+    const OnDevice here(s->device);
+    (void)hipStreamSynchronize(s->stream);
+    if (s->ws) (void)hipFree(s->ws);
+    delete s;
+}
+
+int fi_verify_run(fi_verify *s, const fi_verify_args *a) {
+    if (!s || !a) return FI_ERR_INVALID;
+    const fi_verify_config &f = s->cfg;
+    if (a->B < 0 || a->B > f.B || a->N < 0 || a->N > f.N) return FI_ERR_INVALID;
+    if (a->B == 0) return FI_OK;   // no rows: their arrays may be NULL
+    if (!a->target || !a->r || !a->out || !a->kept || (a->N > 0 && (!a->tokens || !a->u))) return FI_ERR_INVALID;
+    if (a->target_row < 0 || a->target_ld < 0 || a->draft_row < 0 || a->draft_ld < 0) return FI_ERR_INVALID;
+    const int io = raw_int(f.io_dtype);
+    const bool draft = a->draft && a->N > 0;
+    const auto within = [&](int64_t n, int64_t stride) { return stride <= kMaxCount / n; };
+    if (!within(a->B, a->target_row) || !within(a->N + 1, a->target_ld) || (draft && (!within(a->B, a->draft_row) || !within(a->N, a->draft_ld))))
+        return FI_ERR_INVALID;
+    if (!aligned(a->target, esize(io)) || !aligned(a->draft, esize(io)) || !aligned(a->tokens, 8) || !aligned(a->out, 8)) return FI_ERR_INVALID;
+    for (const void *p : {(const void *)a->lens, (const void *)a->u, (const void *)a->r, (const void *)a->kept, (const void *)a->logprob})
+        if (!aligned(p, 4)) return FI_ERR_INVALID;
+    VerifyCall c{};
+    c.B = a->B;
+    c.V = f.V;
+    c.N = (int)a->N;
+    c.io_bf16 = io == FI_BF16;
+    constexpr double log2e = 1.4426950408889634074;
+    c.scale = (double)f.scale * log2e;
+    c.draft_scale = (double)f.draft_scale * log2e;
+    c.target = a->target;
+    c.target_row = a->target_row;
+    c.target_ld = a->target_ld;
+    c.draft = draft ? a->draft : nullptr;
+    c.draft_row = a->draft_row;
+    c.draft_ld = a->draft_ld;
+    c.tokens = a->tokens;
+    c.lens = a->lens;
+    c.u = a->u;
+    c.r = a->r;
+    c.out = a->out;
+    c.kept = a->kept;
+    c.logprob = a->logprob;
+    c.sums = s->ws;
+    const OnDevice here(s->device);
+    FI_HIP(here.error);
+    FI_HIP(launch_verify(c, s->stream));
+    return FI_OK;
 }
 
 }  // extern "C"

@@ -1,6 +1,6 @@
 // fi_operators.h -- declarations shared by the host side of the operators
 // around the mixers (fi_operators.cpp) and their kernels (fi_lattn.hip,
-// fi_dense.hip, fi_scores.hip).  Not part of the public C ABI.
+// fi_dense.hip, fi_scores.hip, fi_delta.hip, fi_rotary.hip, fi_verify.hip).  Not part of the public C ABI.
 #pragma once
 
 #include <hip/hip_runtime_api.h>
@@ -88,5 +88,62 @@ hipError_t launch_scores(ScoresCall c, hipStream_t st);
 void plan_scores(ScoresCall &c);   // a row's parts
 size_t scores_ws_used(const ScoresCall &c);                      // rows x parts of a call
 size_t scores_ws_parts(int64_t rows, int64_t V, int io_bf16);   // the most of any call of so many rows or fewer
+
+// ------------------------------------------------------------ gated delta rule
+struct DeltaCall {
+    int64_t B, n_slots;
+    int L, Hk, Hv, G, dk, dv;   // G = Hv / Hk
+    float scale;
+    int io_bf16, fresh, hold;
+    int vec;                    // every view loads whole 16-byte units
+    View q, k, v, o, ld, beta;
+    const int32_t *lens, *slots;
+    float *state;
+};
+
+// Recurrent form, position by position.
+hipError_t launch_delta_step(const DeltaCall &c, hipStream_t st);
+
+// ------------------------------------------------------------ normed and turned heads
+struct RotaryCall {
+    int64_t B;
+    int L, Hq, Hk, d, rot, norm, pairs, io_bf16;
+    float eps;
+    const double *turns;        // [rot / 2] turns of a position: inv_freq / 2 pi
+    View q, k, qo, ko;
+    const void *wq, *wk;
+    const int32_t *first, *positions;
+    int unit;                   // elements that every head and its halves load and store at once
+    int shares;                 // waves that share out a position's heads
+};
+
+hipError_t launch_rotary(RotaryCall c, hipStream_t st);
+
+// ------------------------------------------------------------ drafted tokens
+constexpr int kVerifyMaxRows = 1 << 22;   // rows of logits of a call
+
+struct VerifyCall {
+    int64_t B, V;
+    int N, io_bf16;
+    double scale, draft_scale;  // with log2 e
+    const void *target, *draft;
+    int64_t target_row, target_ld, draft_row, draft_ld;
+    const int64_t *tokens;
+    const int32_t *lens;
+    const float *u, *r;
+    int64_t *out;
+    int32_t *kept;
+    float *logprob;
+    // a row's parts of `per` logits: sums[B (2 N + 1)][parts] of the probabilities against 2^ref, and
+    // rest[B][parts] of what the token is drawn from
+    int parts;
+    int64_t per;
+    double *sums, *ref, *rest;
+};
+
+hipError_t launch_verify(VerifyCall c, hipStream_t st);
+void plan_verify(VerifyCall &c);   // a row's parts
+size_t verify_ws_used(const VerifyCall &c);                            // doubles of a call
+size_t verify_ws_doubles(int64_t B, int N, int64_t V, int io_bf16);   // the most of any call of so many rows and drafts or fewer
 
 }  // namespace fi

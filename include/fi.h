@@ -420,6 +420,180 @@ int fi_scores_run(fi_scores *s, const fi_scores_args *a);
 /* fi_scores_destroy: synchronise the stream and free everything; NULL is a no-op. */
 void fi_scores_destroy(fi_scores *s);
 
+/*
+ * The gated delta rule: linear attention that replaces what its state holds at
+ * a key instead of adding to it.  For every row b, value head n, its key head
+ * n / (Hv/Hk) and position t, with a = exp(log_decay[t][n]):
+ *
+ *     u[t] = beta[t][n] (v[t] - a S[t-1]^T k[t])
+ *     S[t] = a S[t-1] + k[t] u[t]^T                (S is dk x dv)
+ *     o[t] = scale * S[t]^T q[t]
+ *
+ * q, k, v and o are of io_dtype, log_decay and beta fp32; S is held, summed and
+ * stored in fp32, and o is rounded to io_dtype once.  log_decay is <= 0, -inf for
+ * a = 0.  Keys of length one and beta in [0, 2] keep S bounded
+ * (fi_rotary_run norms them); others are taken, and S grows as the formula
+ * has it.  Calls run on the device that was current when the handle was made.  States, slots and rows out of the pool are as fi_lattn's; two
+ * rows of one call must not share a slot unless the call holds.
+ */
+typedef struct fi_delta fi_delta;   /* opaque; owns its device memory */
+typedef struct {
+    int64_t B;                /* most rows of one call, >= 1 */
+    int64_t L;                /* most positions of one fi_delta_prompt call, >= 1 */
+    int64_t Hk;               /* query and key heads, >= 1 */
+    int64_t Hv;               /* value heads, a multiple of Hk */
+    int64_t dk, dv;           /* sizes of a key and of a value head, 1 .. 256 */
+    float scale;              /* multiplies o; finite */
+    fi_dtype io_dtype;        /* type of q, k, v and o */
+    void *stream;             /* hipStream_t; NULL = the null stream */
+} fi_delta_config;
+
+typedef struct {
+    int64_t B, L;             /* rows and positions of this call, within the config's */
+    fi_view q, k, v;          /* [B][L][Hk][dk], [B][L][Hk][dk], [B][L][Hv][dv] */
+    fi_view o;                /* [B][L][Hv][dv]; overlaps no input */
+    fi_view log_decay, beta;  /* [B][L][Hv], fp32: the value of head n at position t of row b lies at p + b*row + t*pos + n*head */
+    const int32_t *lens;      /* [B] on the device: row b has lens[b] positions (taken into [0, L]); NULL:
+                                 all have L.  What lies past a row's end is not read as a number; o is zero there. */
+    const int32_t *slots;     /* [B] on the device, or NULL */
+    int64_t n_slots;          /* states in `state` (>= B where slots is NULL) */
+    float *state;             /* read, and updated in place; aligned to 16 bytes; may be NULL in a fresh prompt */
+    int32_t fresh;            /* nonzero: every row begins from S = 0, whatever its slot holds */
+    int32_t hold;             /* nonzero: no state is changed (positions that may yet be taken back) */
+} fi_delta_args;
+
+/* fi_delta_create: allocates the workspace of the longest prompt.  Synchronous.
+ * FI_ERR_INVALID for a NULL pointer, a size < 1, Hv not a multiple of Hk, an
+ * infinite or NaN scale, an unknown dtype or sizes that overflow;
+ * FI_ERR_UNSUPPORTED for dk or dv > 256, L > FI_MAX_L, B Hv > 2^20 or a device
+ * that is not gfx950; FI_ERR_NOMEM / FI_ERR_HIP from the device. */
+int fi_delta_create(const fi_delta_config *cfg, fi_delta **out);
+
+/* fi_delta_prompt: L given positions of every row, from the row's state, which is
+ * left after its last position.  B = 0 and L = 0 are allowed.  FI_ERR_INVALID
+ * for a NULL pointer, sizes beyond the config's, fewer than B states without
+ * slots, or a pointer that is not aligned to its element.  A NaN or infinity in an input at t makes
+ * every later output of its row and head and the state not finite, and can make
+ * outputs of up to 63 positions before t NaN. */
+int fi_delta_prompt(fi_delta *s, const fi_delta_args *a);
+
+/* fi_delta_step: one new position of every row in the recurrent form; L is 1,
+ * lens NULL and state not NULL, also where fresh (else FI_ERR_INVALID).  Errors
+ * as fi_delta_prompt. */
+int fi_delta_step(fi_delta *s, const fi_delta_args *a);
+
+/* fi_delta_destroy: synchronise the stream and free everything; NULL is a no-op. */
+void fi_delta_destroy(fi_delta *s);
+
+/*
+ * Queries and keys before a mixer: every head normed, and turned by its
+ * position, in one pass.  For a head x[0 .. d) at position p:
+ *
+ *     FI_NORM_RMS: x[c] /= sqrt(sum_c x[c]^2 / d + eps)
+ *     FI_NORM_L2:  x[c] /= sqrt(sum_c x[c]^2 + eps)
+ *     x[c] *= w[c]                                     (where w is given)
+ *     (x[a], x[b]) turned by p * inv_freq[i], i < rot/2:
+ *         y[a] = x[a] cos - x[b] sin,  y[b] = x[b] cos + x[a] sin
+ *
+ * with (a, b) = (i, i + rot/2) or (2i, 2i + 1); elements from rot on are not
+ * turned.  Everything is fp32 (the angles are reduced in 64 bits), rounded to
+ * io_dtype once.  Calls run on the device that was current when the handle was made.
+ */
+typedef enum { FI_NORM_NONE = 0, FI_NORM_RMS = 1, FI_NORM_L2 = 2 } fi_norm;
+typedef enum { FI_PAIRS_HALVES = 0, FI_PAIRS_ADJACENT = 1 } fi_pairs;
+typedef struct fi_rotary fi_rotary;   /* opaque; owns its device memory */
+typedef struct {
+    int64_t B, L;             /* most rows and positions of one call, >= 1 */
+    int64_t Hq, Hk;           /* query heads, >= 1, and key heads, >= 0 */
+    int64_t d;                /* size of a head, 1 .. 256 */
+    int64_t rot;              /* elements of a head that are turned: even, 0 .. d */
+    fi_norm norm;
+    float eps;                /* finite, >= 0 */
+    fi_pairs pairs;
+    fi_dtype io_dtype;        /* type of the heads and of their weights */
+    void *stream;             /* hipStream_t; NULL = the null stream */
+} fi_rotary_config;
+typedef struct {
+    int64_t B, L;             /* rows and positions of this call, within the config's */
+    fi_view q, k;             /* [B][L][Hq][d], [B][L][Hk][d]; k is ignored where Hk = 0 */
+    fi_view qo, ko;           /* the results; each may be its input (the same pointer and strides), else overlaps no input */
+    const void *wq, *wk;      /* [d] weights of the query (key) heads, or NULL */
+    const int32_t *first;     /* [B] on the device: position t of row b stands at first[b] + t; or NULL: at t */
+    const int32_t *positions; /* [B][L] on the device: where each position stands; or NULL.  Not with first. */
+} fi_rotary_args;
+
+/* fi_rotary_create: copies inv_freq[rot/2] (device, fp32, finite; NULL where rot
+ * is 0).  Synchronous.  FI_ERR_INVALID for a NULL pointer, a size out of range, an odd
+ * rot, eps negative or not finite, an unknown norm, pairs or dtype, an inv_freq that
+ * is not finite or sizes that overflow; FI_ERR_UNSUPPORTED for d > 256 or a device that
+ * is not gfx950; FI_ERR_NOMEM / FI_ERR_HIP from the device. */
+int fi_rotary_create(const fi_rotary_config *cfg, const float *inv_freq, fi_rotary **out);
+
+/* fi_rotary_run: B = 0 and L = 0 are allowed.  FI_ERR_INVALID for a NULL pointer,
+ * sizes beyond the config's, a pointer that is not aligned to its element, or
+ * first and positions both given. */
+int fi_rotary_run(fi_rotary *s, const fi_rotary_args *a);
+
+/* fi_rotary_destroy: synchronise the stream and free everything; NULL is a no-op. */
+void fi_rotary_destroy(fi_rotary *s);
+
+/*
+ * Drafted tokens against the target's probabilities, from given random numbers, so
+ * that what comes out is distributed as the target's own tokens.  Row b
+ * has lens[b] = n drafts x_0 .. x_{n-1}, the target's logits at each and behind the last,
+ * p_i = softmax(scale z_i), and the logits that the drafts were drawn by,
+ * q_i = softmax(draft_scale y_i) (without them the drafts are certain: q_i(x_i) = 1).
+ *
+ *     kept = the first i with u[i] q_i(x_i) >= p_i(x_i), n where there is none
+ *     w = max(p_kept - q_kept, 0), and p_n where kept = n
+ *     out = x_0 .. x_{kept-1}, then the first token j with w_j > 0 and
+ *           w_0 + .. + w_j > r (w_0 + .. + w_{V-1}) (the last with w_j > 0 where there is none),
+ *           then -1
+ *     logprob = log p_i(out[i]), 0 behind the last
+ *
+ * all in 64 bits.  Where w is zero everywhere (a draft that neither allows), the token is
+ * drawn from p_kept.  A logit of -inf is a token that is ruled out.  A draft
+ * outside [0, V) is not kept.  Logits with a NaN or +inf, or without any token left, are no
+ * distribution: a target's keep no draft, and out there is -1, logprob NaN; a draft's do not keep it
+ * either, and the token is drawn from p_kept.  Calls run on the device that was current when the
+ * handle was made.
+ */
+typedef struct fi_verify fi_verify;   /* opaque; owns its device memory */
+#define FI_VERIFY_MAX_DRAFTS 63
+typedef struct {
+    int64_t B;                /* most rows of one call, >= 1 */
+    int64_t N;                /* most drafts of a row, 0 .. FI_VERIFY_MAX_DRAFTS */
+    int64_t V;                /* tokens of the vocabulary, 1 .. 2^31 - 1 */
+    fi_dtype io_dtype;        /* type of the logits */
+    float scale, draft_scale; /* finite, > 0 */
+    void *stream;             /* hipStream_t; NULL = the null stream */
+} fi_verify_config;
+typedef struct {
+    int64_t B, N;             /* rows and places for drafts of this call, within the config's */
+    const void *target; int64_t target_row, target_ld;   /* [B][N+1][V]: rows target_row, positions target_ld elements apart, */
+    const void *draft; int64_t draft_row, draft_ld;      /* [B][N][V]; any strides >= 0; draft may be NULL */
+    const int64_t *tokens;    /* [B][N] drafts */
+    const int32_t *lens;      /* [B] drafts of each row (taken into [0, N]), or NULL: all have N */
+    const float *u;           /* [B][N] random numbers in [0, 1) for the drafts */
+    const float *r;           /* [B] random numbers in [0, 1) for the token after them */
+    int64_t *out;             /* [B][N+1] */
+    int32_t *kept;            /* [B] */
+    float *logprob;           /* [B][N+1], or NULL */
+} fi_verify_args;
+
+/* fi_verify_create: allocates the workspace.  FI_ERR_INVALID for a NULL pointer, a
+ * size or scale out of range or an unknown dtype; FI_ERR_UNSUPPORTED for B (2 N + 1) > 2^22 or
+ * when the device is not gfx950; FI_ERR_NOMEM / FI_ERR_HIP from the device. */
+int fi_verify_create(const fi_verify_config *cfg, fi_verify **out);
+
+/* fi_verify_run: FI_ERR_INVALID for a NULL handle, args, target, r, out or kept, for NULL
+ * tokens or u where N > 0, sizes beyond the config's, a negative stride, or a
+ * pointer not aligned to its element. */
+int fi_verify_run(fi_verify *s, const fi_verify_args *a);
+
+/* fi_verify_destroy: synchronise the stream and free everything; NULL is a no-op. */
+void fi_verify_destroy(fi_verify *s);
+
 #ifdef __cplusplus
 }
 #endif
