@@ -2,6 +2,7 @@
 //
 // Per row b, value head n and position t, a = exp(log_decay[t]):
 //     u[t] = beta[t] (v[t] - a S[t-1]^T k[t]),   S[t] = a S[t-1] + k[t] u[t]^T,   o[t] = scale S[t]^T q[t].
+#include <algorithm>
 #include <type_traits>
 
 #include "fi_opdev.hpp"
@@ -157,6 +158,702 @@ hipError_t launch_delta_step(const DeltaCall& c, hipStream_t st) {
     else if (c.io_bf16) go(std::true_type{}, integral_constant<int, 8>{});
     else if (small) go(std::false_type{}, integral_constant<int, 4>{});
     else go(std::false_type{}, integral_constant<int, 8>{});
+    return hipGetLastError();
+}
+
+// ------------------------------------------------------------ chunked form
+// With Q, K, V a chunk's C positions, E the state before it, G_i the sum of the
+// log decays to position i (it included) and i, j < C:
+//     A[i][j] = beta_i e^{G_i - G_j} k_i . k_j  (j < i),   T = (I + A)^{-1} diag(beta)
+//     U = T (V - diag(e^{G_i}) K E)
+//     O = scale (diag(e^{G_i}) Q E + P U),   P[i][j] = e^{G_i - G_j} q_i . k_j  (j <= i)
+//     S = e^{G_C} E + K^T diag(e^{G_C - G_j}) U
+// T does not depend on the state: k_delta_tri forms it for all chunks at once.
+// k_delta_chunk then follows a row's chunks, a workgroup to a head and a slice of
+// DVS columns of S, 16 columns to a wave.
+//
+// Long rows of few heads are split into segments.  What a segment does to the
+// state before it is linear: S = M E + N; OUT = false forms N (the state from
+// zero) and M (the same, without values, from the identity: dk more columns),
+// k_delta_join the states before the segments, and OUT = true starts from those.
+template <bool BF16>
+struct Dl {
+    static constexpr int C = BF16 ? 64 : 32, CT = C / 16;               // positions of a chunk, tiles of them
+    static constexpr int KB = Mm<BF16>::KB, E = Mm<BF16>::E, PER = KB / 16;   // tiles of an operand
+    static constexpr int NF = BF16 ? 6 : 3;                            // operands of a lower triangle of C x C
+    static constexpr int PARTS = BF16 ? 3 : 1, HALF = BF16 ? 2 : 1;     // parts of an fp32 factor, of one for an output
+    static constexpr int TRI = NF * kWave * E, GATES = 4 * C;           // floats of a chunk: T, then the gates
+    // operand (it, kb) of the triangle
+    static __device__ __forceinline__ int frag(int it, int kb) { return BF16 ? (it / 2 * (it / 2 + 1) + it % 2 * (it / 2 + 1)) + kb : it * (it + 1) / 2 + kb; }
+};
+constexpr float kLog2E = 1.44269504088896341f;
+
+// Sums of C log decays, to each position (its own included), as two floats.
+// Below -150 a decay is 0 in fp32: clamped, so that differences stay finite.
+struct Gate {
+    float hi, lo;
+};
+template <int C>
+__device__ __forceinline__ Gate gate_sum(float g, int lane) {
+    double s = g < -150.f ? -150.0 : (double)g;
+#pragma unroll
+    for (int d = 1; d < C; d <<= 1) {
+        const double x = __shfl_up(s, d);
+        if (lane % C >= d) s += x;
+    }
+    const float hi = (float)s;
+    return {hi, (float)(s - hi)};
+}
+__device__ __forceinline__ float exp_of(Gate a, Gate b) {   // e^{a - b}, a <= b
+    return __builtin_amdgcn_exp2f(((a.hi - b.hi) + (a.lo - b.lo)) * kLog2E);
+}
+
+// One chunk's T and gates.  A in LDS; a wave inverts its 16 x 16 block on the
+// diagonal, D_i, by substitution (stable, where powers of A would not be: equal keys
+// make them as large as binomials), then forms the blocks beside it,
+//     T_ij = -(sum_{j < k <= i} T_ik A_kj) D_j,   j = i - 1, i - 2, ..,
+// transposed, so that a result is the next product's operand as it lies in
+// the registers, and what is stored is the operand that k_delta_chunk loads.
+template <bool BF16, int DK, bool VEC>
+__global__ __launch_bounds__(Dl<BF16>::CT * kWave) void k_delta_tri(DeltaCall a) {
+    using M = Mm<BF16>;
+    using T = typename M::T;
+    using Frag = typename M::Frag;
+    using D = Dl<BF16>;
+    constexpr int C = D::C, CT = D::CT, E = D::E, KB = D::KB, PA = C + 4;
+    __shared__ __align__(16) float as[C * PA], ds[CT][16][20], gs[4][C];
+    const int tid = threadIdx.x, lane = tid % kWave, wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+    const int l16 = lane % 16, g = lane / 16;
+    const int64_t unit = blockIdx.x, task = unit / a.chunks;
+    const int c = a.chunk0 + (int)(unit - task * a.chunks);
+    const int64_t b = task / a.Hv;
+    const int n = (int)(task - b * a.Hv), dk = a.dk;
+    const int64_t slot = a.slots ? a.slots[b] : b;
+    int len = a.lens ? a.lens[b] : a.L;
+    len = slot >= 0 && slot < a.n_slots ? (len > a.L ? a.L : len) : 0;
+    const int t0 = c * C, left = len - t0;   // positions from the chunk's first on
+    if (left <= 0) return;
+
+    Gate mine = {0.f, 0.f};
+    if (wave == 0) {
+        const int t = t0 + lane % C;
+        float ld = 0.f, beta = 0.f;
+        if (lane % C < left) {
+            ld = gmem(static_cast<const float*>(a.ld.p))[b * a.ld.row + t * a.ld.pos + n * a.ld.head];
+            beta = gmem(static_cast<const float*>(a.beta.p))[b * a.beta.row + t * a.beta.pos + n * a.beta.head];
+        }
+        mine = gate_sum<C>(ld, lane);
+        const Gate end = {__shfl(mine.hi, C - 1), __shfl(mine.lo, C - 1)};
+        float* const to = a.tri + unit * (D::TRI + D::GATES) + D::TRI;
+        if (lane < C) {
+            gs[0][lane] = mine.hi;
+            gs[1][lane] = mine.lo;
+            gs[2][lane] = beta;
+            const Gate zero = {0.f, 0.f};
+            to[lane] = exp_of(mine, zero);
+            to[C + lane] = exp_of(end, mine);
+            to[2 * C + lane] = mine.hi;
+            to[3 * C + lane] = mine.lo;
+        }
+    }
+    __syncthreads();
+    // A, tiles of 16 x 16 on and below the diagonal
+    const T* const kp = static_cast<const T*>(a.k.p) + b * a.k.row + n / a.G * a.k.head;
+    const auto row_frag = [&](int tile, int kb) -> Frag {
+        const int r = 16 * tile + l16, col = kb * KB + g * E;
+        const T* p = kp + (int64_t)(t0 + (r < left ? r : left - 1)) * a.k.pos;
+        Frag f = {};
+        if (r < left && col < dk) {
+            if constexpr (VEC) f = *gmem(reinterpret_cast<const Frag*>(p + col));
+            else f = load_loose<BF16>(p, col, dk);
+        }
+        return f;
+    };
+    for (int tile = wave; tile < CT * (CT + 1) / 2; tile += CT) {
+        const int it = tile < 1 ? 0 : tile < 3 ? 1 : tile < 6 ? 2 : 3, jt = tile - it * (it + 1) / 2;
+        V4 p = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int kb = 0; kb < DK / KB; ++kb) {
+            const Frag x = row_frag(it, kb);
+            p = M::mma(x, it == jt ? x : row_frag(jt, kb), p);
+        }
+        const int j = 16 * jt + l16;
+        const Gate gj = {gs[0][j], gs[1][j]};
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int i = 16 * it + 4 * g + r;
+            const Gate gi = {gs[0][i], gs[1][i]};
+            as[i * PA + j] = j < i ? gs[2][i] * exp_of(gi, gj) * p[r] : 0.f;
+        }
+    }
+    __syncthreads();
+    // row l16 of D_wave: x (I + A) = e, from the last column on
+    float x[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) x[j] = j == l16 ? 1.f : 0.f;
+#pragma unroll
+    for (int k = 15; k > 0; --k)
+#pragma unroll
+        for (int j0 = 0; j0 < k; j0 += 4) {
+            const V4 y = *smem_ptr(reinterpret_cast<const V4*>(&as[(16 * wave + k) * PA + 16 * wave + j0]));
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (j0 + j < k) x[j0 + j] = fmaf(-x[k], y[j], x[j0 + j]);
+        }
+    if (g == 0)
+#pragma unroll
+        for (int j = 0; j < 16; j += 4)
+            *smem_ptr(reinterpret_cast<V4*>(&ds[wave][l16][j])) = V4{x[j], x[j + 1], x[j + 2], x[j + 3]};
+    __syncthreads();
+    V4 t[CT];   // t[j]: block (wave, j), transposed: its columns 4 g .. 4 g + 3 of row l16
+#pragma unroll
+    for (int r = 0; r < 4; ++r) t[CT - 1][r] = g == 0 ? x[r] : g == 1 ? x[4 + r] : g == 2 ? x[8 + r] : x[12 + r];
+    // (the block on the diagonal last in t, those before it towards the front: indexes are constants)
+    const auto column = [&](const float* p, int pitch) {
+        return V4{p[(4 * g) * pitch + l16], p[(4 * g + 1) * pitch + l16], p[(4 * g + 2) * pitch + l16], p[(4 * g + 3) * pitch + l16]};
+    };
+    const auto product = [](V4 p, V4 q, V4 acc) { return Mm<false>::mma(p, q, acc); };
+#pragma unroll
+    for (int back = 1; back < CT; ++back) {
+        const int j = wave - back;
+        if (j < 0) break;
+        V4 s = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int near = 0; near < back; ++near)   // block (wave, wave - near)
+            s = product(column(as + 16 * (wave - near) * PA + 16 * j, PA), t[CT - 1 - near], s);
+        t[CT - 1 - back] = -product(column(&ds[j][0][0], 20), s, V4{0.f, 0.f, 0.f, 0.f});
+    }
+    // with beta, as operands: tile j of row `wave` is the part j % PER of operand j / PER
+    float* const to = a.tri + unit * (D::TRI + D::GATES);
+    const auto put = [&](int j, V4 v) {
+        *gmem(reinterpret_cast<V4*>(to + (D::frag(wave, j / D::PER) * kWave + lane) * E + j % D::PER * 4)) = v;
+    };
+#pragma unroll
+    for (int back = 0; back < CT; ++back) {
+        const int j = wave - back;
+        if (j < 0) break;
+        put(j, t[CT - 1 - back] * *smem_ptr(reinterpret_cast<const V4*>(&gs[2][16 * j + 4 * g])));
+    }
+    if (D::PER == 2 && wave % 2 == 0) put(wave + 1, V4{0.f, 0.f, 0.f, 0.f});
+}
+
+constexpr int dl_threads(int dvs) { return dvs / 16 * kWave; }
+
+template <bool BF16, int DK, int DVS, bool OUT, bool VEC>
+__global__ __launch_bounds__(dl_threads(DVS)) void k_delta_chunk(DeltaCall a) {
+    using M = Mm<BF16>;
+    using T = typename M::T;
+    using Frag = typename M::Frag;
+    using Four = T __attribute__((ext_vector_type(4)));
+    using D = Dl<BF16>;
+    constexpr int C = D::C, CT = D::CT, E = D::E, KB = D::KB, PER = D::PER, NF = D::NF, PARTS = D::PARTS, HALF = D::HALF;
+    constexpr int NTH = dl_threads(DVS), WAVES = NTH / kWave, KT = DK / 16;
+    constexpr int PV = DVS + (BF16 ? 16 : 4);                    // V's LDS rows
+    constexpr int UK = C * DK / E / NTH, UV = C * DVS / E / NTH; // 16-byte units of a thread
+    constexpr int UT = (D::TRI / 4 + NTH - 1) / NTH;             // fours of T of a thread
+    __shared__ __align__(16) T ks[C * DK], vs[C * PV], qs[OUT ? C * DK : 1], ps[OUT ? HALF * D::TRI : 1], ts[PARTS * D::TRI];
+    __shared__ __align__(16) float gs[D::GATES];                 // e^{G_i}, e^{G_C - G_i}, G_i in two floats
+
+    const int tid = threadIdx.x, lane = tid % kWave, wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+    const uint32_t l16 = (uint32_t)lane % 16, g = (uint32_t)lane / 16;
+    const int dk = a.dk, dv = a.dv;
+    const int values = (dv + DVS - 1) / DVS, slices = OUT ? values : values + (dk + DVS - 1) / DVS;
+    // the slices of one segment read the same Q and K: eight workgroups apart, on one XCD and its L2
+    const int tasks = (int)a.B * a.Hv, unit = blockIdx.x / (8 * slices) * 8 + blockIdx.x % 8, slice = blockIdx.x / 8 % slices;
+    if (unit >= tasks * a.nseg) return;
+    const int seg = unit / tasks, task = unit % tasks, b = task / a.Hv, n = task % a.Hv;
+    const bool moves = !OUT && slice >= values;                  // columns of what the segment does to a state
+    const int width = moves ? dk : dv, col0 = (moves ? slice - values : slice) * DVS;
+    const int64_t slot = a.slots ? a.slots[b] : b;
+    const bool in = slot >= 0 && slot < a.n_slots;
+    int len = a.lens ? a.lens[b] : a.L;
+    len = in ? (len < 0 ? 0 : len > a.L ? a.L : len) : 0;
+    const int chunks = (len + C - 1) / C, stop = a.chunk0 + a.chunks < chunks ? a.chunk0 + a.chunks : chunks;
+    const int c0 = a.chunk0 + seg * a.seg_chunks;
+    int c1 = c0 + a.seg_chunks;
+    if (c1 > stop) c1 = stop;
+    if (!OUT && c1 >= stop) return;      // a row's last segment hands nothing on
+
+    if constexpr (OUT) {                 // o is zero past the row's end
+        const bool last = seg == a.nseg - 1 && a.chunk0 + a.chunks >= (a.L + C - 1) / C;
+        const int64_t end = (int64_t)(seg == a.nseg - 1 ? a.chunk0 + a.chunks : c0 + a.seg_chunks) * C, z1 = last || end > a.L ? a.L : end;
+        const int64_t z0 = len > c0 * C ? len : c0 * C;
+        constexpr int Z = VEC ? E : 1, UNITS = DVS / Z;   // elements of a store, stores of a row
+        const int col = col0 + tid % UNITS * Z;
+        if (col < dv)
+            for (int64_t t = z0 + tid / UNITS; t < z1; t += NTH / UNITS) {
+                T* const p = static_cast<T*>(a.o.p) + b * a.o.row + t * a.o.pos + n * a.o.head + col;
+                if constexpr (VEC) *gmem(reinterpret_cast<Frag*>(p)) = Frag{};
+                else *gmem(p) = (T)0.f;
+            }
+        if (c0 >= stop && !(c0 == 0 && in && a.fresh)) return;   // (a fresh row without positions leaves zeros)
+    }
+
+    // the lane's part of S: rows 16 kt + 4 g + r of column scol
+    float* const sp = a.state && in ? a.state + (slot * a.Hv + n) * dk * (int64_t)dv : nullptr;
+    float* const ep = a.nseg > 1 ? a.ent + ((int64_t)task * a.nseg + seg) * dk * dv : nullptr;
+    float* const cp = a.carry ? a.carry + (int64_t)task * dk * dv : nullptr;
+    const float* const from = !OUT ? nullptr : ep ? ep : a.chunk0 ? cp : a.fresh ? nullptr : sp;
+    const int scol = col0 + 16 * wave + (int)l16;
+    V4 S[KT] = {};
+    if (from && scol < dv)
+#pragma unroll
+        for (int i = 0; i < 4 * KT; ++i) {
+            const int row = 4 * g + i / 4 * 16 + i % 4;
+            if (row < dk) S[i / 4][i % 4] = gmem(from)[row * dv + scol];
+        }
+    if (moves)
+#pragma unroll
+        for (int i = 0; i < 4 * KT; ++i)
+            if ((int)(4 * g) + i / 4 * 16 + i % 4 == scol && scol < dk) S[i / 4][i % 4] = 1.f;
+
+    // Staging: a thread has the same columns of rows RK (RV) apart.  Loads are of
+    // valid places always (columns past the head's end and rows past the
+    // row's repeat another one) and are blanked on their way to LDS.
+    constexpr int RK = NTH * E / DK, RV = NTH * E / DVS;
+    const int kcol = tid % (DK / E) * E, krow = tid / (DK / E), vcol = tid % (DVS / E) * E, vrow = tid / (DVS / E);
+    const bool kin = kcol < dk, vin = !moves && col0 + vcol < dv;
+    const int kleft = kin ? dk - kcol : 0, vleft = vin ? dv - col0 - vcol : 0;   // elements from there on
+    const int klcol = kin ? kcol : 0, vlcol = vin ? vcol : 0;
+    const T* const kp = static_cast<const T*>(a.k.p) + b * a.k.row + n / a.G * a.k.head;
+    const T* const qp = static_cast<const T*>(a.q.p) + b * a.q.row + n / a.G * a.q.head;
+    const T* const vp = static_cast<const T*>(a.v.p) + b * a.v.row + n * a.v.head + (moves ? 0 : col0);
+    const float* const tp = a.tri + (int64_t)task * a.chunks * (D::TRI + D::GATES);
+    Frag fk[UK], fv[UV], fq[UK];
+    V4 ft[UT];
+    float fg;
+    const auto fetch = [&](auto& f, const T* p, int64_t pos, int c, int row, int step, int col, int left) {
+        constexpr int count = sizeof(f) / sizeof(f[0]);
+        const int t0 = c * C, most = len - 1 - t0;
+        p += t0 * pos;
+#pragma unroll
+        for (int i = 0; i < count; ++i) {
+            const int r = row + i * step < most ? row + i * step : most;
+            if constexpr (VEC) {
+                const uint32_t off = (uint32_t)(r * (int)pos + col) * sizeof(T);
+                f[i] = *gmem(reinterpret_cast<const Frag*>(reinterpret_cast<const char*>(p) + off));
+            } else f[i] = load_loose<BF16>(p + r * pos + col, 0, left);
+        }
+    };
+    const auto fetch_t = [&](int c) {
+        const float* p = tp + (int64_t)(c - a.chunk0) * (D::TRI + D::GATES);
+#pragma unroll
+        for (int i = 0; i < UT; ++i)
+            if ((i + 1) * NTH <= D::TRI / 4 || tid + i * NTH < D::TRI / 4) ft[i] = *gmem(reinterpret_cast<const V4*>(p + 4 * (tid + i * NTH)));
+        if (tid < D::GATES) fg = gmem(p)[D::TRI + tid];
+    };
+    // Q and K in LDS: unit (16 bytes) u of row r at u ^ mix(r).  bf16: each block of KB columns is stored in
+    // the order 4 (g, tile) + r, for whole 16-byte operand reads beside S's, whose lanes hold
+    // rows 4 g .. 4 g + 3 of two tiles.
+    const auto place = [](uint32_t row, uint32_t u) -> uint32_t {
+        constexpr int UNITS = DK / E;
+        const uint32_t m = !BF16 ? row % 16 : UNITS == 8 ? 4 * (row / 2 % 2) + row / 4 % 4 : 4 * (row % 4) + row / 4 % 4;
+        return (row * UNITS + (u ^ m)) * E;
+    };
+    const auto put_rows = [&](T* to, auto& f, int rows) {
+#pragma unroll
+        for (int i = 0; i < UK; ++i) {
+            const int row = krow + i * RK, u = kcol / E;
+            if (!kin || row >= rows) f[i] = Frag{};
+            if constexpr (BF16) {
+                const int at = u / 4 * 4 + u % 2 * 2, half = u / 2 % 2 * 4;
+                *smem_ptr(reinterpret_cast<BF4*>(to + place(row, at) + half)) = __builtin_shufflevector(f[i], f[i], 0, 1, 2, 3);
+                *smem_ptr(reinterpret_cast<BF4*>(to + place(row, at + 1) + half)) = __builtin_shufflevector(f[i], f[i], 4, 5, 6, 7);
+            } else *smem_ptr(reinterpret_cast<Frag*>(to + place(row, u))) = f[i];
+        }
+    };
+    const auto row_frag = [&](const T* from, int tile, int kb) {
+        return *smem_ptr(reinterpret_cast<const Frag*>(from + place(16 * tile + l16, kb * 4 + g)));
+    };
+    // columns 16 kt + l16 of K, as an operand over the positions of block kb
+    const auto transposed = [&](int kt, int kb) {
+        Frag f;
+        if constexpr (BF16) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const T* p = ks + place(KB * kb + 16 * h + 4 * g + l16 / 4, kt / 2 * 4 + l16 % 4) + kt % 2 * 4;
+                const BF4 y = __builtin_bit_cast(BF4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((FI_SHARED S4*)(p)));
+#pragma unroll
+                for (int e = 0; e < 4; ++e) f[4 * h + e] = y[e];
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) f[e] = smem_ptr(ks)[place(KB * kb + 4 * g + e, 4 * kt + l16 / 4) + l16 % 4];
+        }
+        return f;
+    };
+    // fp32 values of a block's tiles as the sum of parts, each the nearest to what is left
+    const auto split = [](const V4* x, auto& f) {
+        constexpr int N = sizeof(f) / sizeof(f[0]);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            float y = x[e / 4][e % 4];
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                f[i][e] = (T)y;
+                if (i + 1 < N) y -= (float)f[i][e];
+            }
+        }
+    };
+    const auto tri_frag = [&](const T* from, int part, int f) {
+        return *smem_ptr(reinterpret_cast<const Frag*>(from + (part * NF + f) * kWave * E + lane * E));
+    };
+
+    if (c0 < c1) {
+        fetch(fk, kp, a.k.pos, c0, krow, RK, klcol, kleft);
+        if (!moves) fetch(fv, vp, a.v.pos, c0, vrow, RV, vlcol, vleft);
+        if constexpr (OUT) fetch(fq, qp, a.q.pos, c0, krow, RK, klcol, kleft);
+        fetch_t(c0);
+    }
+    for (int c = c0; c < c1; ++c) {
+        const int rows = len - c * C;   // positions from the chunk's first on
+        put_rows(ks, fk, rows);
+        if constexpr (OUT) put_rows(qs, fq, rows);
+        if (!moves) {
+#pragma unroll
+            for (int i = 0; i < UV; ++i) {
+                if (!vin || vrow + i * RV >= rows) fv[i] = Frag{};
+                *smem_ptr(reinterpret_cast<Frag*>(vs + (vrow + i * RV) * PV + vcol)) = fv[i];
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < UT; ++i)
+            if ((i + 1) * NTH <= D::TRI / 4 || tid + i * NTH < D::TRI / 4) {
+                V4 y = ft[i];
+#pragma unroll
+                for (int p = 0; p < PARTS; ++p) {
+                    Four z;
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        z[r] = (T)y[r];
+                        y[r] -= (float)z[r];
+                    }
+                    *smem_ptr(reinterpret_cast<Four*>(ts + p * D::TRI + 4 * (tid + i * NTH))) = z;
+                }
+            }
+        if (tid < D::GATES) gs[tid] = fg;
+        __syncthreads();
+        // the next chunk's (the last one's again at the end: no branch, so that nothing waits for them before their use)
+        const int ahead = c + 1 < c1 ? c + 1 : c;
+        fetch(fk, kp, a.k.pos, ahead, krow, RK, klcol, kleft);
+        if (!moves) fetch(fv, vp, a.v.pos, ahead, vrow, RV, vlcol, vleft);
+        if constexpr (OUT) fetch(fq, qp, a.q.pos, ahead, krow, RK, klcol, kleft);
+        fetch_t(ahead);
+
+        if constexpr (OUT) {
+            // P^T, tiles of 16 keys x 16 queries, jt <= it, shared out among the waves
+#pragma unroll
+            for (int at = 0; at < CT * (CT + 1) / 2; at += WAVES) {
+                const int tile = at + wave;
+                if (tile >= CT * (CT + 1) / 2) break;
+                const int it = tile < 1 ? 0 : tile < 3 ? 1 : tile < 6 ? 2 : 3, jt = tile - it * (it + 1) / 2;
+                V4 p = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int kb = 0; kb < DK / KB; ++kb) p = M::mma(row_frag(ks, jt, kb), row_frag(qs, it, kb), p);
+                const int i = 16 * it + l16;
+                const Gate gi = {gs[2 * C + i], gs[3 * C + i]};
+                const V4 hi = *smem_ptr(reinterpret_cast<const V4*>(&gs[2 * C + 16 * jt + 4 * g])),
+                         lo = *smem_ptr(reinterpret_cast<const V4*>(&gs[3 * C + 16 * jt + 4 * g]));
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int j = 16 * jt + 4 * g + r;
+                    p[r] = j <= i ? p[r] * exp_of(gi, Gate{hi[r], lo[r]}) : 0.f;
+                }
+                const auto to = [&](int tile, int part) {
+                    return smem_ptr(reinterpret_cast<Four*>(ps + part * D::TRI + (D::frag(it, tile / PER) * kWave + lane) * E + tile % PER * 4));
+                };
+#pragma unroll
+                for (int part = 0; part < HALF; ++part) {
+                    Four z;
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        z[r] = (T)p[r];
+                        p[r] -= (float)z[r];
+                    }
+                    *to(jt, part) = z;
+                    if (PER == 2 && it == jt && it % 2 == 0) *to(jt + 1, part) = Four{};
+                }
+            }
+        }
+        // K E (rows are positions), and O^T = E^T Q^T (columns are positions)
+        V4 R[CT] = {}, O[OUT ? CT : 1] = {};
+#pragma unroll
+        for (int kb = 0; kb < DK / KB; ++kb) {
+            Frag f[PARTS];
+            split(&S[kb * PER], f);
+#pragma unroll
+            for (int it = 0; it < CT; ++it) {
+                const Frag k = row_frag(ks, it, kb);
+#pragma unroll
+                for (int i = PARTS - 1; i >= 0; --i) R[it] = M::mma(k, f[i], R[it]);
+                if constexpr (OUT) {
+                    const Frag q = row_frag(qs, it, kb);
+#pragma unroll
+                    for (int i = HALF - 1; i >= 0; --i) O[it] = M::mma(f[i], q, O[it]);
+                }
+            }
+        }
+        // R = V - diag(e^G) K E
+#pragma unroll
+        for (int it = 0; it < CT; ++it) {
+            const V4 e = *smem_ptr(reinterpret_cast<const V4*>(&gs[16 * it + 4 * g]));
+            V4 v = {0.f, 0.f, 0.f, 0.f};
+            if (!moves) {
+                if constexpr (BF16) {
+                    const T* p = vs + (16 * it + 4 * g + l16 / 4) * PV + 16 * wave + l16 % 4 * 4;
+                    const BF4 y = __builtin_bit_cast(BF4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((FI_SHARED S4*)(p)));
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) v[r] = (float)y[r];
+                } else {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) v[r] = smem_ptr(vs)[(16 * it + 4 * g + r) * PV + 16 * wave + l16];
+                }
+            }
+#pragma unroll
+            for (int r = 0; r < 4; ++r) R[it][r] = fmaf(-e[r], R[it][r], v[r]);
+        }
+        // U = T R
+        V4 U[CT] = {};
+#pragma unroll
+        for (int kb = 0; kb < C / KB; ++kb) {
+            Frag f[PARTS];
+            split(&R[kb * PER], f);
+#pragma unroll
+            for (int it = kb * PER; it < CT; ++it)
+#pragma unroll
+                for (int p = PARTS - 1; p >= 0; --p) {
+                    const Frag t = tri_frag(ts, p, D::frag(it, kb));
+#pragma unroll
+                    for (int i = PARTS - 1 - p; i >= 0; --i) U[it] = M::mma(t, f[i], U[it]);
+                }
+        }
+        if constexpr (OUT) {
+            // O = e^G Q E + P U
+#pragma unroll
+            for (int it = 0; it < CT; ++it) O[it] *= gs[16 * it + l16];
+            __syncthreads();
+#pragma unroll
+            for (int kb = 0; kb < C / KB; ++kb) {
+                Frag f[HALF];
+                split(&U[kb * PER], f);
+#pragma unroll
+                for (int it = kb * PER; it < CT; ++it)
+#pragma unroll
+                    for (int p = HALF - 1; p >= 0; --p) {
+                        const Frag t = tri_frag(ps, p, D::frag(it, kb));
+#pragma unroll
+                        for (int i = HALF - 1 - p; i >= 0; --i) O[it] = M::mma(f[i], t, O[it]);
+                    }
+            }
+            T* const op = static_cast<T*>(a.o.p) + b * a.o.row + n * a.o.head + (int64_t)c * C * a.o.pos + col0 + 16 * wave;
+            const int left = dv - (col0 + 16 * wave + 4 * (int)g);
+#pragma unroll
+            for (int it = 0; it < CT; ++it) {
+                Four y;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) y[r] = (T)(a.scale * O[it][r]);
+                if (16 * it + (int)l16 < rows) {
+                    T* to = op + (16 * it + l16) * a.o.pos + 4 * g;
+                    if constexpr (VEC) {
+                        if (left > 0) *gmem(reinterpret_cast<Four*>(to)) = y;
+                    } else
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+                            if (r < left) gmem(to)[r] = y[r];
+                }
+            }
+        }
+        // S: its decay as S + (e^G - 1) S (the rounding of e^G would add up over the chunks of
+        // a long memory), then the chunk's own products
+        const float d = expm1f(gs[3 * C - 1]) + gs[C - 1] * gs[4 * C - 1];
+#pragma unroll
+        for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) S[kt][r] = fmaf(d, S[kt][r], S[kt][r]);
+#pragma unroll
+        for (int kb = 0; kb < C / KB; ++kb) {
+#pragma unroll
+            for (int it = kb * PER; it < (kb + 1) * PER; ++it) U[it] *= *smem_ptr(reinterpret_cast<const V4*>(&gs[C + 16 * it + 4 * g]));
+            Frag f[PARTS];
+            split(&U[kb * PER], f);
+#pragma unroll
+            for (int kt = 0; kt < KT; ++kt) {
+                const Frag k = transposed(kt, kb);
+#pragma unroll
+                for (int i = PARTS - 1; i >= 0; --i) S[kt] = M::mma(k, f[i], S[kt]);
+            }
+        }
+        __syncthreads();
+    }
+    float* to;
+    if constexpr (OUT) to = c1 < chunks ? (c1 == a.chunk0 + a.chunks ? cp : nullptr) : a.hold ? nullptr : sp;
+    else to = moves ? a.move + ((int64_t)task * a.nseg + seg) * dk * dk : ep + (int64_t)dk * dv;
+    if (!to || scol >= width) return;
+#pragma unroll
+    for (int i = 0; i < 4 * KT; ++i) {
+        const int row = 4 * g + i / 4 * 16 + i % 4;
+        if (row < dk) gmem(to)[row * width + scol] = S[i / 4][i % 4];
+    }
+}
+
+// States before a split row's segments, in place: ent[s + 1] holds what segment s
+// makes of zero and becomes M_s ent[s] + that; ent[0] is the row's state.
+// Four waves share out the rows of a slice of 16 columns and meet in LDS.
+constexpr int kDjThreads = 256;
+template <int DK>
+__global__ __launch_bounds__(kDjThreads) void k_delta_join(DeltaCall a, int C) {
+    constexpr int KT = DK / 16, MINE = (KT + 3) / 4, PE = DK + 4;   // tiles of rows, of a wave, LDS columns
+    __shared__ __align__(16) float es[16 * PE];                      // the state, transposed
+    const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave, l16 = lane % 16, g = lane / 16;
+    const int dk = a.dk, dv = a.dv, slices = (dv + 15) / 16;
+    const int64_t task = blockIdx.x / slices, b = task / a.Hv;
+    const int n = (int)(task - b * a.Hv), col = blockIdx.x % slices * 16 + l16;
+    const int64_t slot = a.slots ? a.slots[b] : b;
+    if (slot < 0 || slot >= a.n_slots) return;
+    int len = a.lens ? a.lens[b] : a.L;
+    len = len < 0 ? 0 : len > a.L ? a.L : len;
+    const int chunks = (len + C - 1) / C, stop = a.chunk0 + a.chunks < chunks ? a.chunk0 + a.chunks : chunks;
+    const int segs = (stop - a.chunk0 + a.seg_chunks - 1) / a.seg_chunks;
+    float* const ent = a.ent + task * a.nseg * dk * dv;
+    const float* const from = a.chunk0 ? a.carry + task * dk * dv : a.fresh || !a.state ? nullptr : a.state + (slot * a.Hv + n) * dk * (int64_t)dv;
+    for (int i = tid; i < 16 * DK; i += kDjThreads) {
+        const int row = i / 16, c = blockIdx.x % slices * 16 + i % 16;
+        const float x = from && row < dk && c < dv ? gmem(from)[row * dv + c] : 0.f;
+        es[i % 16 * PE + row] = x;
+        if (row < dk && c < dv) gmem(ent)[row * dv + c] = x;
+    }
+    __syncthreads();
+    for (int s = 0; s + 1 < segs; ++s) {
+        const float* const m = a.move + (task * a.nseg + s) * dk * dk;
+        float* const to = ent + (int64_t)(s + 1) * dk * dv;
+        V4 acc[MINE];
+#pragma unroll
+        for (int i = 0; i < MINE; ++i) {
+            const int row0 = 16 * (wave + 4 * i) + 4 * g;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) acc[i][r] = row0 + r < dk && col < dv ? gmem(to)[(row0 + r) * dv + col] : 0.f;
+        }
+#pragma unroll
+        for (int kt = 0; kt < KT; ++kt) {
+            if (16 * kt >= dk) break;
+            const V4 e = *smem_ptr(reinterpret_cast<const V4*>(&es[l16 * PE + 16 * kt + 4 * g]));
+#pragma unroll
+            for (int i = 0; i < MINE; ++i) {
+                const int row = 16 * (wave + 4 * i) + l16;
+                V4 x = {0.f, 0.f, 0.f, 0.f};
+                if (row < dk) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (16 * kt + 4 * g + k < dk) x[k] = gmem(m)[row * dk + 16 * kt + 4 * g + k];
+                }
+                acc[i] = Mm<false>::mma(x, e, acc[i]);
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < MINE; ++i) {
+            const int row0 = 16 * (wave + 4 * i) + 4 * g;
+            if (row0 < DK) *smem_ptr(reinterpret_cast<V4*>(&es[l16 * PE + row0])) = acc[i];
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                if (row0 + r < dk && col < dv) gmem(to)[(row0 + r) * dv + col] = acc[i][r];
+        }
+        __syncthreads();
+    }
+}
+
+namespace {
+
+constexpr int64_t kDlTri = 32768;       // chunks of all heads whose systems are held at a time (bf16: 436 MB)
+constexpr int64_t kDlWorkgroups = 256;  // wanted of a launch
+
+int dl_chunk(int io_bf16) { return io_bf16 ? Dl<true>::C : Dl<false>::C; }
+int64_t dl_floats(int io_bf16) { return io_bf16 ? Dl<true>::TRI + Dl<true>::GATES : Dl<false>::TRI + Dl<false>::GATES; }
+int dl_cols(int dk) { return dk <= 64 ? 64 : 128; }
+constexpr int64_t kDlLeast = 8;         // chunks of a segment at least
+
+template <bool BF16, int DK, int DVS, bool VEC>
+void delta_launches(const DeltaCall& c, hipStream_t st) {
+    const int64_t tasks = c.B * c.Hv, units = tasks * c.nseg;
+    const int values = (c.dv + DVS - 1) / DVS, all = values + (c.dk + DVS - 1) / DVS;
+    k_delta_tri<BF16, DK, VEC><<<(unsigned)(tasks * c.chunks), Dl<BF16>::CT * kWave, 0, st>>>(c);
+    if (c.nseg > 1) {
+        k_delta_chunk<BF16, DK, DVS, false, VEC><<<(unsigned)((units + 7) / 8 * 8 * all), dl_threads(DVS), 0, st>>>(c);
+        k_delta_join<DK><<<(unsigned)(tasks * ((c.dv + 15) / 16)), kDjThreads, 0, st>>>(c, Dl<BF16>::C);
+    }
+    k_delta_chunk<BF16, DK, DVS, true, VEC><<<(unsigned)((units + 7) / 8 * 8 * values), dl_threads(DVS), 0, st>>>(c);
+}
+
+template <bool BF16>
+void delta_dims(const DeltaCall& c, hipStream_t st) {
+    if (c.dk <= 64) c.vec ? delta_launches<BF16, 64, 64, true>(c, st) : delta_launches<BF16, 64, 64, false>(c, st);
+    else if (c.dk <= 128) c.vec ? delta_launches<BF16, 128, 128, true>(c, st) : delta_launches<BF16, 128, 128, false>(c, st);
+    else c.vec ? delta_launches<BF16, 256, 128, true>(c, st) : delta_launches<BF16, 256, 128, false>(c, st);
+}
+
+}  // namespace
+
+bool delta_by_steps(const DeltaCall& c) { return c.L <= 16; }
+
+void plan_delta(DeltaCall& c) {
+    const int C = dl_chunk(c.io_bf16);
+    const int64_t tasks = c.B * c.Hv, all = (c.L + C - 1) / C, most = kDlTri / tasks < 1 ? 1 : kDlTri / tasks;
+    c.chunk0 = 0;
+    c.chunks = (int)(all < most ? all : most);
+    const int slices = (c.dv + dl_cols(c.dk) - 1) / dl_cols(c.dk);
+    int64_t n = kDlWorkgroups / (tasks * slices);
+    if (n > c.chunks / kDlLeast) n = c.chunks / kDlLeast;
+    if (n < 1) n = 1;
+    c.seg_chunks = c.chunks ? (int)((c.chunks + n - 1) / n) : 1;
+    c.nseg = c.chunks ? (c.chunks + c.seg_chunks - 1) / c.seg_chunks : 1;
+}
+
+namespace {
+
+// the workspace's parts, in floats
+struct DeltaParts {
+    size_t tri, ent, move, carry;
+    size_t all() const { return tri + ent + move + carry; }
+};
+DeltaParts delta_parts(const DeltaCall& c) {
+    const size_t tasks = (size_t)c.B * c.Hv, states = (size_t)c.dk * c.dv, segs = c.nseg > 1 ? tasks * c.nseg : 0;
+    const int C = dl_chunk(c.io_bf16);
+    return {tasks * c.chunks * dl_floats(c.io_bf16), segs * states, segs * c.dk * c.dk,
+            (c.L + C - 1) / C > c.chunks ? tasks * states : 0};
+}
+
+}  // namespace
+
+size_t delta_ws_used(const DeltaCall& c) { return delta_by_steps(c) ? 0 : delta_parts(c).all() * sizeof(float); }
+
+size_t delta_ws_bytes(int64_t B, int64_t L, int Hv, int dk, int dv, int io_bf16) {
+    DeltaCall c = {};
+    c.L = (int)L;
+    if (delta_by_steps(c)) return 0;
+    const int64_t C = dl_chunk(io_bf16), tasks = B * Hv, chunks = (L + C - 1) / C;
+    // systems: of all chunks, or of as many as are held at a time (one of each head at least)
+    const int64_t held = std::max(kDlTri, tasks), tri = chunks > held / tasks ? held : tasks * chunks;
+    // segments: at most kDlWorkgroups over all heads and slices of any call
+    const int slices = (dv + dl_cols(dk) - 1) / dl_cols(dk);
+    const int64_t segs = chunks >= 2 * kDlLeast ? kDlWorkgroups / slices : 0;
+    const int64_t carry = chunks > kDlTri / tasks ? tasks * dk * dv : 0;
+    return (size_t)(tri * dl_floats(io_bf16) + segs * (dk * dv + dk * dk) + carry) * sizeof(float);
+}
+
+hipError_t launch_delta_chunk(DeltaCall c, float* ws, hipStream_t st) {
+    plan_delta(c);
+    const int C = dl_chunk(c.io_bf16), all = (c.L + C - 1) / C, held = c.chunks;
+    const DeltaParts p = delta_parts(c);
+    c.tri = ws;
+    c.ent = c.tri + p.tri;
+    c.move = c.ent + p.ent;
+    c.carry = p.carry ? c.move + p.move : nullptr;
+    do {   // (an empty prompt: one launch, which may leave zeros)
+        if (all - c.chunk0 < held) c.chunks = all - c.chunk0;
+        if (c.io_bf16) delta_dims<true>(c, st);
+        else delta_dims<false>(c, st);
+        c.chunk0 += held;
+    } while (c.chunk0 < all);
     return hipGetLastError();
 }
 

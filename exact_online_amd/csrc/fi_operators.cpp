@@ -38,6 +38,7 @@ struct fi_delta {
     fi_delta_config cfg;
     hipStream_t stream;
     int device;
+    float *ws;       // chunks' systems, segments' states
 };
 
 struct fi_rotary {
@@ -337,9 +338,12 @@ int fi_delta_create(const fi_delta_config *cfg, fi_delta **out) {
     if (!s) return FI_ERR_NOMEM;
     s->cfg = *cfg;
     s->stream = static_cast<hipStream_t>(cfg->stream);
-    const hipError_t e = hipGetDevice(&s->device);
+    s->ws = nullptr;
+    hipError_t e = hipGetDevice(&s->device);
+    const size_t ws = delta_ws_bytes(cfg->B, cfg->L, (int)cfg->Hv, (int)cfg->dk, (int)cfg->dv, raw_int(cfg->io_dtype) == FI_BF16);
+    if (e == hipSuccess && ws > 0) e = dalloc(&s->ws, ws);
     if (e != hipSuccess) {
-        delete s;
+        fi_delta_destroy(s);
         return hip_fail(e);
     }
     *out = s;
@@ -350,6 +354,7 @@ void fi_delta_destroy(fi_delta *s) {
     if (!s) return;
     const OnDevice here(s->device);
     (void)hipStreamSynchronize(s->stream);
+    if (s->ws) (void)hipFree(s->ws);
     delete s;
 }
 
@@ -407,7 +412,7 @@ int fi_delta_prompt(fi_delta *s, const fi_delta_args *a) {
     if (rc != FI_OK || c.B == 0) return rc;
     const OnDevice here(s->device);
     FI_HIP(here.error);
-    FI_HIP(launch_delta_step(c, s->stream));
+    FI_HIP(delta_by_steps(c) ? launch_delta_step(c, s->stream) : launch_delta_chunk(c, s->ws, s->stream));
     return FI_OK;
 }
 

@@ -99,10 +99,21 @@ struct DeltaCall {
     View q, k, v, o, ld, beta;
     const int32_t *lens, *slots;
     float *state;
+    // the chunked form: chunks chunk0 .. chunk0 + chunks - 1 of every row at a time, in nseg segments of seg_chunks
+    int chunk0, chunks, nseg, seg_chunks;
+    float *tri;                 // [B Hv][chunks] systems and gates (delta_tri_floats each)
+    float *ent, *move;          // of several segments: [B Hv][nseg][dk][dv] states before them, [B Hv][nseg][dk][dk] what they do to a state
+    float *carry;               // [B Hv][dk][dv] states between two runs of chunks
 };
 
 // Recurrent form, position by position.
 hipError_t launch_delta_step(const DeltaCall &c, hipStream_t st);
+// Chunked form; ws holds delta_ws_bytes, the most that plan_delta makes any call of these sizes and smaller ones use.
+hipError_t launch_delta_chunk(DeltaCall c, float *ws, hipStream_t st);
+void plan_delta(DeltaCall &c);   // chunks at a time, segments
+size_t delta_ws_used(const DeltaCall &c);
+size_t delta_ws_bytes(int64_t B, int64_t L, int Hv, int dk, int dv, int io_bf16);
+bool delta_by_steps(const DeltaCall &c);   // few positions: the recurrent form
 
 // ------------------------------------------------------------ normed and turned heads
 struct RotaryCall {

@@ -238,6 +238,14 @@ def test_long_memory_of_few_heads(dtype):
     check(inputs(11, 1, 4097, 1, 1, 128, 128, dtype, memory=(1e4, 1e6)), dtype, fresh=True)
 
 
+@pytest.mark.parametrize("dtype,L", [("bf16", 8400), ("f32", 4200)])
+@pytest.mark.parametrize("fresh,hold", [(False, False), (True, True)])
+def test_more_chunks_than_are_held_at_a_time(fresh, hold, dtype, L):
+    """256 heads of more than 128 chunks: their systems are formed in several runs, states handed from one to the next."""
+    x = inputs(20, 4, L, 2, 64, 24, 8, dtype, memory=(100.0, 5000.0))
+    check(x, dtype, lens=[L, L - 300, 77, 0], fresh=fresh, hold=hold)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_prompt_in_pieces_then_steps(dtype):
     """A prompt in calls of odd lengths and then single steps equals one prompt."""
