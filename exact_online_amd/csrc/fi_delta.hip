@@ -337,18 +337,65 @@ __global__ __launch_bounds__(Dl<BF16>::CT * kWave) void k_delta_tri(DeltaCall a)
     if (D::PER == 2 && wave % 2 == 0) put(wave + 1, V4{0.f, 0.f, 0.f, 0.f});
 }
 
-constexpr int dl_threads(int dvs) { return dvs / 16 * kWave; }
+// Values of a block's tiles as the sum of N parts, each the nearest to what is
+// left: two hold an fp32 value to 2^-18, three hold it whole.
+template <bool BF16, int N>
+__device__ __forceinline__ void split(const V4* x, typename Mm<BF16>::Frag* f) {
+    if constexpr (BF16) {
+        using BF2 = BF __attribute__((ext_vector_type(2)));
+        uint32_t part[N][4];
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) {
+            V2 y = {x[e / 4][e % 4], x[e / 4][e % 4 + 1]};
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const uint32_t u = part[i][e / 2] = __builtin_bit_cast(uint32_t, __builtin_convertvector(y, BF2));
+                if (i + 1 < N) {
+                    y.x -= __uint_as_float(u << 16);
+                    y.y -= __uint_as_float(u & 0xFFFF0000u);
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) f[i] = __builtin_bit_cast(BF8, part[i]);
+    } else f[0] = x[0];
+}
+// The same of four values, to LDS: part i at to + i * pitch
+template <bool BF16, int N>
+__device__ __forceinline__ void split_to(V4 x, typename Mm<BF16>::T* to, int pitch) {
+    if constexpr (BF16) {
+        using U2 = uint32_t __attribute__((ext_vector_type(2)));
+        using BF2 = BF __attribute__((ext_vector_type(2)));
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            U2 u;
+#pragma unroll
+            for (int e = 0; e < 4; e += 2) {
+                u[e / 2] = __builtin_bit_cast(uint32_t, __builtin_convertvector(V2{x[e], x[e + 1]}, BF2));
+                x[e] -= __uint_as_float(u[e / 2] << 16);
+                x[e + 1] -= __uint_as_float(u[e / 2] & 0xFFFF0000u);
+            }
+            *smem_ptr(reinterpret_cast<U2*>(to + i * pitch)) = u;
+        }
+    } else *smem_ptr(reinterpret_cast<V4*>(to)) = x;
+}
 
+constexpr int kDcThreads = 256, kDcWaves = kDcThreads / kWave;
+
+// A wave has NC = DVS / 64 tiles of 16 columns of S in its registers, which are the
+// operand of its products as they lie there: lane (g, l16) of tile kt has column l16 and the rows row_of(kt) + r,
+// so that the tiles of one operand hold rows that follow one another for each lane.
+// The waves meet only in P and in what is staged.
 template <bool BF16, int DK, int DVS, bool OUT, bool VEC>
-__global__ __launch_bounds__(dl_threads(DVS)) void k_delta_chunk(DeltaCall a) {
+__global__ __launch_bounds__(kDcThreads, DK <= 128 ? 2 : 1) void k_delta_chunk(DeltaCall a) {
     using M = Mm<BF16>;
     using T = typename M::T;
     using Frag = typename M::Frag;
     using Four = T __attribute__((ext_vector_type(4)));
     using D = Dl<BF16>;
     constexpr int C = D::C, CT = D::CT, E = D::E, KB = D::KB, PER = D::PER, NF = D::NF, PARTS = D::PARTS, HALF = D::HALF;
-    constexpr int NTH = dl_threads(DVS), WAVES = NTH / kWave, KT = DK / 16;
-    constexpr int PV = DVS + (BF16 ? 16 : 4);                    // V's LDS rows
+    constexpr int NTH = kDcThreads, KT = DK / 16, NC = DVS / 16 / kDcWaves;
+    constexpr int PV = DVS + E;                                  // V's LDS rows
     constexpr int UK = C * DK / E / NTH, UV = C * DVS / E / NTH; // 16-byte units of a thread
     constexpr int UT = (D::TRI / 4 + NTH - 1) / NTH;             // fours of T of a thread
     __shared__ __align__(16) T ks[C * DK], vs[C * PV], qs[OUT ? C * DK : 1], ps[OUT ? HALF * D::TRI : 1], ts[PARTS * D::TRI];
@@ -363,7 +410,7 @@ __global__ __launch_bounds__(dl_threads(DVS)) void k_delta_chunk(DeltaCall a) {
     if (unit >= tasks * a.nseg) return;
     const int seg = unit / tasks, task = unit % tasks, b = task / a.Hv, n = task % a.Hv;
     const bool moves = !OUT && slice >= values;                  // columns of what the segment does to a state
-    const int width = moves ? dk : dv, col0 = (moves ? slice - values : slice) * DVS;
+    const int col0 = (moves ? slice - values : slice) * DVS;
     const int64_t slot = a.slots ? a.slots[b] : b;
     const bool in = slot >= 0 && slot < a.n_slots;
     int len = a.lens ? a.lens[b] : a.L;
@@ -389,27 +436,32 @@ __global__ __launch_bounds__(dl_threads(DVS)) void k_delta_chunk(DeltaCall a) {
         if (c0 >= stop && !(c0 == 0 && in && a.fresh)) return;   // (a fresh row without positions leaves zeros)
     }
 
-    // the lane's part of S: rows 16 kt + 4 g + r of column scol
+    // the lane's part of S: rows row_of(kt) + r of the columns scol + 16 nc
+    const auto row_of = [&](int kt) { return BF16 ? kt / 2 * 32 + (int)g * 8 + kt % 2 * 4 : 16 * kt + 4 * (int)g; };
     float* const sp = a.state && in ? a.state + (slot * a.Hv + n) * dk * (int64_t)dv : nullptr;
     float* const ep = a.nseg > 1 ? a.ent + ((int64_t)task * a.nseg + seg) * dk * dv : nullptr;
     float* const cp = a.carry ? a.carry + (int64_t)task * dk * dv : nullptr;
     const float* const from = !OUT ? nullptr : ep ? ep : a.chunk0 ? cp : a.fresh ? nullptr : sp;
-    const int scol = col0 + 16 * wave + (int)l16;
-    V4 S[KT] = {};
-    if (from && scol < dv)
+    const int wcol = 16 * NC * wave, scol = col0 + wcol + (int)l16;
+    V4 S[NC][KT] = {};
 #pragma unroll
-        for (int i = 0; i < 4 * KT; ++i) {
-            const int row = 4 * g + i / 4 * 16 + i % 4;
-            if (row < dk) S[i / 4][i % 4] = gmem(from)[row * dv + scol];
-        }
-    if (moves)
+    for (int nc = 0; nc < NC; ++nc) {
+        const int col = scol + 16 * nc;
+        if (from && col < dv)
 #pragma unroll
-        for (int i = 0; i < 4 * KT; ++i)
-            if ((int)(4 * g) + i / 4 * 16 + i % 4 == scol && scol < dk) S[i / 4][i % 4] = 1.f;
+            for (int i = 0; i < 4 * KT; ++i) {
+                const int row = row_of(i / 4) + i % 4;
+                if (row < dk) S[nc][i / 4][i % 4] = gmem(from)[row * dv + col];
+            }
+        if (moves)
+#pragma unroll
+            for (int i = 0; i < 4 * KT; ++i)
+                if (row_of(i / 4) + i % 4 == col && col < dk) S[nc][i / 4][i % 4] = 1.f;
+    }
 
     // Staging: a thread has the same columns of rows RK (RV) apart.  Loads are of
-    // valid places always (columns past the head's end and rows past the
-    // row's repeat another one) and are blanked on their way to LDS.
+    // valid places always: columns past the head's end are blanked on their way to
+    // LDS, rows past the row's repeat its last, and weigh nothing (beta is 0 there).
     constexpr int RK = NTH * E / DK, RV = NTH * E / DVS;
     const int kcol = tid % (DK / E) * E, krow = tid / (DK / E), vcol = tid % (DVS / E) * E, vrow = tid / (DVS / E);
     const bool kin = kcol < dk, vin = !moves && col0 + vcol < dv;
@@ -442,33 +494,27 @@ __global__ __launch_bounds__(dl_threads(DVS)) void k_delta_chunk(DeltaCall a) {
             if ((i + 1) * NTH <= D::TRI / 4 || tid + i * NTH < D::TRI / 4) ft[i] = *gmem(reinterpret_cast<const V4*>(p + 4 * (tid + i * NTH)));
         if (tid < D::GATES) fg = gmem(p)[D::TRI + tid];
     };
-    // Q and K in LDS: unit (16 bytes) u of row r at u ^ mix(r).  bf16: each block of KB columns is stored in
-    // the order 4 (g, tile) + r, for whole 16-byte operand reads beside S's, whose lanes hold
-    // rows 4 g .. 4 g + 3 of two tiles.
+    // Q and K in LDS: unit (16 bytes) u of row r at u ^ mix(r): 16 lanes with 16 rows meet every bank once
     const auto place = [](uint32_t row, uint32_t u) -> uint32_t {
         constexpr int UNITS = DK / E;
         const uint32_t m = !BF16 ? row % 16 : UNITS == 8 ? 4 * (row / 2 % 2) + row / 4 % 4 : 4 * (row % 4) + row / 4 % 4;
         return (row * UNITS + (u ^ m)) * E;
     };
-    const auto put_rows = [&](T* to, auto& f, int rows) {
+    const auto put_rows = [&](T* to, auto& f) {
 #pragma unroll
         for (int i = 0; i < UK; ++i) {
-            const int row = krow + i * RK, u = kcol / E;
-            if (!kin || row >= rows) f[i] = Frag{};
-            if constexpr (BF16) {
-                const int at = u / 4 * 4 + u % 2 * 2, half = u / 2 % 2 * 4;
-                *smem_ptr(reinterpret_cast<BF4*>(to + place(row, at) + half)) = __builtin_shufflevector(f[i], f[i], 0, 1, 2, 3);
-                *smem_ptr(reinterpret_cast<BF4*>(to + place(row, at + 1) + half)) = __builtin_shufflevector(f[i], f[i], 4, 5, 6, 7);
-            } else *smem_ptr(reinterpret_cast<Frag*>(to + place(row, u))) = f[i];
+            if (!kin) f[i] = Frag{};
+            *smem_ptr(reinterpret_cast<Frag*>(to + place(krow + i * RK, kcol / E))) = f[i];
         }
     };
     const auto row_frag = [&](const T* from, int tile, int kb) {
         return *smem_ptr(reinterpret_cast<const Frag*>(from + place(16 * tile + l16, kb * 4 + g)));
     };
-    // columns 16 kt + l16 of K, as an operand over the positions of block kb
+    // tile kt of K's columns, as an operand over the positions of block kb
     const auto transposed = [&](int kt, int kb) {
         Frag f;
         if constexpr (BF16) {
+            // a 16-lane group reads 4 positions x 16 columns and gets them transposed
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const T* p = ks + place(KB * kb + 16 * h + 4 * g + l16 / 4, kt / 2 * 4 + l16 % 4) + kt % 2 * 4;
@@ -482,68 +528,38 @@ __global__ __launch_bounds__(dl_threads(DVS)) void k_delta_chunk(DeltaCall a) {
         }
         return f;
     };
-    // fp32 values of a block's tiles as the sum of parts, each the nearest to what is left
-    const auto split = [](const V4* x, auto& f) {
-        constexpr int N = sizeof(f) / sizeof(f[0]);
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            float y = x[e / 4][e % 4];
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-                f[i][e] = (T)y;
-                if (i + 1 < N) y -= (float)f[i][e];
-            }
-        }
-    };
     const auto tri_frag = [&](const T* from, int part, int f) {
         return *smem_ptr(reinterpret_cast<const Frag*>(from + (part * NF + f) * kWave * E + lane * E));
     };
+    const auto fetch_all = [&](int c) {
+        fetch(fk, kp, a.k.pos, c, krow, RK, klcol, kleft);
+        if (!moves) fetch(fv, vp, a.v.pos, c, vrow, RV, vlcol, vleft);
+        if constexpr (OUT) fetch(fq, qp, a.q.pos, c, krow, RK, klcol, kleft);
+        fetch_t(c);
+    };
 
-    if (c0 < c1) {
-        fetch(fk, kp, a.k.pos, c0, krow, RK, klcol, kleft);
-        if (!moves) fetch(fv, vp, a.v.pos, c0, vrow, RV, vlcol, vleft);
-        if constexpr (OUT) fetch(fq, qp, a.q.pos, c0, krow, RK, klcol, kleft);
-        fetch_t(c0);
-    }
+    if (c0 < c1) fetch_all(c0);
     for (int c = c0; c < c1; ++c) {
         const int rows = len - c * C;   // positions from the chunk's first on
-        put_rows(ks, fk, rows);
-        if constexpr (OUT) put_rows(qs, fq, rows);
+        put_rows(ks, fk);
+        if constexpr (OUT) put_rows(qs, fq);
         if (!moves) {
 #pragma unroll
             for (int i = 0; i < UV; ++i) {
-                if (!vin || vrow + i * RV >= rows) fv[i] = Frag{};
+                if (!vin) fv[i] = Frag{};
                 *smem_ptr(reinterpret_cast<Frag*>(vs + (vrow + i * RV) * PV + vcol)) = fv[i];
             }
         }
 #pragma unroll
         for (int i = 0; i < UT; ++i)
-            if ((i + 1) * NTH <= D::TRI / 4 || tid + i * NTH < D::TRI / 4) {
-                V4 y = ft[i];
-#pragma unroll
-                for (int p = 0; p < PARTS; ++p) {
-                    Four z;
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        z[r] = (T)y[r];
-                        y[r] -= (float)z[r];
-                    }
-                    *smem_ptr(reinterpret_cast<Four*>(ts + p * D::TRI + 4 * (tid + i * NTH))) = z;
-                }
-            }
+            if ((i + 1) * NTH <= D::TRI / 4 || tid + i * NTH < D::TRI / 4) split_to<BF16, PARTS>(ft[i], ts + 4 * (tid + i * NTH), D::TRI);
         if (tid < D::GATES) gs[tid] = fg;
         __syncthreads();
-        // the next chunk's (the last one's again at the end: no branch, so that nothing waits for them before their use)
-        const int ahead = c + 1 < c1 ? c + 1 : c;
-        fetch(fk, kp, a.k.pos, ahead, krow, RK, klcol, kleft);
-        if (!moves) fetch(fv, vp, a.v.pos, ahead, vrow, RV, vlcol, vleft);
-        if constexpr (OUT) fetch(fq, qp, a.q.pos, ahead, krow, RK, klcol, kleft);
-        fetch_t(ahead);
 
         if constexpr (OUT) {
             // P^T, tiles of 16 keys x 16 queries, jt <= it, shared out among the waves
 #pragma unroll
-            for (int at = 0; at < CT * (CT + 1) / 2; at += WAVES) {
+            for (int at = 0; at < CT * (CT + 1) / 2; at += kDcWaves) {
                 const int tile = at + wave;
                 if (tile >= CT * (CT + 1) / 2) break;
                 const int it = tile < 1 ? 0 : tile < 3 ? 1 : tile < 6 ? 2 : 3, jt = tile - it * (it + 1) / 2;
@@ -559,37 +575,31 @@ __global__ __launch_bounds__(dl_threads(DVS)) void k_delta_chunk(DeltaCall a) {
                     const int j = 16 * jt + 4 * g + r;
                     p[r] = j <= i ? p[r] * exp_of(gi, Gate{hi[r], lo[r]}) : 0.f;
                 }
-                const auto to = [&](int tile, int part) {
-                    return smem_ptr(reinterpret_cast<Four*>(ps + part * D::TRI + (D::frag(it, tile / PER) * kWave + lane) * E + tile % PER * 4));
-                };
-#pragma unroll
-                for (int part = 0; part < HALF; ++part) {
-                    Four z;
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        z[r] = (T)p[r];
-                        p[r] -= (float)z[r];
-                    }
-                    *to(jt, part) = z;
-                    if (PER == 2 && it == jt && it % 2 == 0) *to(jt + 1, part) = Four{};
-                }
+                T* const to = ps + (D::frag(it, jt / PER) * kWave + lane) * E;
+                split_to<BF16, HALF>(p, to + jt % PER * 4, D::TRI);
+                if (PER == 2 && it == jt && it % 2 == 0) split_to<BF16, HALF>(V4{0.f, 0.f, 0.f, 0.f}, to + 4, D::TRI);
             }
         }
         // K E (rows are positions), and O^T = E^T Q^T (columns are positions)
-        V4 R[CT] = {}, O[OUT ? CT : 1] = {};
+        V4 R[NC][CT] = {}, O[OUT ? NC : 1][OUT ? CT : 1] = {};
 #pragma unroll
         for (int kb = 0; kb < DK / KB; ++kb) {
-            Frag f[PARTS];
-            split(&S[kb * PER], f);
+            Frag f[NC][PARTS];
+#pragma unroll
+            for (int nc = 0; nc < NC; ++nc) split<BF16, PARTS>(&S[nc][kb * PER], f[nc]);
 #pragma unroll
             for (int it = 0; it < CT; ++it) {
                 const Frag k = row_frag(ks, it, kb);
 #pragma unroll
-                for (int i = PARTS - 1; i >= 0; --i) R[it] = M::mma(k, f[i], R[it]);
+                for (int i = PARTS - 1; i >= 0; --i)
+#pragma unroll
+                    for (int nc = 0; nc < NC; ++nc) R[nc][it] = M::mma(k, f[nc][i], R[nc][it]);
                 if constexpr (OUT) {
                     const Frag q = row_frag(qs, it, kb);
 #pragma unroll
-                    for (int i = HALF - 1; i >= 0; --i) O[it] = M::mma(f[i], q, O[it]);
+                    for (int i = HALF - 1; i >= 0; --i)
+#pragma unroll
+                        for (int nc = 0; nc < NC; ++nc) O[nc][it] = M::mma(f[nc][i], q, O[nc][it]);
                 }
             }
         }
@@ -597,167 +607,197 @@ __global__ __launch_bounds__(dl_threads(DVS)) void k_delta_chunk(DeltaCall a) {
 #pragma unroll
         for (int it = 0; it < CT; ++it) {
             const V4 e = *smem_ptr(reinterpret_cast<const V4*>(&gs[16 * it + 4 * g]));
-            V4 v = {0.f, 0.f, 0.f, 0.f};
-            if (!moves) {
-                if constexpr (BF16) {
-                    const T* p = vs + (16 * it + 4 * g + l16 / 4) * PV + 16 * wave + l16 % 4 * 4;
-                    const BF4 y = __builtin_bit_cast(BF4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((FI_SHARED S4*)(p)));
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) v[r] = (float)y[r];
-                } else {
+            for (int nc = 0; nc < NC; ++nc) {
+                V4 v = {0.f, 0.f, 0.f, 0.f};
+                if (!moves) {
+                    if constexpr (BF16) {
+                        const T* p = vs + (16 * it + 4 * g + l16 / 4) * PV + wcol + 16 * nc + l16 % 4 * 4;
+                        const BF4 y = __builtin_bit_cast(BF4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((FI_SHARED S4*)(p)));
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) v[r] = smem_ptr(vs)[(16 * it + 4 * g + r) * PV + 16 * wave + l16];
+                        for (int r = 0; r < 4; ++r) v[r] = (float)y[r];
+                    } else {
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) v[r] = smem_ptr(vs)[(16 * it + 4 * g + r) * PV + wcol + 16 * nc + l16];
+                    }
                 }
-            }
 #pragma unroll
-            for (int r = 0; r < 4; ++r) R[it][r] = fmaf(-e[r], R[it][r], v[r]);
+                for (int r = 0; r < 4; ++r) R[nc][it][r] = fmaf(-e[r], R[nc][it][r], v[r]);
+            }
         }
         // U = T R
-        V4 U[CT] = {};
+        V4 U[NC][CT] = {};
 #pragma unroll
         for (int kb = 0; kb < C / KB; ++kb) {
-            Frag f[PARTS];
-            split(&R[kb * PER], f);
+            Frag f[NC][PARTS];
+#pragma unroll
+            for (int nc = 0; nc < NC; ++nc) split<BF16, PARTS>(&R[nc][kb * PER], f[nc]);
 #pragma unroll
             for (int it = kb * PER; it < CT; ++it)
 #pragma unroll
                 for (int p = PARTS - 1; p >= 0; --p) {
                     const Frag t = tri_frag(ts, p, D::frag(it, kb));
 #pragma unroll
-                    for (int i = PARTS - 1 - p; i >= 0; --i) U[it] = M::mma(t, f[i], U[it]);
+                    for (int i = PARTS - 1 - p; i >= 0; --i)
+#pragma unroll
+                        for (int nc = 0; nc < NC; ++nc) U[nc][it] = M::mma(t, f[nc][i], U[nc][it]);
                 }
         }
         if constexpr (OUT) {
             // O = e^G Q E + P U
 #pragma unroll
-            for (int it = 0; it < CT; ++it) O[it] *= gs[16 * it + l16];
+            for (int it = 0; it < CT; ++it) {
+                const float e = gs[16 * it + l16];
+#pragma unroll
+                for (int nc = 0; nc < NC; ++nc) O[nc][it] *= e;
+            }
             __syncthreads();
 #pragma unroll
             for (int kb = 0; kb < C / KB; ++kb) {
-                Frag f[HALF];
-                split(&U[kb * PER], f);
+                Frag f[NC][HALF];
+#pragma unroll
+                for (int nc = 0; nc < NC; ++nc) split<BF16, HALF>(&U[nc][kb * PER], f[nc]);
 #pragma unroll
                 for (int it = kb * PER; it < CT; ++it)
 #pragma unroll
                     for (int p = HALF - 1; p >= 0; --p) {
                         const Frag t = tri_frag(ps, p, D::frag(it, kb));
 #pragma unroll
-                        for (int i = HALF - 1 - p; i >= 0; --i) O[it] = M::mma(f[i], t, O[it]);
+                        for (int i = HALF - 1 - p; i >= 0; --i)
+#pragma unroll
+                            for (int nc = 0; nc < NC; ++nc) O[nc][it] = M::mma(f[nc][i], t, O[nc][it]);
                     }
             }
-            T* const op = static_cast<T*>(a.o.p) + b * a.o.row + n * a.o.head + (int64_t)c * C * a.o.pos + col0 + 16 * wave;
-            const int left = dv - (col0 + 16 * wave + 4 * (int)g);
+            T* const op = static_cast<T*>(a.o.p) + b * a.o.row + n * a.o.head + (int64_t)c * C * a.o.pos + col0 + wcol;
 #pragma unroll
-            for (int it = 0; it < CT; ++it) {
-                Four y;
+            for (int nc = 0; nc < NC; ++nc) {
+                const int left = dv - (col0 + wcol + 16 * nc + 4 * (int)g);
 #pragma unroll
-                for (int r = 0; r < 4; ++r) y[r] = (T)(a.scale * O[it][r]);
-                if (16 * it + (int)l16 < rows) {
-                    T* to = op + (16 * it + l16) * a.o.pos + 4 * g;
-                    if constexpr (VEC) {
-                        if (left > 0) *gmem(reinterpret_cast<Four*>(to)) = y;
-                    } else
+                for (int it = 0; it < CT; ++it) {
+                    Four y;
 #pragma unroll
-                        for (int r = 0; r < 4; ++r)
-                            if (r < left) gmem(to)[r] = y[r];
+                    for (int r = 0; r < 4; ++r) y[r] = (T)(a.scale * O[nc][it][r]);
+                    if (16 * it + (int)l16 < rows) {
+                        T* to = op + (16 * it + l16) * a.o.pos + 16 * nc + 4 * g;
+                        if constexpr (VEC) {
+                            if (left > 0) *gmem(reinterpret_cast<Four*>(to)) = y;
+                        } else
+#pragma unroll
+                            for (int r = 0; r < 4; ++r)
+                                if (r < left) gmem(to)[r] = y[r];
+                    }
                 }
             }
         }
+        // the next chunk's (the last one's again at the end: no branch, so that nothing waits for them before their use)
+        fetch_all(c + 1 < c1 ? c + 1 : c);
         // S: its decay as S + (e^G - 1) S (the rounding of e^G would add up over the chunks of
         // a long memory), then the chunk's own products
         const float d = expm1f(gs[3 * C - 1]) + gs[C - 1] * gs[4 * C - 1];
 #pragma unroll
-        for (int kt = 0; kt < KT; ++kt)
+        for (int nc = 0; nc < NC; ++nc)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) S[kt][r] = fmaf(d, S[kt][r], S[kt][r]);
+            for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) S[nc][kt][r] = fmaf(d, S[nc][kt][r], S[nc][kt][r]);
 #pragma unroll
         for (int kb = 0; kb < C / KB; ++kb) {
+            Frag f[NC][PARTS];
 #pragma unroll
-            for (int it = kb * PER; it < (kb + 1) * PER; ++it) U[it] *= *smem_ptr(reinterpret_cast<const V4*>(&gs[C + 16 * it + 4 * g]));
-            Frag f[PARTS];
-            split(&U[kb * PER], f);
+            for (int nc = 0; nc < NC; ++nc) {
+#pragma unroll
+                for (int it = kb * PER; it < (kb + 1) * PER; ++it)
+                    U[nc][it] *= *smem_ptr(reinterpret_cast<const V4*>(&gs[C + 16 * it + 4 * g]));
+                split<BF16, PARTS>(&U[nc][kb * PER], f[nc]);
+            }
 #pragma unroll
             for (int kt = 0; kt < KT; ++kt) {
                 const Frag k = transposed(kt, kb);
 #pragma unroll
-                for (int i = PARTS - 1; i >= 0; --i) S[kt] = M::mma(k, f[i], S[kt]);
+                for (int i = PARTS - 1; i >= 0; --i)
+#pragma unroll
+                    for (int nc = 0; nc < NC; ++nc) S[nc][kt] = M::mma(k, f[nc][i], S[nc][kt]);
             }
         }
         __syncthreads();
     }
     float* to;
     if constexpr (OUT) to = c1 < chunks ? (c1 == a.chunk0 + a.chunks ? cp : nullptr) : a.hold ? nullptr : sp;
-    else to = moves ? a.move + ((int64_t)task * a.nseg + seg) * dk * dk : ep + (int64_t)dk * dv;
-    if (!to || scol >= width) return;
+    else to = moves ? a.move + ((int64_t)task * a.nseg + seg) * DK * DK : ep + (int64_t)dk * dv;
+    if (!to) return;
+    // (M is kept whole, DK x DK: its rows and columns beyond dk are zero)
+    const int width = moves ? DK : dv, height = moves ? DK : dk;
 #pragma unroll
-    for (int i = 0; i < 4 * KT; ++i) {
-        const int row = 4 * g + i / 4 * 16 + i % 4;
-        if (row < dk) gmem(to)[row * width + scol] = S[i / 4][i % 4];
+    for (int nc = 0; nc < NC; ++nc) {
+        const int col = scol + 16 * nc;
+        if (col < width)
+#pragma unroll
+            for (int i = 0; i < 4 * KT; ++i) {
+                const int row = row_of(i / 4) + i % 4;
+                if (row < height) gmem(to)[row * width + col] = S[nc][i / 4][i % 4];
+            }
     }
 }
 
 // States before a split row's segments, in place: ent[s + 1] holds what segment s
 // makes of zero and becomes M_s ent[s] + that; ent[0] is the row's state.
-// Four waves share out the rows of a slice of 16 columns and meet in LDS.
-constexpr int kDjThreads = 256;
+// A workgroup has a slice of 16 columns, a wave 16 rows of it; they meet in LDS.  What
+// the next segment needs is asked for a segment ahead.
+constexpr int dj_threads(int dk) { return dk / 16 * kWave; }
 template <int DK>
-__global__ __launch_bounds__(kDjThreads) void k_delta_join(DeltaCall a, int C) {
-    constexpr int KT = DK / 16, MINE = (KT + 3) / 4, PE = DK + 4;   // tiles of rows, of a wave, LDS columns
-    __shared__ __align__(16) float es[16 * PE];                      // the state, transposed
-    const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave, l16 = lane % 16, g = lane / 16;
+__global__ __launch_bounds__(dj_threads(DK)) void k_delta_join(DeltaCall a, int C) {
+    constexpr int KT = DK / 16, NTH = dj_threads(DK), PE = DK + 4;   // LDS columns
+    constexpr bool AHEAD = DK <= 128;                                 // (registers for one segment's M only)
+    __shared__ __align__(16) float es[2][16 * PE];                    // the state, transposed
+    const int tid = threadIdx.x, lane = tid % kWave, wave = __builtin_amdgcn_readfirstlane(tid / kWave), l16 = lane % 16, g = lane / 16;
     const int dk = a.dk, dv = a.dv, slices = (dv + 15) / 16;
     const int64_t task = blockIdx.x / slices, b = task / a.Hv;
-    const int n = (int)(task - b * a.Hv), col = blockIdx.x % slices * 16 + l16;
+    const int n = (int)(task - b * a.Hv), col0 = blockIdx.x % slices * 16, col = col0 + l16;
     const int64_t slot = a.slots ? a.slots[b] : b;
     if (slot < 0 || slot >= a.n_slots) return;
     int len = a.lens ? a.lens[b] : a.L;
     len = len < 0 ? 0 : len > a.L ? a.L : len;
     const int chunks = (len + C - 1) / C, stop = a.chunk0 + a.chunks < chunks ? a.chunk0 + a.chunks : chunks;
-    const int segs = (stop - a.chunk0 + a.seg_chunks - 1) / a.seg_chunks;
+    const int segs = stop <= a.chunk0 ? 1 : (stop - a.chunk0 + a.seg_chunks - 1) / a.seg_chunks;
     float* const ent = a.ent + task * a.nseg * dk * dv;
+    const float* const mine = a.move + task * a.nseg * DK * DK + (16 * wave + l16) * DK + 4 * g;
+    const int row0 = 16 * wave + 4 * g;
+    V4 m[KT], ahead[AHEAD ? KT : 1], add, next = {0.f, 0.f, 0.f, 0.f};
+    const auto ask = [&](int s, auto& x, V4& y) {
+#pragma unroll
+        for (int kt = 0; kt < KT; ++kt) x[kt] = *gmem(reinterpret_cast<const V4*>(mine + (int64_t)s * DK * DK + 16 * kt));
+        const float* const p = ent + (int64_t)(s + 1) * dk * dv;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) y[r] = row0 + r < dk && col < dv ? gmem(p)[(row0 + r) * dv + col] : 0.f;
+    };
+    if (segs > 1) ask(0, m, add);
     const float* const from = a.chunk0 ? a.carry + task * dk * dv : a.fresh || !a.state ? nullptr : a.state + (slot * a.Hv + n) * dk * (int64_t)dv;
-    for (int i = tid; i < 16 * DK; i += kDjThreads) {
-        const int row = i / 16, c = blockIdx.x % slices * 16 + i % 16;
+    for (int i = tid; i < 16 * DK; i += NTH) {
+        const int row = i / 16, c = col0 + i % 16;
         const float x = from && row < dk && c < dv ? gmem(from)[row * dv + c] : 0.f;
-        es[i % 16 * PE + row] = x;
+        es[0][i % 16 * PE + row] = x;
         if (row < dk && c < dv) gmem(ent)[row * dv + c] = x;
     }
     __syncthreads();
     for (int s = 0; s + 1 < segs; ++s) {
-        const float* const m = a.move + (task * a.nseg + s) * dk * dk;
+        if constexpr (AHEAD) {
+            if (s + 2 < segs) ask(s + 1, ahead, next);
+        }
+        V4 acc[2] = {add, {0.f, 0.f, 0.f, 0.f}};   // two, as a product waits for the one before
+#pragma unroll
+        for (int kt = 0; kt < KT; ++kt)
+            acc[kt % 2] = Mm<false>::mma(m[kt], *smem_ptr(reinterpret_cast<const V4*>(&es[s % 2][l16 * PE + 16 * kt + 4 * g])), acc[kt % 2]);
+        acc[0] += acc[1];
+        *smem_ptr(reinterpret_cast<V4*>(&es[(s + 1) % 2][l16 * PE + row0])) = acc[0];
         float* const to = ent + (int64_t)(s + 1) * dk * dv;
-        V4 acc[MINE];
 #pragma unroll
-        for (int i = 0; i < MINE; ++i) {
-            const int row0 = 16 * (wave + 4 * i) + 4 * g;
+        for (int r = 0; r < 4; ++r)
+            if (row0 + r < dk && col < dv) gmem(to)[(row0 + r) * dv + col] = acc[0][r];
+        if constexpr (AHEAD) {
 #pragma unroll
-            for (int r = 0; r < 4; ++r) acc[i][r] = row0 + r < dk && col < dv ? gmem(to)[(row0 + r) * dv + col] : 0.f;
-        }
-#pragma unroll
-        for (int kt = 0; kt < KT; ++kt) {
-            if (16 * kt >= dk) break;
-            const V4 e = *smem_ptr(reinterpret_cast<const V4*>(&es[l16 * PE + 16 * kt + 4 * g]));
-#pragma unroll
-            for (int i = 0; i < MINE; ++i) {
-                const int row = 16 * (wave + 4 * i) + l16;
-                V4 x = {0.f, 0.f, 0.f, 0.f};
-                if (row < dk) {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        if (16 * kt + 4 * g + k < dk) x[k] = gmem(m)[row * dk + 16 * kt + 4 * g + k];
-                }
-                acc[i] = Mm<false>::mma(x, e, acc[i]);
-            }
-        }
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < MINE; ++i) {
-            const int row0 = 16 * (wave + 4 * i) + 4 * g;
-            if (row0 < DK) *smem_ptr(reinterpret_cast<V4*>(&es[l16 * PE + row0])) = acc[i];
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-                if (row0 + r < dk && col < dv) gmem(to)[(row0 + r) * dv + col] = acc[i][r];
-        }
+            for (int kt = 0; kt < KT; ++kt) m[kt] = ahead[kt];
+            add = next;
+        } else if (s + 2 < segs) ask(s + 1, m, add);
         __syncthreads();
     }
 }
@@ -769,6 +809,7 @@ constexpr int64_t kDlWorkgroups = 256;  // wanted of a launch
 
 int dl_chunk(int io_bf16) { return io_bf16 ? Dl<true>::C : Dl<false>::C; }
 int64_t dl_floats(int io_bf16) { return io_bf16 ? Dl<true>::TRI + Dl<true>::GATES : Dl<false>::TRI + Dl<false>::GATES; }
+int64_t dl_wide(int dk) { return dk <= 64 ? 64 : dk <= 128 ? 128 : 256; }   // keys of the kernels
 int dl_cols(int dk) { return dk <= 64 ? 64 : 128; }
 constexpr int64_t kDlLeast = 8;         // chunks of a segment at least
 
@@ -778,10 +819,10 @@ void delta_launches(const DeltaCall& c, hipStream_t st) {
     const int values = (c.dv + DVS - 1) / DVS, all = values + (c.dk + DVS - 1) / DVS;
     k_delta_tri<BF16, DK, VEC><<<(unsigned)(tasks * c.chunks), Dl<BF16>::CT * kWave, 0, st>>>(c);
     if (c.nseg > 1) {
-        k_delta_chunk<BF16, DK, DVS, false, VEC><<<(unsigned)((units + 7) / 8 * 8 * all), dl_threads(DVS), 0, st>>>(c);
-        k_delta_join<DK><<<(unsigned)(tasks * ((c.dv + 15) / 16)), kDjThreads, 0, st>>>(c, Dl<BF16>::C);
+        k_delta_chunk<BF16, DK, DVS, false, VEC><<<(unsigned)((units + 7) / 8 * 8 * all), kDcThreads, 0, st>>>(c);
+        k_delta_join<DK><<<(unsigned)(tasks * ((c.dv + 15) / 16)), dj_threads(DK), 0, st>>>(c, Dl<BF16>::C);
     }
-    k_delta_chunk<BF16, DK, DVS, true, VEC><<<(unsigned)((units + 7) / 8 * 8 * values), dl_threads(DVS), 0, st>>>(c);
+    k_delta_chunk<BF16, DK, DVS, true, VEC><<<(unsigned)((units + 7) / 8 * 8 * values), kDcThreads, 0, st>>>(c);
 }
 
 template <bool BF16>
@@ -818,7 +859,7 @@ struct DeltaParts {
 DeltaParts delta_parts(const DeltaCall& c) {
     const size_t tasks = (size_t)c.B * c.Hv, states = (size_t)c.dk * c.dv, segs = c.nseg > 1 ? tasks * c.nseg : 0;
     const int C = dl_chunk(c.io_bf16);
-    return {tasks * c.chunks * dl_floats(c.io_bf16), segs * states, segs * c.dk * c.dk,
+    return {tasks * c.chunks * dl_floats(c.io_bf16), segs * states, segs * dl_wide(c.dk) * dl_wide(c.dk),
             (c.L + C - 1) / C > c.chunks ? tasks * states : 0};
 }
 
@@ -837,7 +878,7 @@ size_t delta_ws_bytes(int64_t B, int64_t L, int Hv, int dk, int dv, int io_bf16)
     const int slices = (dv + dl_cols(dk) - 1) / dl_cols(dk);
     const int64_t segs = chunks >= 2 * kDlLeast ? kDlWorkgroups / slices : 0;
     const int64_t carry = chunks > kDlTri / tasks ? tasks * dk * dv : 0;
-    return (size_t)(tri * dl_floats(io_bf16) + segs * (dk * dv + dk * dk) + carry) * sizeof(float);
+    return (size_t)(tri * dl_floats(io_bf16) + segs * (dk * dv + dl_wide(dk) * dl_wide(dk)) + carry) * sizeof(float);
 }
 
 hipError_t launch_delta_chunk(DeltaCall c, float* ws, hipStream_t st) {
