@@ -188,19 +188,27 @@ struct Dl {
 };
 constexpr float kLog2E = 1.44269504088896341f;
 
-// Sums of C log decays, to each position (its own included), as two floats.
+// Sums of C log decays, to each position (its own included), as two floats, in lanes % C.
 // Below -150 a decay is 0 in fp32: clamped, so that differences stay finite.
 struct Gate {
     float hi, lo;
 };
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double moved64(double v) {   // 0 where nothing comes
+    const uint64_t u = (uint64_t)__double_as_longlong(v);
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, ROWS, 0xf, false),
+                   hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), CTRL, ROWS, 0xf, false);
+    return __longlong_as_double((long long)((uint64_t)hi << 32 | lo));
+}
 template <int C>
-__device__ __forceinline__ Gate gate_sum(float g, int lane) {
+__device__ __forceinline__ Gate gate_sum(float g) {
     double s = g < -150.f ? -150.0 : (double)g;
-#pragma unroll
-    for (int d = 1; d < C; d <<= 1) {
-        const double x = __shfl_up(s, d);
-        if (lane % C >= d) s += x;
-    }
+    s += moved64<0x111, 0xf>(s);   // lanes 1, 2, 4 and 8 before in a row of 16
+    s += moved64<0x112, 0xf>(s);
+    s += moved64<0x114, 0xf>(s);
+    s += moved64<0x118, 0xf>(s);
+    s += moved64<0x142, 0xa>(s);                        // a row's last lane to the next row
+    if (C == 64) s += moved64<0x143, 0xc>(s);           // lane 31 to the upper half
     const float hi = (float)s;
     return {hi, (float)(s - hi)};
 }
@@ -208,11 +216,11 @@ __device__ __forceinline__ float exp_of(Gate a, Gate b) {   // e^{a - b}, a <= b
     return __builtin_amdgcn_exp2f(((a.hi - b.hi) + (a.lo - b.lo)) * kLog2E);
 }
 
-// One chunk's T and gates.  A in LDS; a wave inverts its 16 x 16 block on the
-// diagonal, D_i, by substitution (stable, where powers of A would not be: equal keys
-// make them as large as binomials), then forms the blocks beside it,
+// One chunk's T and gates.  A wave has 16 rows of A: it forms the block on the diagonal, inverts
+// it by substitution to D_i (stable, where powers of A would not be: equal keys make them as
+// large as binomials), and the blocks before it; then the waves meet, and
 //     T_ij = -(sum_{j < k <= i} T_ik A_kj) D_j,   j = i - 1, i - 2, ..,
-// transposed, so that a result is the next product's operand as it lies in
+// is formed transposed, so that a result is the next product's operand as it lies in
 // the registers, and what is stored is the operand that k_delta_chunk loads.
 template <bool BF16, int DK, bool VEC>
 __global__ __launch_bounds__(Dl<BF16>::CT * kWave) void k_delta_tri(DeltaCall a) {
@@ -220,8 +228,8 @@ __global__ __launch_bounds__(Dl<BF16>::CT * kWave) void k_delta_tri(DeltaCall a)
     using T = typename M::T;
     using Frag = typename M::Frag;
     using D = Dl<BF16>;
-    constexpr int C = D::C, CT = D::CT, E = D::E, KB = D::KB, PA = C + 4;
-    __shared__ __align__(16) float as[C * PA], ds[CT][16][20], gs[4][C];
+    constexpr int C = D::C, CT = D::CT, E = D::E, KB = D::KB, NK = DK / KB, PA = C + 4;
+    __shared__ __align__(16) float as[C * PA], ds[CT][16][20], gs[CT][3][C];
     const int tid = threadIdx.x, lane = tid % kWave, wave = __builtin_amdgcn_readfirstlane(tid / kWave);
     const int l16 = lane % 16, g = lane / 16;
     const int64_t unit = blockIdx.x, task = unit / a.chunks;
@@ -234,59 +242,68 @@ __global__ __launch_bounds__(Dl<BF16>::CT * kWave) void k_delta_tri(DeltaCall a)
     const int t0 = c * C, left = len - t0;   // positions from the chunk's first on
     if (left <= 0) return;
 
-    Gate mine = {0.f, 0.f};
-    if (wave == 0) {
-        const int t = t0 + lane % C;
-        float ld = 0.f, beta = 0.f;
-        if (lane % C < left) {
-            ld = gmem(static_cast<const float*>(a.ld.p))[b * a.ld.row + t * a.ld.pos + n * a.ld.head];
-            beta = gmem(static_cast<const float*>(a.beta.p))[b * a.beta.row + t * a.beta.pos + n * a.beta.head];
+    // everything that the wave reads is asked for at once
+    const int at = t0 + lane % C;
+    float ld = 0.f, beta = 0.f;
+    if (lane % C < left) {
+        ld = gmem(static_cast<const float*>(a.ld.p))[b * a.ld.row + at * a.ld.pos + n * a.ld.head];
+        beta = gmem(static_cast<const float*>(a.beta.p))[b * a.beta.row + at * a.beta.pos + n * a.beta.head];
+    }
+    const T* const kp = static_cast<const T*>(a.k.p) + b * a.k.row + n / a.G * a.k.head;
+    const auto rows = [&](int tile, Frag* f) {
+        const int r = 16 * tile + l16;
+        const T* p = kp + (int64_t)(t0 + (r < left ? r : left - 1)) * a.k.pos;
+#pragma unroll
+        for (int kb = 0; kb < NK; ++kb) {
+            const int col = kb * KB + g * E;
+            f[kb] = Frag{};
+            if (r < left && col < dk) {
+                if constexpr (VEC) f[kb] = *gmem(reinterpret_cast<const Frag*>(p + col));
+                else f[kb] = load_loose<BF16>(p, col, dk);
+            }
         }
-        mine = gate_sum<C>(ld, lane);
-        const Gate end = {__shfl(mine.hi, C - 1), __shfl(mine.lo, C - 1)};
-        float* const to = a.tri + unit * (D::TRI + D::GATES) + D::TRI;
-        if (lane < C) {
-            gs[0][lane] = mine.hi;
-            gs[1][lane] = mine.lo;
-            gs[2][lane] = beta;
-            const Gate zero = {0.f, 0.f};
+    };
+    Frag own[NK], before[CT - 1][NK];
+    rows(wave, own);
+#pragma unroll
+    for (int j = 0; j < CT - 1; ++j)
+        if (j < wave) rows(j, before[j]);
+
+    const Gate mine = gate_sum<C>(ld);
+    const auto last = [](float x) { return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(x), C - 1)); };
+    if (lane < C) {
+        gs[wave][0][lane] = mine.hi;   // a copy of its own: the waves need not wait for one another here
+        gs[wave][1][lane] = mine.lo;
+        gs[wave][2][lane] = beta;
+        if (wave == 0) {
+            float* const to = a.tri + unit * (D::TRI + D::GATES) + D::TRI;
+            const Gate zero = {0.f, 0.f}, end = {last(mine.hi), last(mine.lo)};
             to[lane] = exp_of(mine, zero);
             to[C + lane] = exp_of(end, mine);
             to[2 * C + lane] = mine.hi;
             to[3 * C + lane] = mine.lo;
         }
     }
-    __syncthreads();
-    // A, tiles of 16 x 16 on and below the diagonal
-    const T* const kp = static_cast<const T*>(a.k.p) + b * a.k.row + n / a.G * a.k.head;
-    const auto row_frag = [&](int tile, int kb) -> Frag {
-        const int r = 16 * tile + l16, col = kb * KB + g * E;
-        const T* p = kp + (int64_t)(t0 + (r < left ? r : left - 1)) * a.k.pos;
-        Frag f = {};
-        if (r < left && col < dk) {
-            if constexpr (VEC) f = *gmem(reinterpret_cast<const Frag*>(p + col));
-            else f = load_loose<BF16>(p, col, dk);
-        }
-        return f;
-    };
-    for (int tile = wave; tile < CT * (CT + 1) / 2; tile += CT) {
-        const int it = tile < 1 ? 0 : tile < 3 ? 1 : tile < 6 ? 2 : 3, jt = tile - it * (it + 1) / 2;
-        V4 p = {0.f, 0.f, 0.f, 0.f};
+    wave_order();
+    const V4 ghi = *smem_ptr(reinterpret_cast<const V4*>(&gs[wave][0][16 * wave + 4 * g])),
+             glo = *smem_ptr(reinterpret_cast<const V4*>(&gs[wave][1][16 * wave + 4 * g])),
+             gb = *smem_ptr(reinterpret_cast<const V4*>(&gs[wave][2][16 * wave + 4 * g]));
+    const auto block = [&](int jt, const Frag* f) {   // A's tile (wave, jt)
+        V4 p[2] = {};
 #pragma unroll
-        for (int kb = 0; kb < DK / KB; ++kb) {
-            const Frag x = row_frag(it, kb);
-            p = M::mma(x, it == jt ? x : row_frag(jt, kb), p);
-        }
+        for (int kb = 0; kb < NK; ++kb) p[kb % 2] = M::mma(own[kb], f[kb], p[kb % 2]);
+        p[0] += p[1];
         const int j = 16 * jt + l16;
-        const Gate gj = {gs[0][j], gs[1][j]};
+        const Gate gj = {gs[wave][0][j], gs[wave][1][j]};
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            const int i = 16 * it + 4 * g + r;
-            const Gate gi = {gs[0][i], gs[1][i]};
-            as[i * PA + j] = j < i ? gs[2][i] * exp_of(gi, gj) * p[r] : 0.f;
+            const int i = 16 * wave + 4 * g + r;
+            const float x = gb[r] * exp_of(Gate{ghi[r], glo[r]}, gj) * p[0][r];
+            as[i * PA + j] = j < i ? x : 0.f;
         }
-    }
-    __syncthreads();
+    };
+    block(wave, own);
+    wave_order();
     // row l16 of D_wave: x (I + A) = e, from the last column on
     float x[16];
 #pragma unroll
@@ -304,37 +321,38 @@ __global__ __launch_bounds__(Dl<BF16>::CT * kWave) void k_delta_tri(DeltaCall a)
 #pragma unroll
         for (int j = 0; j < 16; j += 4)
             *smem_ptr(reinterpret_cast<V4*>(&ds[wave][l16][j])) = V4{x[j], x[j + 1], x[j + 2], x[j + 3]};
+#pragma unroll
+    for (int j = 0; j < CT - 1; ++j)
+        if (j < wave) block(j, before[j]);
     __syncthreads();
-    V4 t[CT];   // t[j]: block (wave, j), transposed: its columns 4 g .. 4 g + 3 of row l16
+    // t: block (wave, j), transposed: its columns 4 g .. 4 g + 3 of row l16; the block on the diagonal last in t,
+    // those before it towards the front: indexes are constants
+    V4 t[CT];
 #pragma unroll
     for (int r = 0; r < 4; ++r) t[CT - 1][r] = g == 0 ? x[r] : g == 1 ? x[4 + r] : g == 2 ? x[8 + r] : x[12 + r];
-    // (the block on the diagonal last in t, those before it towards the front: indexes are constants)
     const auto column = [&](const float* p, int pitch) {
-        return V4{p[(4 * g) * pitch + l16], p[(4 * g + 1) * pitch + l16], p[(4 * g + 2) * pitch + l16], p[(4 * g + 3) * pitch + l16]};
+        const FI_SHARED float* q = smem_ptr(p) + 4 * g * pitch + l16;
+        return V4{q[0], q[pitch], q[2 * pitch], q[3 * pitch]};
     };
-    const auto product = [](V4 p, V4 q, V4 acc) { return Mm<false>::mma(p, q, acc); };
+    float* const to = a.tri + unit * (D::TRI + D::GATES);
+    // with beta, as operands: tile j of row `wave` is the part j % PER of operand j / PER
+    const auto put = [&](int j, V4 v) {
+        *gmem(reinterpret_cast<V4*>(to + (D::frag(wave, j / D::PER) * kWave + lane) * E + j % D::PER * 4)) = v;
+    };
+    const auto with_beta = [&](int j, V4 v) { put(j, v * *smem_ptr(reinterpret_cast<const V4*>(&gs[wave][2][16 * j + 4 * g]))); };
+    with_beta(wave, t[CT - 1]);
+    if (D::PER == 2 && wave % 2 == 0) put(wave + 1, V4{0.f, 0.f, 0.f, 0.f});
 #pragma unroll
     for (int back = 1; back < CT; ++back) {
         const int j = wave - back;
         if (j < 0) break;
-        V4 s = {0.f, 0.f, 0.f, 0.f};
+        V4 s[2] = {};
 #pragma unroll
         for (int near = 0; near < back; ++near)   // block (wave, wave - near)
-            s = product(column(as + 16 * (wave - near) * PA + 16 * j, PA), t[CT - 1 - near], s);
-        t[CT - 1 - back] = -product(column(&ds[j][0][0], 20), s, V4{0.f, 0.f, 0.f, 0.f});
+            s[near % 2] = Mm<false>::mma(column(as + 16 * (wave - near) * PA + 16 * j, PA), t[CT - 1 - near], s[near % 2]);
+        t[CT - 1 - back] = -Mm<false>::mma(column(&ds[j][0][0], 20), s[0] + s[1], V4{0.f, 0.f, 0.f, 0.f});
+        with_beta(j, t[CT - 1 - back]);
     }
-    // with beta, as operands: tile j of row `wave` is the part j % PER of operand j / PER
-    float* const to = a.tri + unit * (D::TRI + D::GATES);
-    const auto put = [&](int j, V4 v) {
-        *gmem(reinterpret_cast<V4*>(to + (D::frag(wave, j / D::PER) * kWave + lane) * E + j % D::PER * 4)) = v;
-    };
-#pragma unroll
-    for (int back = 0; back < CT; ++back) {
-        const int j = wave - back;
-        if (j < 0) break;
-        put(j, t[CT - 1 - back] * *smem_ptr(reinterpret_cast<const V4*>(&gs[2][16 * j + 4 * g])));
-    }
-    if (D::PER == 2 && wave % 2 == 0) put(wave + 1, V4{0.f, 0.f, 0.f, 0.f});
 }
 
 // Values of a block's tiles as the sum of N parts, each the nearest to what is
@@ -380,21 +398,19 @@ __device__ __forceinline__ void split_to(V4 x, typename Mm<BF16>::T* to, int pit
     } else *smem_ptr(reinterpret_cast<V4*>(to)) = x;
 }
 
-constexpr int kDcThreads = 256, kDcWaves = kDcThreads / kWave;
-
 // A wave has NC = DVS / 64 tiles of 16 columns of S in its registers, which are the
 // operand of its products as they lie there: lane (g, l16) of tile kt has column l16 and the rows row_of(kt) + r,
 // so that the tiles of one operand hold rows that follow one another for each lane.
 // The waves meet only in P and in what is staged.
-template <bool BF16, int DK, int DVS, bool OUT, bool VEC>
-__global__ __launch_bounds__(kDcThreads, DK <= 128 ? 2 : 1) void k_delta_chunk(DeltaCall a) {
+template <bool BF16, int DK, int WAVES, int NC, bool OUT, bool VEC>
+__global__ __launch_bounds__(WAVES * kWave, DK <= 128 || WAVES == 8 ? 2 : 1) void k_delta_chunk(DeltaCall a) {
     using M = Mm<BF16>;
     using T = typename M::T;
     using Frag = typename M::Frag;
     using Four = T __attribute__((ext_vector_type(4)));
     using D = Dl<BF16>;
     constexpr int C = D::C, CT = D::CT, E = D::E, KB = D::KB, PER = D::PER, NF = D::NF, PARTS = D::PARTS, HALF = D::HALF;
-    constexpr int NTH = kDcThreads, KT = DK / 16, NC = DVS / 16 / kDcWaves;
+    constexpr int NTH = WAVES * kWave, KT = DK / 16, DVS = 16 * NC * WAVES;
     constexpr int PV = DVS + E;                                  // V's LDS rows
     constexpr int UK = C * DK / E / NTH, UV = C * DVS / E / NTH; // 16-byte units of a thread
     constexpr int UT = (D::TRI / 4 + NTH - 1) / NTH;             // fours of T of a thread
@@ -538,6 +554,9 @@ __global__ __launch_bounds__(kDcThreads, DK <= 128 ? 2 : 1) void k_delta_chunk(D
         fetch_t(c);
     };
 
+    // the halves of P's operands that lie above the diagonal
+    if constexpr (OUT && PER == 2)
+        if (wave < CT / 2) split_to<BF16, HALF>(V4{0.f, 0.f, 0.f, 0.f}, ps + (D::frag(2 * wave, wave) * kWave + lane) * E + 4, D::TRI);
     if (c0 < c1) fetch_all(c0);
     for (int c = c0; c < c1; ++c) {
         const int rows = len - c * C;   // positions from the chunk's first on
@@ -555,17 +574,23 @@ __global__ __launch_bounds__(kDcThreads, DK <= 128 ? 2 : 1) void k_delta_chunk(D
             if ((i + 1) * NTH <= D::TRI / 4 || tid + i * NTH < D::TRI / 4) split_to<BF16, PARTS>(ft[i], ts + 4 * (tid + i * NTH), D::TRI);
         if (tid < D::GATES) gs[tid] = fg;
         __syncthreads();
+        // the next chunk's (the last one's again at the end: no branch, so that nothing waits for them before
+        // their use); where registers are short behind the outputs
+        constexpr bool EARLY = NC == 1;
+        if constexpr (EARLY) fetch_all(c + 1 < c1 ? c + 1 : c);
 
         if constexpr (OUT) {
-            // P^T, tiles of 16 keys x 16 queries, jt <= it, shared out among the waves
+            // P^T, tiles of 16 keys x 16 queries, jt <= it, shared out among the waves (the last
+            // ones form the last tile again: without branches the products below run beside it)
+            constexpr int TILES = CT * (CT + 1) / 2;
 #pragma unroll
-            for (int at = 0; at < CT * (CT + 1) / 2; at += kDcWaves) {
-                const int tile = at + wave;
-                if (tile >= CT * (CT + 1) / 2) break;
+            for (int at = 0; at < TILES; at += WAVES) {
+                const int tile = at + WAVES <= TILES || at + wave < TILES ? at + wave : TILES - 1;
                 const int it = tile < 1 ? 0 : tile < 3 ? 1 : tile < 6 ? 2 : 3, jt = tile - it * (it + 1) / 2;
-                V4 p = {0.f, 0.f, 0.f, 0.f};
+                V4 p[2] = {};
 #pragma unroll
-                for (int kb = 0; kb < DK / KB; ++kb) p = M::mma(row_frag(ks, jt, kb), row_frag(qs, it, kb), p);
+                for (int kb = 0; kb < DK / KB; ++kb) p[kb % 2] = M::mma(row_frag(ks, jt, kb), row_frag(qs, it, kb), p[kb % 2]);
+                p[0] += p[1];
                 const int i = 16 * it + l16;
                 const Gate gi = {gs[2 * C + i], gs[3 * C + i]};
                 const V4 hi = *smem_ptr(reinterpret_cast<const V4*>(&gs[2 * C + 16 * jt + 4 * g])),
@@ -573,11 +598,10 @@ __global__ __launch_bounds__(kDcThreads, DK <= 128 ? 2 : 1) void k_delta_chunk(D
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const int j = 16 * jt + 4 * g + r;
-                    p[r] = j <= i ? p[r] * exp_of(gi, Gate{hi[r], lo[r]}) : 0.f;
+                    const float x = p[0][r] * exp_of(gi, Gate{hi[r], lo[r]});
+                    p[0][r] = j <= i ? x : 0.f;
                 }
-                T* const to = ps + (D::frag(it, jt / PER) * kWave + lane) * E;
-                split_to<BF16, HALF>(p, to + jt % PER * 4, D::TRI);
-                if (PER == 2 && it == jt && it % 2 == 0) split_to<BF16, HALF>(V4{0.f, 0.f, 0.f, 0.f}, to + 4, D::TRI);
+                split_to<BF16, HALF>(p[0], ps + (D::frag(it, jt / PER) * kWave + lane) * E + jt % PER * 4, D::TRI);
             }
         }
         // K E (rows are positions), and O^T = E^T Q^T (columns are positions)
@@ -587,21 +611,23 @@ __global__ __launch_bounds__(kDcThreads, DK <= 128 ? 2 : 1) void k_delta_chunk(D
             Frag f[NC][PARTS];
 #pragma unroll
             for (int nc = 0; nc < NC; ++nc) split<BF16, PARTS>(&S[nc][kb * PER], f[nc]);
+            Frag k[CT], q[OUT ? CT : 1];
 #pragma unroll
             for (int it = 0; it < CT; ++it) {
-                const Frag k = row_frag(ks, it, kb);
-#pragma unroll
-                for (int i = PARTS - 1; i >= 0; --i)
-#pragma unroll
-                    for (int nc = 0; nc < NC; ++nc) R[nc][it] = M::mma(k, f[nc][i], R[nc][it]);
-                if constexpr (OUT) {
-                    const Frag q = row_frag(qs, it, kb);
-#pragma unroll
-                    for (int i = HALF - 1; i >= 0; --i)
-#pragma unroll
-                        for (int nc = 0; nc < NC; ++nc) O[nc][it] = M::mma(f[nc][i], q, O[nc][it]);
-                }
+                k[it] = row_frag(ks, it, kb);
+                if constexpr (OUT) q[it] = row_frag(qs, it, kb);
             }
+#pragma unroll
+            for (int i = PARTS - 1; i >= 0; --i)
+#pragma unroll
+                for (int it = 0; it < CT; ++it)
+#pragma unroll
+                    for (int nc = 0; nc < NC; ++nc) {
+                        R[nc][it] = M::mma(k[it], f[nc][i], R[nc][it]);
+                        if constexpr (OUT) {
+                            if (i < HALF) O[nc][it] = M::mma(f[nc][i], q[it], O[nc][it]);
+                        }
+                    }
         }
         // R = V - diag(e^G) K E
 #pragma unroll
@@ -633,15 +659,17 @@ __global__ __launch_bounds__(kDcThreads, DK <= 128 ? 2 : 1) void k_delta_chunk(D
 #pragma unroll
             for (int nc = 0; nc < NC; ++nc) split<BF16, PARTS>(&R[nc][kb * PER], f[nc]);
 #pragma unroll
-            for (int it = kb * PER; it < CT; ++it)
+            for (int p = PARTS - 1; p >= 0; --p) {
+                Frag t[CT];
 #pragma unroll
-                for (int p = PARTS - 1; p >= 0; --p) {
-                    const Frag t = tri_frag(ts, p, D::frag(it, kb));
+                for (int it = kb * PER; it < CT; ++it) t[it] = tri_frag(ts, p, D::frag(it, kb));
 #pragma unroll
-                    for (int i = PARTS - 1 - p; i >= 0; --i)
+                for (int i = PARTS - 1 - p; i >= 0; --i)
 #pragma unroll
-                        for (int nc = 0; nc < NC; ++nc) U[nc][it] = M::mma(t, f[nc][i], U[nc][it]);
-                }
+                    for (int it = kb * PER; it < CT; ++it)
+#pragma unroll
+                        for (int nc = 0; nc < NC; ++nc) U[nc][it] = M::mma(t[it], f[nc][i], U[nc][it]);
+            }
         }
         if constexpr (OUT) {
             // O = e^G Q E + P U
@@ -658,16 +686,19 @@ __global__ __launch_bounds__(kDcThreads, DK <= 128 ? 2 : 1) void k_delta_chunk(D
 #pragma unroll
                 for (int nc = 0; nc < NC; ++nc) split<BF16, HALF>(&U[nc][kb * PER], f[nc]);
 #pragma unroll
-                for (int it = kb * PER; it < CT; ++it)
+                for (int p = HALF - 1; p >= 0; --p) {
+                    Frag t[CT];
 #pragma unroll
-                    for (int p = HALF - 1; p >= 0; --p) {
-                        const Frag t = tri_frag(ps, p, D::frag(it, kb));
+                    for (int it = kb * PER; it < CT; ++it) t[it] = tri_frag(ps, p, D::frag(it, kb));
 #pragma unroll
-                        for (int i = HALF - 1 - p; i >= 0; --i)
+                    for (int i = HALF - 1 - p; i >= 0; --i)
 #pragma unroll
-                            for (int nc = 0; nc < NC; ++nc) O[nc][it] = M::mma(f[nc][i], t, O[nc][it]);
-                    }
+                        for (int it = kb * PER; it < CT; ++it)
+#pragma unroll
+                            for (int nc = 0; nc < NC; ++nc) O[nc][it] = M::mma(f[nc][i], t[it], O[nc][it]);
+                }
             }
+            const bool whole = rows >= C;
             T* const op = static_cast<T*>(a.o.p) + b * a.o.row + n * a.o.head + (int64_t)c * C * a.o.pos + col0 + wcol;
 #pragma unroll
             for (int nc = 0; nc < NC; ++nc) {
@@ -677,7 +708,7 @@ __global__ __launch_bounds__(kDcThreads, DK <= 128 ? 2 : 1) void k_delta_chunk(D
                     Four y;
 #pragma unroll
                     for (int r = 0; r < 4; ++r) y[r] = (T)(a.scale * O[nc][it][r]);
-                    if (16 * it + (int)l16 < rows) {
+                    if (whole || 16 * it + (int)l16 < rows) {
                         T* to = op + (16 * it + l16) * a.o.pos + 16 * nc + 4 * g;
                         if constexpr (VEC) {
                             if (left > 0) *gmem(reinterpret_cast<Four*>(to)) = y;
@@ -689,8 +720,7 @@ __global__ __launch_bounds__(kDcThreads, DK <= 128 ? 2 : 1) void k_delta_chunk(D
                 }
             }
         }
-        // the next chunk's (the last one's again at the end: no branch, so that nothing waits for them before their use)
-        fetch_all(c + 1 < c1 ? c + 1 : c);
+        if constexpr (!EARLY) fetch_all(c + 1 < c1 ? c + 1 : c);
         // S: its decay as S + (e^G - 1) S (the rounding of e^G would add up over the chunks of
         // a long memory), then the chunk's own products
         const float d = expm1f(gs[3 * C - 1]) + gs[C - 1] * gs[4 * C - 1];
@@ -711,12 +741,16 @@ __global__ __launch_bounds__(kDcThreads, DK <= 128 ? 2 : 1) void k_delta_chunk(D
                 split<BF16, PARTS>(&U[nc][kb * PER], f[nc]);
             }
 #pragma unroll
-            for (int kt = 0; kt < KT; ++kt) {
-                const Frag k = transposed(kt, kb);
+            for (int k0 = 0; k0 < KT; k0 += 4) {   // a few at a time: a product does not wait for the one before
+                Frag k[4];
+#pragma unroll
+                for (int kt = 0; kt < 4; ++kt) k[kt] = transposed(k0 + kt, kb);
 #pragma unroll
                 for (int i = PARTS - 1; i >= 0; --i)
 #pragma unroll
-                    for (int nc = 0; nc < NC; ++nc) S[nc][kt] = M::mma(k, f[nc][i], S[nc][kt]);
+                    for (int kt = 0; kt < 4; ++kt)
+#pragma unroll
+                        for (int nc = 0; nc < NC; ++nc) S[nc][k0 + kt] = M::mma(k[kt], f[nc][i], S[nc][k0 + kt]);
             }
         }
         __syncthreads();
@@ -813,23 +847,26 @@ int64_t dl_wide(int dk) { return dk <= 64 ? 64 : dk <= 128 ? 128 : 256; }   // k
 int dl_cols(int dk) { return dk <= 64 ? 64 : 128; }
 constexpr int64_t kDlLeast = 8;         // chunks of a segment at least
 
-template <bool BF16, int DK, int DVS, bool VEC>
+// (WAVES x NC columns of 16 to a slice; the segments' pass may share them out otherwise)
+template <bool BF16, int DK, int WAVES, int NC, int SWAVES, int SNC, bool VEC>
 void delta_launches(const DeltaCall& c, hipStream_t st) {
+    constexpr int DVS = 16 * NC * WAVES;
+    static_assert(WAVES * NC == SWAVES * SNC, "the same slices");
     const int64_t tasks = c.B * c.Hv, units = tasks * c.nseg;
     const int values = (c.dv + DVS - 1) / DVS, all = values + (c.dk + DVS - 1) / DVS;
     k_delta_tri<BF16, DK, VEC><<<(unsigned)(tasks * c.chunks), Dl<BF16>::CT * kWave, 0, st>>>(c);
     if (c.nseg > 1) {
-        k_delta_chunk<BF16, DK, DVS, false, VEC><<<(unsigned)((units + 7) / 8 * 8 * all), kDcThreads, 0, st>>>(c);
+        k_delta_chunk<BF16, DK, SWAVES, SNC, false, VEC><<<(unsigned)((units + 7) / 8 * 8 * all), SWAVES * kWave, 0, st>>>(c);
         k_delta_join<DK><<<(unsigned)(tasks * ((c.dv + 15) / 16)), dj_threads(DK), 0, st>>>(c, Dl<BF16>::C);
     }
-    k_delta_chunk<BF16, DK, DVS, true, VEC><<<(unsigned)((units + 7) / 8 * 8 * values), kDcThreads, 0, st>>>(c);
+    k_delta_chunk<BF16, DK, WAVES, NC, true, VEC><<<(unsigned)((units + 7) / 8 * 8 * values), WAVES * kWave, 0, st>>>(c);
 }
 
 template <bool BF16>
 void delta_dims(const DeltaCall& c, hipStream_t st) {
-    if (c.dk <= 64) c.vec ? delta_launches<BF16, 64, 64, true>(c, st) : delta_launches<BF16, 64, 64, false>(c, st);
-    else if (c.dk <= 128) c.vec ? delta_launches<BF16, 128, 128, true>(c, st) : delta_launches<BF16, 128, 128, false>(c, st);
-    else c.vec ? delta_launches<BF16, 256, 128, true>(c, st) : delta_launches<BF16, 256, 128, false>(c, st);
+    if (c.dk <= 64) c.vec ? delta_launches<BF16, 64, 4, 1, 4, 1, true>(c, st) : delta_launches<BF16, 64, 4, 1, 4, 1, false>(c, st);
+    else if (c.dk <= 128) c.vec ? delta_launches<BF16, 128, 8, 1, 4, 2, true>(c, st) : delta_launches<BF16, 128, 8, 1, 4, 2, false>(c, st);
+    else c.vec ? delta_launches<BF16, 256, 4, 2, 4, 2, true>(c, st) : delta_launches<BF16, 256, 4, 2, 4, 2, false>(c, st);
 }
 
 }  // namespace
