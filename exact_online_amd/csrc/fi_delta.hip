@@ -207,8 +207,8 @@ __device__ __forceinline__ Gate gate_sum(float g) {
     s += moved64<0x112, 0xf>(s);
     s += moved64<0x114, 0xf>(s);
     s += moved64<0x118, 0xf>(s);
-    s += moved64<0x142, 0xa>(s);                        // a row's last lane to the next row
-    if (C == 64) s += moved64<0x143, 0xc>(s);           // lane 31 to the upper half
+    if (C > 16) s += moved64<0x142, 0xa>(s);            // a row's last lane to the next row
+    if (C > 32) s += moved64<0x143, 0xc>(s);            // lane 31 to the upper half
     const float hi = (float)s;
     return {hi, (float)(s - hi)};
 }
@@ -773,6 +773,255 @@ __global__ __launch_bounds__(WAVES * kWave, DK <= 128 || WAVES == 8 ? 2 : 1) voi
     }
 }
 
+// ------------------------------------------------------------ few positions
+// The chunked form with chunks of 16 positions, all of it in one wave: a wave follows a
+// row and head with 16 columns of S, forms T and P for itself and meets no other.  For
+// calls of a few chunks of 16, where one launch and no workspace are worth more than
+// forming T once for all columns.
+constexpr int kDfWaves = 4, kDfC = 16;
+
+template <bool BF16, int DK, bool VEC>
+__global__ __launch_bounds__(kDfWaves * kWave, BF16 && DK <= 128 ? 3 : DK <= 128 ? 2 : 1) void k_delta_few(DeltaCall a) {
+    using M = Mm<BF16>;
+    using T = typename M::T;
+    using Frag = typename M::Frag;
+    using Four = T __attribute__((ext_vector_type(4)));
+    using D = Dl<BF16>;
+    constexpr int E = D::E, KB = D::KB, NK = DK / KB, KT = DK / 16, PER = D::PER, PARTS = D::PARTS, HALF = D::HALF, C = kDfC;
+    __shared__ __align__(16) T ks_[kDfWaves][C * DK];
+    __shared__ __align__(16) float as_[kDfWaves][C][20], gs_[kDfWaves][4][C];
+    const int tid = threadIdx.x, lane = tid % kWave, wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+    const uint32_t l16 = (uint32_t)lane % 16, g = (uint32_t)lane / 16;
+    T* const ks = ks_[wave];
+    float (* const as)[20] = as_[wave];
+    float (* const gs)[C] = gs_[wave];
+    const int dk = a.dk, dv = a.dv, slices = (dv + 16 * kDfWaves - 1) / (16 * kDfWaves);
+    const int64_t task = blockIdx.x / slices, b = task / a.Hv;
+    const int n = (int)(task - b * a.Hv), col0 = (blockIdx.x % slices * kDfWaves + wave) * 16, col = col0 + (int)l16;
+    if (col0 >= dv) return;   // (nothing waits for this wave)
+    const int64_t slot = a.slots ? a.slots[b] : b;
+    const bool in = slot >= 0 && slot < a.n_slots;
+    int len = a.lens ? a.lens[b] : a.L;
+    len = in ? (len < 0 ? 0 : len > a.L ? a.L : len) : 0;
+
+    const auto row_of = [&](int kt) { return BF16 ? kt / 2 * 32 + (int)g * 8 + kt % 2 * 4 : 16 * kt + 4 * (int)g; };
+    float* const sp = a.state && in ? a.state + (slot * a.Hv + n) * dk * (int64_t)dv : nullptr;
+    V4 S[KT] = {};
+    if (sp && !a.fresh && col < dv && len > 0)
+#pragma unroll
+        for (int i = 0; i < 4 * KT; ++i) {
+            const int row = row_of(i / 4) + i % 4;
+            if (row < dk) S[i / 4][i % 4] = gmem(sp)[row * dv + col];
+        }
+    const T* const kp = static_cast<const T*>(a.k.p) + b * a.k.row + n / a.G * a.k.head;
+    const T* const qp = static_cast<const T*>(a.q.p) + b * a.q.row + n / a.G * a.q.head;
+    const T* const vp = static_cast<const T*>(a.v.p) + b * a.v.row + n * a.v.head + (col < dv ? col : col0);
+    const float* const ldp = static_cast<const float*>(a.ld.p) + b * a.ld.row + n * a.ld.head;
+    const float* const bp = static_cast<const float*>(a.beta.p) + b * a.beta.row + n * a.beta.head;
+    Frag fk[NK], fq[NK];
+    float fv[4], fld, fbeta;
+    // a chunk's: rows past the row's end repeat its last, and weigh nothing (beta is 0 there)
+    const auto fetch = [&](int t0) {
+        const int most = len - 1 - t0, r = (int)l16 < most ? (int)l16 : most;
+        const T *k = kp + (int64_t)(t0 + r) * a.k.pos, *q = qp + (int64_t)(t0 + r) * a.q.pos;
+#pragma unroll
+        for (int kb = 0; kb < NK; ++kb) {
+            const int c = kb * KB + (int)g * E;
+            fk[kb] = fq[kb] = Frag{};
+            if (c < dk) {
+                if constexpr (VEC) {
+                    fk[kb] = *gmem(reinterpret_cast<const Frag*>(k + c));
+                    fq[kb] = *gmem(reinterpret_cast<const Frag*>(q + c));
+                } else {
+                    fk[kb] = load_loose<BF16>(k, c, dk);
+                    fq[kb] = load_loose<BF16>(q, c, dk);
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int p = 4 * (int)g + i < most ? 4 * (int)g + i : most;
+            fv[i] = (float)gmem(vp)[(int64_t)(t0 + p) * a.v.pos];
+        }
+        fld = fbeta = 0.f;
+        if ((int)l16 <= most) {
+            fld = gmem(ldp)[(int64_t)(t0 + (int)l16) * a.ld.pos];
+            fbeta = gmem(bp)[(int64_t)(t0 + (int)l16) * a.beta.pos];
+        }
+    };
+    const auto place = [](uint32_t row, uint32_t u) -> uint32_t {   // as in k_delta_chunk
+        constexpr int UNITS = DK / E;
+        const uint32_t m = !BF16 ? row % 16 : UNITS == 8 ? 4 * (row / 2 % 2) + row / 4 % 4 : 4 * (row % 4) + row / 4 % 4;
+        return (row * UNITS + (u ^ m)) * E;
+    };
+    // four values as the first half of an operand over KB positions, the rest of which are none
+    const auto operand = [](V4 x, auto& f) {
+        constexpr int N = sizeof(f) / sizeof(f[0]);
+        const V4 both[2] = {x, {0.f, 0.f, 0.f, 0.f}};
+        split<BF16, N>(both, f);
+    };
+    if (len > 0) fetch(0);
+    for (int t0 = 0; t0 < len; t0 += C) {
+        const int left = len - t0;
+        const bool moves = !a.hold || t0 + C < len;   // the state is needed again
+        const Gate mine = gate_sum<C>(fld);
+        if (g == 0) {
+            gs[0][l16] = mine.hi;
+            gs[1][l16] = mine.lo;
+            gs[2][l16] = fbeta;
+        }
+        if (moves)
+#pragma unroll
+            for (int kb = 0; kb < NK; ++kb) *smem_ptr(reinterpret_cast<Frag*>(ks + place(l16, kb * 4 + g))) = fk[kb];
+        wave_order();
+        const V4 hi = *smem_ptr(reinterpret_cast<const V4*>(&gs[0][4 * g])), lo = *smem_ptr(reinterpret_cast<const V4*>(&gs[1][4 * g])),
+                 beta = *smem_ptr(reinterpret_cast<const V4*>(&gs[2][4 * g]));
+        const Gate zero = {0.f, 0.f}, end = {gs[0][C - 1], gs[1][C - 1]};
+        // K K^T (rows i = 4 g + r, column j = l16) and its mirror for P (rows j, column i)
+        V4 p = {0.f, 0.f, 0.f, 0.f}, w = p;
+#pragma unroll
+        for (int kb = 0; kb < NK; ++kb) {
+            p = M::mma(fk[kb], fk[kb], p);
+            w = M::mma(fk[kb], fq[kb], w);
+        }
+        V4 from_start, to_end;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int i = 4 * (int)g + r;
+            const Gate at = {hi[r], lo[r]};
+            const float x = beta[r] * exp_of(at, mine) * p[r], y = w[r] * exp_of(mine, at);
+            as[i][l16] = (int)l16 < i ? x : 0.f;
+            w[r] = i <= (int)l16 ? y : 0.f;
+            from_start[r] = exp_of(at, zero);
+            to_end[r] = exp_of(end, at);
+        }
+        __builtin_amdgcn_sched_barrier(0);   // (here and below: operands are not all read, and kept, before their use)
+        // K E, and O^T = E^T Q^T
+        V4 R = {0.f, 0.f, 0.f, 0.f}, O = R;
+#pragma unroll
+        for (int kb = 0; kb < NK; ++kb) {
+            Frag f[PARTS];
+            split<BF16, PARTS>(&S[kb * PER], f);
+#pragma unroll
+            for (int i = PARTS - 1; i >= 0; --i) {
+                R = M::mma(fk[kb], f[i], R);
+                if (i < HALF) O = M::mma(f[i], fq[kb], O);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        wave_order();
+        // row l16 of (I + A)^{-1}: x (I + A) = e, from the last column on
+        float x[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) x[j] = j == (int)l16 ? 1.f : 0.f;
+#pragma unroll
+        for (int k = 15; k > 0; --k) {
+            if (k >= left) continue;   // (rows of no positions are the identity's)
+#pragma unroll
+            for (int j0 = 0; j0 < k; j0 += 4) {
+                const V4 y = *smem_ptr(reinterpret_cast<const V4*>(&as[k][j0]));
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (j0 + j < k) x[j0 + j] = fmaf(-x[k], y[j], x[j0 + j]);
+            }
+        }
+        V4 tt, v;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            tt[r] = (g == 0 ? x[r] : g == 1 ? x[4 + r] : g == 2 ? x[8 + r] : x[12 + r]) * beta[r];
+            v[r] = fmaf(-from_start[r], R[r], fv[r]);
+        }
+        const float mine_start = exp_of(mine, zero);
+        if (t0 + C < len) fetch(t0 + C);
+        // U = T R, O = e^G Q E + P U
+        V4 U = {0.f, 0.f, 0.f, 0.f};
+        {
+            Frag f[PARTS], h[PARTS];
+            operand(tt, f);
+            operand(v, h);
+#pragma unroll
+            for (int i = PARTS - 1; i >= 0; --i)
+#pragma unroll
+                for (int j = PARTS - 1 - i; j >= 0; --j) U = M::mma(f[i], h[j], U);
+        }
+        {
+            Frag f[HALF], h[HALF];
+            operand(U, f);
+            operand(w, h);
+            O *= mine_start;
+#pragma unroll
+            for (int i = HALF - 1; i >= 0; --i)
+#pragma unroll
+                for (int j = HALF - 1 - i; j >= 0; --j) O = M::mma(f[i], h[j], O);
+        }
+        if ((int)l16 < left) {
+            Four y;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) y[r] = (T)(a.scale * O[r]);
+            T* const to = static_cast<T*>(a.o.p) + b * a.o.row + n * a.o.head + (int64_t)(t0 + (int)l16) * a.o.pos + col0 + 4 * (int)g;
+            const int room = dv - (col0 + 4 * (int)g);
+            if constexpr (VEC) {
+                if (room > 0) *gmem(reinterpret_cast<Four*>(to)) = y;
+            } else
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    if (r < room) gmem(to)[r] = y[r];
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        if (moves) {
+            const float d = expm1f(end.hi) + exp_of(end, zero) * end.lo;
+            Frag f[PARTS];
+            operand(U * to_end, f);
+#pragma unroll
+            for (int kt = 0; kt < KT; ++kt) {
+                Frag k = {};
+                if constexpr (BF16) {
+                    const T* q = ks + place(4 * g + l16 / 4, kt / 2 * 4 + l16 % 4) + kt % 2 * 4;
+                    const BF4 y = __builtin_bit_cast(BF4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((FI_SHARED S4*)(q)));
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) k[e] = y[e];
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) k[e] = smem_ptr(ks)[place(4 * g + e, 4 * kt + l16 / 4) + l16 % 4];
+                }
+#pragma unroll
+                for (int r = 0; r < 4; ++r) S[kt][r] = fmaf(d, S[kt][r], S[kt][r]);
+#pragma unroll
+                for (int i = PARTS - 1; i >= 0; --i) S[kt] = M::mma(k, f[i], S[kt]);
+                if (kt % 4 == 3) __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+        wave_order();
+    }
+    if (sp && !a.hold && (len > 0 || a.fresh) && col < dv)
+#pragma unroll
+        for (int i = 0; i < 4 * KT; ++i) {
+            const int row = row_of(i / 4) + i % 4;
+            if (row < dk) gmem(sp)[row * dv + col] = S[i / 4][i % 4];
+        }
+    for (int t = len + (int)g; t < a.L; t += 4)   // o is zero past the row's end
+        if (col < dv) gmem(static_cast<T*>(a.o.p))[b * a.o.row + n * a.o.head + (int64_t)t * a.o.pos + col] = (T)0.f;
+}
+
+template <bool BF16>
+static void delta_few(const DeltaCall& c, hipStream_t st) {
+    const unsigned grid = (unsigned)(c.B * c.Hv * ((c.dv + 16 * kDfWaves - 1) / (16 * kDfWaves)));   // B Hv <= kLattnMaxRows
+    const auto go = [&](auto dk) {
+        constexpr int DK = decltype(dk)::value;
+        if (c.vec) k_delta_few<BF16, DK, true><<<grid, kDfWaves * kWave, 0, st>>>(c);
+        else k_delta_few<BF16, DK, false><<<grid, kDfWaves * kWave, 0, st>>>(c);
+    };
+    if (c.dk <= 64) go(std::integral_constant<int, 64>{});
+    else if (c.dk <= 128) go(std::integral_constant<int, 128>{});
+    else go(std::integral_constant<int, 256>{});
+}
+
+static hipError_t launch_delta_few(const DeltaCall& c, hipStream_t st) {
+    if (c.io_bf16) delta_few<true>(c, st);
+    else delta_few<false>(c, st);
+    return hipGetLastError();
+}
+
 // States before a split row's segments, in place: ent[s + 1] holds what segment s
 // makes of zero and becomes M_s ent[s] + that; ent[0] is the row's state.
 // A workgroup has a slice of 16 columns, a wave 16 rows of it; they meet in LDS.  What
@@ -871,7 +1120,16 @@ void delta_dims(const DeltaCall& c, hipStream_t st) {
 
 }  // namespace
 
-bool delta_by_steps(const DeltaCall& c) { return c.L <= 16; }
+// By steps up to a few positions, then chunks of 16 in one launch, then systems of whole
+// chunks (us, heads of 128 x 128, 32 on 16, with states, steps / 16 / whole.  bf16, one row of 3: 9 / 10
+// / 20, of 5: 10 / 10 / 20, of 48: - / 19 / 21, of 64: - / 23 / 21; 64 rows of 2: 50 / 66 / 129, of 5: 88 / 68 / 130,
+// of 48: - / 133 / 140, of 64: - / 158 / 146.  fp32, whose products take longer, 64 rows of 5: 91 / 122 / 148, of 8:
+// 125 / - / 148, of 16: 238 / 143 / 151, of 32: - / 215 / 160; one row of 32: 38 / 20 / 24, of 48: - / 25 / 32).
+DeltaRoute delta_route(const DeltaCall& c) {
+    if (c.L <= (c.io_bf16 ? 3 : 6)) return DeltaRoute::steps;
+    const bool busy = c.B * c.Hv > 512;   // the CUs are full
+    return c.L <= (c.io_bf16 || !busy ? 48 : 16) ? DeltaRoute::few : DeltaRoute::chunks;
+}
 
 void plan_delta(DeltaCall& c) {
     const int C = dl_chunk(c.io_bf16);
@@ -902,12 +1160,13 @@ DeltaParts delta_parts(const DeltaCall& c) {
 
 }  // namespace
 
-size_t delta_ws_used(const DeltaCall& c) { return delta_by_steps(c) ? 0 : delta_parts(c).all() * sizeof(float); }
+size_t delta_ws_used(const DeltaCall& c) { return delta_route(c) != DeltaRoute::chunks ? 0 : delta_parts(c).all() * sizeof(float); }
 
 size_t delta_ws_bytes(int64_t B, int64_t L, int Hv, int dk, int dv, int io_bf16) {
     DeltaCall c = {};
     c.L = (int)L;
-    if (delta_by_steps(c)) return 0;
+    c.B = B, c.Hv = Hv, c.io_bf16 = io_bf16;
+    if (delta_route(c) != DeltaRoute::chunks) return 0;   // nor do smaller calls
     const int64_t C = dl_chunk(io_bf16), tasks = B * Hv, chunks = (L + C - 1) / C;
     // systems: of all chunks, or of as many as are held at a time (one of each head at least)
     const int64_t held = std::max(kDlTri, tasks), tri = chunks > held / tasks ? held : tasks * chunks;
@@ -918,7 +1177,10 @@ size_t delta_ws_bytes(int64_t B, int64_t L, int Hv, int dk, int dv, int io_bf16)
     return (size_t)(tri * dl_floats(io_bf16) + segs * (dk * dv + dl_wide(dk) * dl_wide(dk)) + carry) * sizeof(float);
 }
 
-hipError_t launch_delta_chunk(DeltaCall c, float* ws, hipStream_t st) {
+hipError_t launch_delta_prompt(DeltaCall c, float* ws, hipStream_t st) {
+    const DeltaRoute route = delta_route(c);
+    if (route == DeltaRoute::steps) return launch_delta_step(c, st);
+    if (route == DeltaRoute::few) return launch_delta_few(c, st);
     plan_delta(c);
     const int C = dl_chunk(c.io_bf16), all = (c.L + C - 1) / C, held = c.chunks;
     const DeltaParts p = delta_parts(c);
@@ -926,7 +1188,7 @@ hipError_t launch_delta_chunk(DeltaCall c, float* ws, hipStream_t st) {
     c.ent = c.tri + p.tri;
     c.move = c.ent + p.ent;
     c.carry = p.carry ? c.move + p.move : nullptr;
-    do {   // (an empty prompt: one launch, which may leave zeros)
+    do {
         if (all - c.chunk0 < held) c.chunks = all - c.chunk0;
         if (c.io_bf16) delta_dims<true>(c, st);
         else delta_dims<false>(c, st);

@@ -412,7 +412,7 @@ int fi_delta_prompt(fi_delta *s, const fi_delta_args *a) {
     if (rc != FI_OK || c.B == 0) return rc;
     const OnDevice here(s->device);
     FI_HIP(here.error);
-    FI_HIP(delta_by_steps(c) ? launch_delta_step(c, s->stream) : launch_delta_chunk(c, s->ws, s->stream));
+    FI_HIP(launch_delta_prompt(c, s->ws, s->stream));
     return FI_OK;
 }
 

@@ -108,12 +108,13 @@ struct DeltaCall {
 
 // Recurrent form, position by position.
 hipError_t launch_delta_step(const DeltaCall &c, hipStream_t st);
-// Chunked form; ws holds delta_ws_bytes, the most that plan_delta makes any call of these sizes and smaller ones use.
-hipError_t launch_delta_chunk(DeltaCall c, float *ws, hipStream_t st);
+// Any number of positions; ws holds delta_ws_bytes, the most that plan_delta makes any call of these sizes and smaller ones use.
+hipError_t launch_delta_prompt(DeltaCall c, float *ws, hipStream_t st);
+enum class DeltaRoute { steps, few, chunks };
+DeltaRoute delta_route(const DeltaCall &c);
 void plan_delta(DeltaCall &c);   // chunks at a time, segments
 size_t delta_ws_used(const DeltaCall &c);
 size_t delta_ws_bytes(int64_t B, int64_t L, int Hv, int dk, int dv, int io_bf16);
-bool delta_by_steps(const DeltaCall &c);   // few positions: the recurrent form
 
 // ------------------------------------------------------------ normed and turned heads
 struct RotaryCall {
