@@ -193,22 +193,9 @@ constexpr float kLog2E = 1.44269504088896341f;
 struct Gate {
     float hi, lo;
 };
-template <int CTRL, int ROWS>
-__device__ __forceinline__ double moved64(double v) {   // 0 where nothing comes
-    const uint64_t u = (uint64_t)__double_as_longlong(v);
-    const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, ROWS, 0xf, false),
-                   hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), CTRL, ROWS, 0xf, false);
-    return __longlong_as_double((long long)((uint64_t)hi << 32 | lo));
-}
 template <int C>
 __device__ __forceinline__ Gate gate_sum(float g) {
-    double s = g < -150.f ? -150.0 : (double)g;
-    s += moved64<0x111, 0xf>(s);   // lanes 1, 2, 4 and 8 before in a row of 16
-    s += moved64<0x112, 0xf>(s);
-    s += moved64<0x114, 0xf>(s);
-    s += moved64<0x118, 0xf>(s);
-    if (C > 16) s += moved64<0x142, 0xa>(s);            // a row's last lane to the next row
-    if (C > 32) s += moved64<0x143, 0xc>(s);            // lane 31 to the upper half
+    const double s = scan64<C>(g < -150.f ? -150.0 : (double)g);
     const float hi = (float)s;
     return {hi, (float)(s - hi)};
 }

@@ -52,6 +52,33 @@ __device__ __forceinline__ float wave_max(float v) {
     return wave_reduce(v, [](float a, float b) { return fmaxf(a, b); });
 }
 
+// The same moves of 64-bit values, 0 where nothing comes, and a wave's inclusive sums by them (64 lanes, or
+// 16 or 32 of them at a time): 1, 2, 4 and 8 lanes on in a row of 16, a row's last lane to
+// the next row, lane 31 to the upper half.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double moved64(double v) {
+    const uint64_t u = (uint64_t)__double_as_longlong(v);
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, ROWS, 0xf, false),
+                   hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), CTRL, ROWS, 0xf, false);
+    return __longlong_as_double((long long)((uint64_t)hi << 32 | lo));
+}
+template <int LANES = kWave>
+__device__ __forceinline__ double scan64(double v) {
+    v += moved64<0x111, 0xf>(v);
+    v += moved64<0x112, 0xf>(v);
+    v += moved64<0x114, 0xf>(v);
+    v += moved64<0x118, 0xf>(v);
+    if (LANES > 16) v += moved64<0x142, 0xa>(v);
+    if (LANES > 32) v += moved64<0x143, 0xc>(v);
+    return v;
+}
+__device__ __forceinline__ double lane64(double v, int lane) {   // a uniform lane's value
+    const uint64_t u = (uint64_t)__double_as_longlong(v);
+    const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)u, lane), hi = __builtin_amdgcn_readlane((uint32_t)(u >> 32), lane);
+    return __longlong_as_double((long long)((uint64_t)hi << 32 | lo));
+}
+__device__ __forceinline__ double sum64(double v) { return lane64(scan64(v), kWave - 1); }
+
 // lam^n = exp(n ld), n >= 0; lam^0 = 1 for lam = 0 (ld = -inf) too
 __device__ __forceinline__ float decay_pow(float ld, float n) { return n == 0.f ? 1.f : expf(n * ld); }
 

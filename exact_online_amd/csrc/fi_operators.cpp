@@ -534,7 +534,7 @@ int fi_verify_create(const fi_verify_config *cfg, fi_verify **out) {
     s->stream = static_cast<hipStream_t>(cfg->stream);
     s->ws = nullptr;
     hipError_t e = hipGetDevice(&s->device);
-    const size_t n = verify_ws_doubles(cfg->B, (int)cfg->N, cfg->V, raw_int(cfg->io_dtype) == FI_BF16);
+    const size_t n = verify_ws_doubles(cfg->B, (int)cfg->N, cfg->V);
     if (e == hipSuccess) e = dalloc(&s->ws, n * sizeof(double));
     if (e != hipSuccess) {
         fi_verify_destroy(s);
@@ -572,9 +572,8 @@ int fi_verify_run(fi_verify *s, const fi_verify_args *a) {
     c.V = f.V;
     c.N = (int)a->N;
     c.io_bf16 = io == FI_BF16;
-    constexpr double log2e = 1.4426950408889634074;
-    c.scale = (double)f.scale * log2e;
-    c.draft_scale = (double)f.draft_scale * log2e;
+    c.scale = (double)f.scale * kVerifyOctave;
+    c.draft_scale = (double)f.draft_scale * kVerifyOctave;
     c.target = a->target;
     c.target_row = a->target_row;
     c.target_ld = a->target_ld;

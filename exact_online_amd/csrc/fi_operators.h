@@ -133,11 +133,12 @@ hipError_t launch_rotary(RotaryCall c, hipStream_t st);
 
 // ------------------------------------------------------------ drafted tokens
 constexpr int kVerifyMaxRows = 1 << 22;   // rows of logits of a call
+constexpr double kVerifyOctave = 32 * 1.4426950408889634074;   // 32 log2 e
 
 struct VerifyCall {
     int64_t B, V;
     int N, io_bf16;
-    double scale, draft_scale;  // with log2 e
+    double scale, draft_scale;  // with kVerifyOctave
     const void *target, *draft;
     int64_t target_row, target_ld, draft_row, draft_ld;
     const int64_t *tokens;
@@ -146,16 +147,16 @@ struct VerifyCall {
     int64_t *out;
     int32_t *kept;
     float *logprob;
-    // a row's parts of `per` logits: sums[B (2 N + 1)][parts] of the probabilities against 2^ref, and
-    // rest[B][parts] of what the token is drawn from
-    int parts;
-    int64_t per;
+    // a row's parts of `per` logits: sums[B (2 N + 1)][parts] of the probabilities against ref; its blocks of
+    // `block` logits, shared out among `keepers` workgroups: rest[B][blocks] of what the token is drawn from
+    int parts, blocks, keepers;
+    int64_t per, block;
     double *sums, *ref, *rest;
 };
 
 hipError_t launch_verify(VerifyCall c, hipStream_t st);
-void plan_verify(VerifyCall &c);   // a row's parts
+void plan_verify(VerifyCall &c);   // a row's parts and blocks
 size_t verify_ws_used(const VerifyCall &c);                            // doubles of a call
-size_t verify_ws_doubles(int64_t B, int N, int64_t V, int io_bf16);   // the most of any call of so many rows and drafts or fewer
+size_t verify_ws_doubles(int64_t B, int N, int64_t V);   // the most of any call of so many rows and drafts or fewer
 
 }  // namespace fi

@@ -11,34 +11,45 @@ namespace fi {
 
 constexpr int kVeThreads = 256, kVeWaves = kVeThreads / kWave;
 constexpr int kVeRun = 8;                          // logits of a thread that follow one another
-constexpr int kVeBlock = kVeThreads * kVeRun;      // a part is a multiple of these
-constexpr int kVeMaxParts = 2 * kWave;
+constexpr int kVeBlock = kVeThreads * kVeRun;      // logits of a workgroup at a time
+constexpr int kVeMaxParts = 2 * kWave, kVeMaxBlocks = 2 * kWave;
 constexpr int kVeMaxDrafts = 63, kVeMaxRows = 2 * kVeMaxDrafts + 1;
-constexpr double kVeLow = -1100.0;                 // 2^kVeLow = 0
+constexpr int kVeTable = 32;                       // powers of an octave
+constexpr double kVeLow = -1020.0 * kVeTable;      // the least power that is formed
 constexpr double kVeNone = -1e300;                 // the reference of a part without a token
 
-// 2^x, x <= 1000, to 2^-45 of itself: n = rint(x), the series of e^{(x - n) ln 2} to the 11th power.
-__device__ __forceinline__ double exp2_64(double x) {
-    x = fmax(x, kVeLow);
-    const double n = rint(x), f = (x - n) * 0.69314718055994530942;
-    double p = fma(f, 1.0 / 39916800.0, 1.0 / 3628800.0);
-    p = fma(f, p, 1.0 / 362880.0);
-    p = fma(f, p, 1.0 / 40320.0);
-    p = fma(f, p, 1.0 / 5040.0);
-    p = fma(f, p, 1.0 / 720.0);
-    p = fma(f, p, 1.0 / 120.0);
-    p = fma(f, p, 1.0 / 24.0);
-    p = fma(f, p, 1.0 / 6.0);
-    p = fma(f, p, 0.5);
-    p = fma(f, p, 1.0);
-    p = fma(f, p, 1.0);
-    return ldexp(p, (int)n);
+// 2^{x / 32} for kVeLow <= x <= 32000 to 2^-48 of itself: n = rint(x), 2^{n / 32} from a
+// table of 32 in LDS (whatever lanes read of it, no two entries share a bank) and an exponent, and the
+// series of e^{(x - n) ln 2 / 32} to the 5th power (the next term is 2e-15).  Scales
+// come with the 32, so that an operation has one constant at most.
+struct Powers {
+    const FI_SHARED double* table;
+    double first;   // (ln 2 / 32)^5 / 5!, kept in a register
+};
+__device__ __forceinline__ Powers make_powers(double* t, int tid) {
+    if (tid < kVeTable) t[tid] = exp2((double)tid / kVeTable);
+    double first = 3.973709984549416e-11;
+    asm("" : "+v"(first));
+    return {smem_ptr(t), first};
 }
-__device__ __forceinline__ double wave_sum64(double v) {
-#pragma unroll
-    for (int d = 1; d < kWave; d <<= 1) v += __shfl_xor(v, d);
-    return v;
+__device__ __forceinline__ double power(double x, const Powers& to) {
+    constexpr double shift = 6755399441055744.0;   // 1.5 2^52: a sum's lowest bits are the nearest whole number
+    const double k = x + shift, r = x - (k - shift);
+    const uint32_t n = (uint32_t)(uint64_t)__double_as_longlong(k);
+    double p = __builtin_fma(r, to.first, 9.172562701824643e-09);   // the 4th power's, and so on
+    p = __builtin_fma(r, p, 1.693850972437182e-06);
+    p = __builtin_fma(r, p, 0.0002345961982022468);
+    p = __builtin_fma(r, p, 0.02166084939249829);
+    p = __builtin_fma(r, p, 1.0);
+    const uint64_t u = (uint64_t)__double_as_longlong(to.table[n & (kVeTable - 1)] * p);
+    const uint32_t high = (uint32_t)(u >> 32) + ((n & ~(uint32_t)(kVeTable - 1)) << 15);   // (n >> 5) << 20
+    return __longlong_as_double((long long)((uint64_t)high << 32 | (uint32_t)u));
 }
+// A logit's weight against the reference; what is far below it or -inf weighs next to nothing (2^kVeLow).
+__device__ __forceinline__ double weight(float z, double ref, double c, const Powers& to) {
+    return power(fmax(((double)z - ref) * c, kVeLow), to);
+}
+constexpr double kVeLeast = 0x1p-1020;   // 2^{kVeLow / 32}: taken off where nothing has to be 0
 
 __device__ __forceinline__ int drafts_of(const VerifyCall& a, int64_t b) {
     const int n = a.lens ? a.lens[b] : a.N;
@@ -54,7 +65,7 @@ __device__ __forceinline__ const typename Mm<BF16>::T* logits_of(const VerifyCal
                     : static_cast<const T*>(a.draft) + b * a.draft_row + (i - a.N - 1) * a.draft_ld;
 }
 
-// A wave takes one part of one row of logits: the sum of 2^((z - R) c) with a reference R near the
+// A wave takes one part of one row of logits: the sum of 2^((z - R) c / 32) with a reference R near the
 // largest z (differences first: they are exact, however large the logits are).  A row
 // that is no distribution has a sum that is NaN or 0.
 template <bool BF16>
@@ -64,19 +75,20 @@ __global__ __launch_bounds__(kVeThreads) void k_verify_sums(VerifyCall a) {
     using Frag = typename M::Frag;
     using Loose = T __attribute__((ext_vector_type(M::E), aligned(sizeof(T))));
     constexpr int E = M::E, UN = 16 / E, STEP = kWave * E;
+    __shared__ double table_[kVeTable];
     const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), rows = rows_of(a);
     const int64_t unit = (int64_t)blockIdx.x * kVeWaves + wave, row = unit / a.parts, b = row / rows;
-    if (b >= a.B) return;
-    const int i = (int)(row - b * rows), n = drafts_of(a, b);
-    if (i <= a.N ? i > n : i - a.N - 1 >= n) return;   // no draft there
-    const T* const z = logits_of<BF16>(a, b, i);
+    const int i = (int)(row - b * rows);
+    bool here = b < a.B;
+    if (here) {
+        const int n = drafts_of(a, b);
+        here = i <= a.N ? i <= n : i - a.N - 1 < n;   // a draft there
+    }
+    const T* const z = here ? logits_of<BF16>(a, b, i) : nullptr;
     const double c = i <= a.N ? a.scale : a.draft_scale;
-    const int64_t v0 = (unit - row * a.parts) * a.per, v1 = v0 + a.per < a.V ? v0 + a.per : a.V;
+    const int64_t v0 = (unit - row * a.parts) * a.per, v1 = !here ? v0 : v0 + a.per < a.V ? v0 + a.per : a.V;
     const float inf = __builtin_inff();
-    double R = kVeNone, sum = 0.0;
-    bool good = true;
-    for (int64_t v = v0; v < v1; v += UN * STEP) {
-        Frag f[UN];
+    const auto load = [&](Frag* f, int64_t v) {
 #pragma unroll
         for (int u = 0; u < UN; ++u) {
             const int64_t at = v + u * STEP + lane * E;
@@ -85,6 +97,16 @@ __global__ __launch_bounds__(kVeThreads) void k_verify_sums(VerifyCall a) {
 #pragma unroll
                 for (int e = 0; e < E; ++e) f[u][e] = at + e < v1 ? gmem(z)[at + e] : (T)-inf;
         }
+    };
+    Frag f[UN], next[UN];
+    load(f, v0);
+    const Powers to = make_powers(table_, threadIdx.x);
+    __syncthreads();
+    if (!here) return;
+    double R = kVeNone, sum = 0.0;
+    bool good = true;
+    for (int64_t v = v0; v < v1; v += UN * STEP) {
+        if (v + UN * STEP < v1) load(next, v + UN * STEP);
         float most = -inf;
 #pragma unroll
         for (int u = 0; u < UN; ++u)
@@ -93,17 +115,21 @@ __global__ __launch_bounds__(kVeThreads) void k_verify_sums(VerifyCall a) {
                 most = fmaxf(most, (float)f[u][e]);
                 good = good && (float)f[u][e] < inf;   // false for NaN
             }
-        if (__ballot(most > -inf && ((double)most - R) * c > 64.0)) {
-            const double to = (double)wave_max(most);
-            sum *= exp2_64((R - to) * c);
-            R = to;
+        if (__ballot(most > -inf && ((double)most - R) * c > 64.0 * kVeTable)) {
+            const double now = (double)wave_max(most);
+            sum *= power(fmax((R - now) * c, kVeLow), to);
+            R = now;
         }
+        double s[4] = {};
 #pragma unroll
         for (int u = 0; u < UN; ++u)
 #pragma unroll
-            for (int e = 0; e < E; ++e) sum += exp2_64(((double)f[u][e] - R) * c);
+            for (int e = 0; e < E; ++e) s[(u * E + e) % 4] += weight((float)f[u][e], R, c, to);
+        sum += (s[0] + s[1]) + (s[2] + s[3]);
+#pragma unroll
+        for (int u = 0; u < UN; ++u) f[u] = next[u];
     }
-    sum = wave_sum64(sum);
+    sum = R == kVeNone ? 0.0 : sum64(sum);
     if (__ballot(!good)) sum = __builtin_nan("");
     if (lane == 0) {
         a.sums[unit] = sum;
@@ -115,16 +141,25 @@ __global__ __launch_bounds__(kVeThreads) void k_verify_sums(VerifyCall a) {
 struct Sum {
     double ref, sum;
 };
-__device__ __forceinline__ Sum whole(const VerifyCall& a, int64_t row, double c, int lane) {
+struct Parts {
+    double sum[2], ref[2];
+};
+__device__ __forceinline__ Parts parts_of(const VerifyCall& a, int64_t row, int lane) {
     const double *s = a.sums + row * a.parts, *f = a.ref + row * a.parts;
-    double sum[2] = {0.0, 0.0}, ref[2] = {kVeNone, kVeNone};
+    Parts p = {{0.0, 0.0}, {kVeNone, kVeNone}};
 #pragma unroll
     for (int i = 0; i < 2; ++i)
-        if (lane + i * kWave < a.parts) sum[i] = s[lane + i * kWave], ref[i] = f[lane + i * kWave];
-    double R = fmax(ref[0], ref[1]);
+        if (lane + i * kWave < a.parts) p.sum[i] = s[lane + i * kWave], p.ref[i] = f[lane + i * kWave];
+    return p;
+}
+__device__ __forceinline__ Sum whole(Parts p, double c, const Powers& to) {
+    // (references are logits, or kVeNone: their order is that of fp32)
+    const float most = wave_max(fmaxf(p.ref[0] > kVeNone ? (float)p.ref[0] : -__FLT_MAX__, p.ref[1] > kVeNone ? (float)p.ref[1] : -__FLT_MAX__));
+    const double R = (double)most;
+    double s = 0.0;
 #pragma unroll
-    for (int d = 1; d < kWave; d <<= 1) R = fmax(R, __shfl_xor(R, d));
-    return {R, wave_sum64(sum[0] * exp2_64((ref[0] - R) * c) + sum[1] * exp2_64((ref[1] - R) * c))};
+    for (int i = 0; i < 2; ++i) s += p.sum[i] * power(fmax((p.ref[i] - R) * c, kVeLow), to);
+    return {R, sum64(s)};
 }
 __device__ __forceinline__ bool is_some(Sum s) { return s.sum > 0.0 && s.sum < __builtin_inf(); }   // false for NaN
 
@@ -136,10 +171,10 @@ struct Weights {
     bool less;               // q is taken off
 
     // (each product rounded by itself: equal logits leave nothing)
-    __device__ __forceinline__ double of(float zp, float zq, int64_t at) const {
+    __device__ __forceinline__ double of(float zp, float zq, int64_t at, const Powers& to) const {
 #pragma clang fp contract(off)
-        double w = exp2_64(((double)zp - p.ref) * cp) * ip;
-        if (less) w = fmax(w - exp2_64(((double)zq - q.ref) * cq) * iq, 0.0);
+        double w = (weight(zp, p.ref, cp, to) - kVeLeast) * ip;
+        if (less) w = fmax(w - (weight(zq, q.ref, cq, to) - kVeLeast) * iq, 0.0);
         return at == without ? 0.0 : w;
     }
 };
@@ -171,44 +206,78 @@ __device__ __forceinline__ Weights weights_of(const VerifyCall& a, int64_t b, in
     return w;
 }
 
+// The weights of one block of row b, a thread's own sum of them
+template <bool BF16>
+__device__ __forceinline__ double block_sum(const VerifyCall& a, const Weights& w, const typename Mm<BF16>::T* zp, const typename Mm<BF16>::T* zq,
+                                            int64_t v0, int tid, const Powers& to) {
+    const int64_t v1 = v0 + a.block < a.V ? v0 + a.block : a.V;
+    double sum = 0.0;
+    for (int64_t v = v0 + tid * kVeRun; v < v1; v += kVeBlock) {
+        float p[kVeRun], q[kVeRun];
+        load_run<BF16>(p, zp, v, v1);
+        if (w.less) load_run<BF16>(q, zq, v, v1);
+#pragma unroll
+        for (int e = 0; e < kVeRun; ++e) sum += w.of(p[e], w.less ? q[e] : 0.f, v + e, to);
+    }
+    return sum;
+}
+
 // Every workgroup of a row finds how many drafts are kept (the first writes that, the tokens
-// and their log probabilities) and adds up its part of the weights that the token is drawn from.
+// and their log probabilities) and adds up the weights of its blocks, which the token is drawn from.
 template <bool BF16>
 __global__ __launch_bounds__(kVeThreads) void k_verify_keep(VerifyCall a) {
     __shared__ Sum got[kVeMaxRows];
-    __shared__ double part[kVeWaves];
+    __shared__ double part[2][kVeWaves], table_[kVeTable];
     __shared__ int kept_;
-    const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave, rows = rows_of(a);
-    const int64_t b = blockIdx.x / a.parts;
-    const int me = blockIdx.x % a.parts, n = drafts_of(a, b);
-    for (int i = wave; i < rows; i += kVeWaves)
-        if (i <= a.N ? i <= n : i - a.N - 1 < n) {
-            const Sum s = whole(a, b * rows + i, i <= a.N ? a.scale : a.draft_scale, lane);
+    const int tid = threadIdx.x, lane = tid % kWave, wave = __builtin_amdgcn_readfirstlane(tid / kWave), rows = rows_of(a);
+    const int64_t b = blockIdx.x / a.keepers;
+    const int me = blockIdx.x % a.keepers, n = drafts_of(a, b);
+    // everything that does not wait for the sums
+    int64_t x = -1;
+    float zp = 0.f, zq = 0.f, u = 0.f;
+    bool known = false;
+    if (wave == 0 && lane < n) {
+        x = a.tokens[b * a.N + lane];
+        u = a.u[b * a.N + lane];
+        known = x >= 0 && x < a.V;
+        if (known) {
+            zp = get_io<BF16>(logits_of<BF16>(a, b, lane), x);
+            if (a.draft) zq = get_io<BF16>(logits_of<BF16>(a, b, a.N + 1 + lane), x);
+        }
+    }
+    const auto used = [&](int i) { return i < rows && (i <= a.N ? i <= n : i - a.N - 1 < n); };
+    Parts next = {};
+    if (used(wave)) next = parts_of(a, b * rows + wave, lane);
+    const Powers to = make_powers(table_, tid);
+    __syncthreads();
+    for (int i = wave; i < rows; i += kVeWaves) {
+        const Parts p = next;
+        if (used(i + kVeWaves)) next = parts_of(a, b * rows + i + kVeWaves, lane);
+        if (used(i)) {
+            const Sum s = whole(p, i <= a.N ? a.scale : a.draft_scale, to);
             if (lane == 0) got[i] = s;
         }
+    }
     __syncthreads();
     if (wave == 0) {
         bool keep = false;
         double lp = 0.0;
-        if (lane < n) {
-            const int64_t x = a.tokens[b * a.N + lane];
+        if (known) {
             const Sum p = got[lane];
-            if (x >= 0 && x < a.V && is_some(p)) {
-                const double t = ((double)get_io<BF16>(logits_of<BF16>(a, b, lane), x) - p.ref) * a.scale;
+            if (is_some(p)) {
                 double q = 1.0;
                 if (a.draft) {
                     const Sum s = got[a.N + 1 + lane];
-                    q = is_some(s) ? exp2_64(((double)get_io<BF16>(logits_of<BF16>(a, b, a.N + 1 + lane), x) - s.ref) * a.draft_scale) / s.sum
-                                   : __builtin_nan("");
+                    q = is_some(s) ? (weight(zq, s.ref, a.draft_scale, to) - kVeLeast) / s.sum : __builtin_nan("");
                 }
-                keep = (double)a.u[b * a.N + lane] * q < exp2_64(t) / p.sum;
-                lp = (t - log2(p.sum)) * 0.69314718055994530942;
+                keep = (double)u * q < (weight(zp, p.ref, a.scale, to) - kVeLeast) / p.sum;
+                lp = (((double)zp - p.ref) * (a.scale / kVeTable) - log2(p.sum)) * 0.69314718055994530942;
             }
         }
         const int kept = __builtin_ctzll(~__ballot(keep));   // (lane 63 keeps none)
         if (lane == 0) kept_ = kept;
         if (me == 0 && lane <= a.N && lane != kept) {
-            a.out[b * (a.N + 1) + lane] = lane < kept ? a.tokens[b * a.N + lane] : -1;
+            a.out[b * (a.N + 1) + lane] = lane < kept ? x : -1;
             if (a.logprob) a.logprob[b * (a.N + 1) + lane] = lane < kept ? (float)lp : 0.f;
         }
         if (me == 0 && lane == 0) a.kept[b] = kept;
@@ -216,50 +285,39 @@ __global__ __launch_bounds__(kVeThreads) void k_verify_keep(VerifyCall a) {
     __syncthreads();
     const int kept = kept_;
     const Weights w = weights_of(a, b, kept, n, got[kept], a.draft && kept < n ? got[a.N + 1 + kept] : Sum{0.0, 0.0});
-    const auto* const zp = logits_of<BF16>(a, b, kept);
-    const auto* const zq = w.less ? logits_of<BF16>(a, b, a.N + 1 + kept) : zp;
-    const int64_t v0 = me * a.per, v1 = v0 + a.per < a.V ? v0 + a.per : a.V;
-    double sum = 0.0;
-    for (int64_t v = v0 + tid * kVeRun; v < v1; v += kVeBlock) {
-        float p[kVeRun], q[kVeRun];
-        load_run<BF16>(p, zp, v, v1);
-        if (w.less) load_run<BF16>(q, zq, v, v1);
-#pragma unroll
-        for (int e = 0; e < kVeRun; ++e) sum += w.of(p[e], w.less ? q[e] : 0.f, v + e);
+    const auto* const p = logits_of<BF16>(a, b, kept);
+    const auto* const q = w.less ? logits_of<BF16>(a, b, a.N + 1 + kept) : p;
+    for (int i = me, turn = 0; i < a.blocks; i += a.keepers, turn ^= 1) {
+        const double sum = sum64(block_sum<BF16>(a, w, p, q, i * a.block, tid, to));
+        if (lane == 0) part[turn][wave] = sum;
+        __syncthreads();
+        if (tid == 0) a.rest[b * a.blocks + i] = (part[turn][0] + part[turn][1]) + (part[turn][2] + part[turn][3]);
     }
-    sum = wave_sum64(sum);
-    if (lane == 0) part[wave] = sum;
-    __syncthreads();
-    if (tid == 0) a.rest[b * a.parts + me] = (part[0] + part[1]) + (part[2] + part[3]);
 }
 
-// Inclusive sums over the wave's lanes.
-__device__ __forceinline__ double wave_scan64(double v, int lane) {
-#pragma unroll
-    for (int d = 1; d < kWave; d <<= 1) {
-        const double x = __shfl_up(v, d);
-        if (lane >= d) v += x;
-    }
-    return v;
-}
-
-// A workgroup finds a row's token: the part that r falls into, then the place in it.
+// A workgroup finds a row's token: the block that r falls into, then the place in it.
 template <bool BF16>
 __global__ __launch_bounds__(kVeThreads) void k_verify_draw(VerifyCall a) {
     __shared__ Sum got[2];
-    __shared__ double total[kVeWaves], whole_, before_;
-    __shared__ int part_, last_[kVeWaves];
-    __shared__ int64_t found;
-    const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave, rows = rows_of(a);
+    __shared__ double total[2][kVeWaves], before_, table_[kVeTable], again[kVeMaxBlocks];
+    __shared__ int block_, last_[kVeWaves];
+    __shared__ unsigned long long found;   // the largest: none yet
+    const int tid = threadIdx.x, lane = tid % kWave, wave = __builtin_amdgcn_readfirstlane(tid / kWave), rows = rows_of(a);
     const int64_t b = blockIdx.x;
+    const double r = a.r[b];
+    const int i0 = 2 * lane, i1 = i0 + 1;
+    double x0 = i0 < a.blocks ? a.rest[b * a.blocks + i0] : 0.0, x1 = i1 < a.blocks ? a.rest[b * a.blocks + i1] : 0.0;
     const int n = drafts_of(a, b), kept = a.kept[b];
     const bool second = a.draft && kept < n;
+    const Powers to = make_powers(table_, tid);
+    if (tid == 0) found = ~0ull;
+    Parts parts = {};
+    if (wave == 0 || (wave == 1 && second)) parts = parts_of(a, b * rows + (wave ? a.N + 1 : 0) + kept, lane);
+    __syncthreads();
     if (wave < 2) {
-        Sum s = {0.0, 0.0};
-        if (wave == 0 || second) s = whole(a, b * rows + (wave ? a.N + 1 : 0) + kept, wave ? a.draft_scale : a.scale, lane);
+        const Sum s = wave == 0 || second ? whole(parts, wave ? a.draft_scale : a.scale, to) : Sum{0.0, 0.0};
         if (lane == 0) got[wave] = s;
     }
-    if (tid == 0) found = -1;
     __syncthreads();
     int64_t* const out = a.out + b * (a.N + 1) + kept;
     float* const lp = a.logprob ? a.logprob + b * (a.N + 1) + kept : nullptr;
@@ -271,42 +329,45 @@ __global__ __launch_bounds__(kVeThreads) void k_verify_draw(VerifyCall a) {
         return;
     }
     Weights w = weights_of(a, b, kept, n, got[0], got[1]);
-    const double r = a.r[b];
-    if (wave == 0) {
-        const int i0 = 2 * lane, i1 = i0 + 1;
-        double x0 = i0 < a.parts ? a.rest[b * a.parts + i0] : 0.0, x1 = i1 < a.parts ? a.rest[b * a.parts + i1] : 0.0;
-        double up = wave_scan64(x0 + x1, lane), all = __shfl(up, kWave - 1);
-        if (!(all > 0.0)) {   // nothing is left: the target's own
-            const Sum p = got[0];
-            const int64_t at = (b * rows + kept) * a.parts;
-            x0 = i0 < a.parts ? a.sums[at + i0] * exp2_64((a.ref[at + i0] - p.ref) * a.scale) / p.sum : 0.0;
-            x1 = i1 < a.parts ? a.sums[at + i1] * exp2_64((a.ref[at + i1] - p.ref) * a.scale) / p.sum : 0.0;
-            up = wave_scan64(x0 + x1, lane);
-            all = -__shfl(up, kWave - 1);   // (the sign says so)
+    const auto* const zp = logits_of<BF16>(a, b, kept);
+    const auto* zq = w.less ? logits_of<BF16>(a, b, a.N + 1 + kept) : zp;
+    double up = scan64(x0 + x1), all = lane64(up, kWave - 1);
+    if (!(all > 0.0)) {   // nothing is left (the same in every wave): the target's own weights
+        w.less = false, w.without = -1, zq = zp;
+        for (int i = 0; i < a.blocks; ++i) {
+            const double sum = sum64(block_sum<BF16>(a, w, zp, zq, i * a.block, tid, to));
+            if (lane == 0) total[i % 2][wave] = sum;
+            __syncthreads();
+            if (tid == 0) again[i] = (total[i % 2][0] + total[i % 2][1]) + (total[i % 2][2] + total[i % 2][3]);
         }
-        const double mark = r < 1.0 ? r * fabs(all) : __builtin_inf(), low = up - (x0 + x1);
+        __syncthreads();
+        x0 = i0 < a.blocks ? again[i0] : 0.0;
+        x1 = i1 < a.blocks ? again[i1] : 0.0;
+        up = scan64(x0 + x1);
+        all = lane64(up, kWave - 1);
+    }
+    const double mark = r < 1.0 ? r * all : __builtin_inf();
+    if (wave == 0) {
+        const double low = up - (x0 + x1);
         const uint64_t hit0 = __ballot(x0 > 0.0 && low + x0 > mark), hit1 = __ballot(x1 > 0.0 && up > mark);
         const uint64_t some0 = __ballot(x0 > 0.0), some1 = __ballot(x1 > 0.0);
-        int part;
+        int block;
         if (hit0 | hit1) {
             const int j = __builtin_ctzll(hit0 | hit1);
-            part = 2 * j + !(hit0 >> j & 1);
+            block = 2 * j + !(hit0 >> j & 1);
         } else {
             const int j = 63 - __builtin_clzll(some0 | some1);
-            part = 2 * j + (int)(some1 >> j & 1);
+            block = 2 * j + (int)(some1 >> j & 1);
         }
-        const double before = __shfl(low, part / 2) + (part % 2 ? __shfl(x0, part / 2) : 0.0);
-        if (lane == 0) part_ = part, whole_ = all, before_ = before;
+        const double before = lane64(low, block / 2) + (block % 2 ? lane64(x0, block / 2) : 0.0);
+        if (lane == 0) block_ = block, before_ = before;
     }
     __syncthreads();
-    if (whole_ < 0.0) w.less = false, w.without = -1;
-    const double mark = r < 1.0 ? r * fabs(whole_) : __builtin_inf();
     double before = before_;
-    const auto* const zp = logits_of<BF16>(a, b, kept);
-    const auto* const zq = w.less ? logits_of<BF16>(a, b, a.N + 1 + kept) : zp;
-    const int64_t v0 = part_ * a.per, v1 = v0 + a.per < a.V ? v0 + a.per : a.V;
+    const int64_t v0 = block_ * a.block, v1 = v0 + a.block < a.V ? v0 + a.block : a.V;
     int last = -1;   // the thread's last place with a weight, from v0
-    for (int64_t v = v0; v < v1; v += kVeBlock) {
+    int turn = 0;
+    for (int64_t v = v0; v < v1; v += kVeBlock, turn ^= 1) {
         float p[kVeRun], q[kVeRun];
         double x[kVeRun], sum = 0.0;
         const int64_t at = v + tid * kVeRun;
@@ -314,19 +375,19 @@ __global__ __launch_bounds__(kVeThreads) void k_verify_draw(VerifyCall a) {
         if (w.less) load_run<BF16>(q, zq, at, v1);
 #pragma unroll
         for (int e = 0; e < kVeRun; ++e) {
-            x[e] = w.of(p[e], w.less ? q[e] : 0.f, at + e);
+            x[e] = w.of(p[e], w.less ? q[e] : 0.f, at + e, to);
             sum += x[e];
             if (x[e] > 0.0) last = (int)(at - v0) + e;
         }
-        const double up = wave_scan64(sum, lane);
-        if (lane == kWave - 1) total[wave] = up;
+        const double run = scan64(sum);
+        if (lane == kWave - 1) total[turn][wave] = run;
         __syncthreads();
-        double low = before + (up - sum);
-        for (int i = 0; i < wave; ++i) low += total[i];
+        double low = before + (run - sum);
+        for (int i = 0; i < wave; ++i) low += total[turn][i];
         const bool hit = sum > 0.0 && low + sum > mark;
         const uint64_t hits = __ballot(hit);
         if (hit && lane == __builtin_ctzll(hits)) {
-            int64_t j = -1, most = 0;
+            int j = -1, most = 0;
 #pragma unroll
             for (int e = 0; e < kVeRun; ++e) {
                 low += x[e];
@@ -336,13 +397,13 @@ __global__ __launch_bounds__(kVeThreads) void k_verify_draw(VerifyCall a) {
                 }
             }
             if (j < 0) j = most;   // (the sums round differently one by one)
-            atomicMin(reinterpret_cast<unsigned long long*>(&found), (unsigned long long)(at + j));   // -1 is the largest
+            atomicMin(&found, (unsigned long long)(at + j));
         }
-        for (int i = 0; i < kVeWaves; ++i) before += total[i];
+        for (int i = 0; i < kVeWaves; ++i) before += total[turn][i];
         __syncthreads();
-        if (found >= 0) break;
+        if (found != ~0ull) break;
     }
-    if (found < 0) {   // r or the sums' rounding past the end: the part's last
+    if (found == ~0ull) {   // r or the sums' rounding past the end: the block's last
 #pragma unroll
         for (int d = 1; d < kWave; d <<= 1) last = max(last, __shfl_xor(last, d));
         if (lane == 0) last_[wave] = last;
@@ -350,46 +411,55 @@ __global__ __launch_bounds__(kVeThreads) void k_verify_draw(VerifyCall a) {
         last = max(max(last_[0], last_[1]), max(last_[2], last_[3]));
     }
     if (tid == 0) {
-        const int64_t x = found >= 0 ? found : v0 + last;
+        const int64_t x = found != ~0ull ? (int64_t)found : v0 + last;
         *out = x;
-        if (lp) *lp = (float)((((double)get_io<BF16>(zp, x) - w.p.ref) * a.scale - log2(w.p.sum)) * 0.69314718055994530942);
+        if (lp) *lp = (float)((((double)get_io<BF16>(zp, x) - w.p.ref) * (a.scale / kVeTable) - log2(w.p.sum)) * 0.69314718055994530942);
     }
 }
 
 namespace {
 
-constexpr int64_t kVeWanted = 4096;   // waves wanted of the sums' launch
+// Waves wanted of the sums' launch, so many that rows without drafts and their neighbours even out (us with
+// 8192 / 16384 / 32768: 64 rows of up to 5 drafts x 100003 80 / 72 / 70, 96 of 8 x 32768 42 / 42 / 44).
+constexpr int64_t kVeWanted = 16384;
+constexpr int64_t kVeKeepers = 2048;   // workgroups wanted of the weights'
+
+int64_t rows_in(const VerifyCall& c) { return c.B * (c.draft ? 2 * c.N + 1 : c.N + 1); }
 
 }  // namespace
 
 void plan_verify(VerifyCall& c) {
-    const int64_t rows = c.B * (c.draft ? 2 * c.N + 1 : c.N + 1), blocks = (c.V + kVeBlock - 1) / kVeBlock;
+    const int64_t rows = rows_in(c), unit = kWave * 16, units = (c.V + unit - 1) / unit;   // of a wave's loads
     int64_t n = kVeWanted / rows;
-    if (n > blocks) n = blocks;
+    if (n > units) n = units;
     if (n > kVeMaxParts) n = kVeMaxParts;
     if (n < 1) n = 1;
-    const int64_t each = (blocks + n - 1) / n;
-    c.per = each * kVeBlock;
-    c.parts = (int)((blocks + each - 1) / each);
+    c.per = (units + n - 1) / n * unit;
+    c.parts = (int)((c.V + c.per - 1) / c.per);
+    const int64_t least = (c.V + kVeBlock - 1) / kVeBlock;
+    c.block = (least + kVeMaxBlocks - 1) / kVeMaxBlocks * kVeBlock;
+    c.blocks = (int)((c.V + c.block - 1) / c.block);
+    const int64_t each = (c.blocks * c.B + kVeKeepers - 1) / kVeKeepers;   // blocks of a workgroup
+    c.keepers = (int)(each < c.blocks ? (c.blocks + each - 1) / each : 1);
 }
 
-size_t verify_ws_used(const VerifyCall& c) {
-    const size_t rows = (size_t)c.B * (c.draft ? 2 * c.N + 1 : c.N + 1);
-    return (2 * rows + (size_t)c.B) * c.parts;
-}
+size_t verify_ws_used(const VerifyCall& c) { return 2 * (size_t)rows_in(c) * c.parts + (size_t)c.B * c.blocks; }
 
-size_t verify_ws_doubles(int64_t B, int N, int64_t, int) {
-    // rows x parts is at most kVeWanted, or the rows where they are more; B is at most the rows
+size_t verify_ws_doubles(int64_t B, int N, int64_t V) {
+    // rows x parts is at most kVeWanted, or the rows where they are more
+    VerifyCall c = {};
+    c.B = B, c.N = N, c.V = V;
+    plan_verify(c);
     const int64_t rows = B * (2 * N + 1);
-    return 3 * (size_t)(rows > kVeWanted ? rows : kVeWanted);
+    return 2 * (size_t)(rows > kVeWanted ? rows : kVeWanted) + (size_t)B * c.blocks;
 }
 
 hipError_t launch_verify(VerifyCall c, hipStream_t st) {
     plan_verify(c);
-    const int64_t rows = c.B * (c.draft ? 2 * c.N + 1 : c.N + 1);
-    c.ref = c.sums + rows * c.parts;
-    c.rest = c.ref + rows * c.parts;
-    const unsigned sums = (unsigned)((rows * c.parts + kVeWaves - 1) / kVeWaves), keep = (unsigned)(c.B * c.parts), draw = (unsigned)c.B;
+    const int64_t all = rows_in(c) * c.parts;
+    c.ref = c.sums + all;
+    c.rest = c.ref + all;
+    const unsigned sums = (unsigned)((all + kVeWaves - 1) / kVeWaves), keep = (unsigned)(c.B * c.keepers), draw = (unsigned)c.B;
     const auto go = [&](auto bf) {
         constexpr bool BF16 = decltype(bf)::value;
         k_verify_sums<BF16><<<sums, kVeThreads, 0, st>>>(c);
