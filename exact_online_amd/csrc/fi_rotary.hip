@@ -54,6 +54,20 @@ __global__ __launch_bounds__(kRoThreads) void k_rotary(RotaryCall a, int log, in
         const int64_t at = id / a.shares, b = at / a.L;
         const int share = (int)(id - at * a.shares), t = (int)(at - b * a.L);
         const int64_t where = a.positions ? a.positions[at] : a.first ? (int64_t)a.first[b] + t : t;
+        // a pass's units are asked for a pass ahead, the first before the angles are formed
+        Unit next[P][2] = {};
+        const auto load = [&](int pass) {
+            const int h = pass * each + mine;
+            const bool key = h >= a.Hq, some = h < heads;
+            const View& from = key ? a.k : a.q;
+            const T* const x = static_cast<const T*>(from.p) + b * from.row + t * from.pos + (key ? h - a.Hq : h) * from.head;
+#pragma unroll
+            for (int p = 0; p < P; ++p) {
+                if (some && c0[p] < d) next[p][0] = *gmem(reinterpret_cast<const Unit*>(x + c0[p]));
+                if (some && c1[p] < d) next[p][1] = *gmem(reinterpret_cast<const Unit*>(x + c1[p]));
+            }
+        };
+        load(share);
         float cs[P][E], sn[P][E];
 #pragma unroll
         for (int p = 0; p < P; ++p)
@@ -65,18 +79,13 @@ __global__ __launch_bounds__(kRoThreads) void k_rotary(RotaryCall a, int log, in
         for (int pass = share; pass < passes; pass += a.shares) {
             const int h = pass * each + mine;
             const bool key = h >= a.Hq, some = h < heads;
-            const View& from = key ? a.k : a.q;
             const View& to = key ? a.ko : a.qo;
-            const int g = key ? h - a.Hq : h;
-            const T* const x = static_cast<const T*>(from.p) + b * from.row + t * from.pos + g * from.head;
-            T* const y = static_cast<T*>(to.p) + b * to.row + t * to.pos + g * to.head;
+            T* const y = static_cast<T*>(to.p) + b * to.row + t * to.pos + (key ? h - a.Hq : h) * to.head;
             const T* const w = static_cast<const T*>(key ? a.wk : a.wq);
-            Unit u[P][2] = {};
+            Unit u[P][2];
 #pragma unroll
-            for (int p = 0; p < P; ++p) {
-                if (some && c0[p] < d) u[p][0] = *gmem(reinterpret_cast<const Unit*>(x + c0[p]));
-                if (some && c1[p] < d) u[p][1] = *gmem(reinterpret_cast<const Unit*>(x + c1[p]));
-            }
+            for (int p = 0; p < P; ++p) u[p][0] = next[p][0], u[p][1] = next[p][1];
+            if (pass + a.shares < passes) load(pass + a.shares);
             float v[P][2 * E], sum = 0.f;
 #pragma unroll
             for (int p = 0; p < P; ++p)
