@@ -210,7 +210,7 @@ __device__ __forceinline__ float exp_of(Gate a, Gate b) {   // e^{a - b}, a <= b
 // is formed transposed, so that a result is the next product's operand as it lies in
 // the registers, and what is stored is the operand that k_delta_chunk loads.
 template <bool BF16, int DK, bool VEC>
-__global__ __launch_bounds__(Dl<BF16>::CT * kWave) void k_delta_tri(DeltaCall a) {
+__global__ __launch_bounds__(Dl<BF16>::CT * kWave, DK <= 128 ? 4 : 2) void k_delta_tri(DeltaCall a) {
     using M = Mm<BF16>;
     using T = typename M::T;
     using Frag = typename M::Frag;
@@ -1081,7 +1081,15 @@ int dl_chunk(int io_bf16) { return io_bf16 ? Dl<true>::C : Dl<false>::C; }
 int64_t dl_floats(int io_bf16) { return io_bf16 ? Dl<true>::TRI + Dl<true>::GATES : Dl<false>::TRI + Dl<false>::GATES; }
 int64_t dl_wide(int dk) { return dk <= 64 ? 64 : dk <= 128 ? 128 : 256; }   // keys of the kernels
 int dl_cols(int dk) { return dk <= 64 ? 64 : 128; }
-constexpr int64_t kDlLeast = 8;         // chunks of a segment at least
+// Each chunk of a segment takes its time twice, and some 40 us go into segments' states and
+// their join: rows are split into kDlFewest segments of kDlLeast chunks at least (us, 16 heads of 128 x 128, bf16, one row
+// of 512: unsplit 51, in 2 75; of 1024: 87, in 2 116, in 4 83; 8 rows of 1000: 106, in 2 162; 4 rows of 2048:
+// 223, in 4 186).
+constexpr int64_t kDlLeast = 4, kDlFewest = 4;
+// Rows that are not split, and leave CUs empty: slices of 64 columns for 128 (the same heads, one row of
+// 512: 61 -> 51 us, 8 of 512 73 -> 63).
+constexpr int64_t kDlNarrow = 128;      // slices of such a launch
+
 
 // (WAVES x NC columns of 16 to a slice; the segments' pass may share them out otherwise)
 template <bool BF16, int DK, int WAVES, int NC, int SWAVES, int SNC, bool VEC>
@@ -1101,6 +1109,7 @@ void delta_launches(const DeltaCall& c, hipStream_t st) {
 template <bool BF16>
 void delta_dims(const DeltaCall& c, hipStream_t st) {
     if (c.dk <= 64) c.vec ? delta_launches<BF16, 64, 4, 1, 4, 1, true>(c, st) : delta_launches<BF16, 64, 4, 1, 4, 1, false>(c, st);
+    else if (c.dk <= 128 && c.narrow) c.vec ? delta_launches<BF16, 128, 4, 1, 4, 1, true>(c, st) : delta_launches<BF16, 128, 4, 1, 4, 1, false>(c, st);
     else if (c.dk <= 128) c.vec ? delta_launches<BF16, 128, 8, 1, 4, 2, true>(c, st) : delta_launches<BF16, 128, 8, 1, 4, 2, false>(c, st);
     else c.vec ? delta_launches<BF16, 256, 4, 2, 4, 2, true>(c, st) : delta_launches<BF16, 256, 4, 2, 4, 2, false>(c, st);
 }
@@ -1126,7 +1135,8 @@ void plan_delta(DeltaCall& c) {
     const int slices = (c.dv + dl_cols(c.dk) - 1) / dl_cols(c.dk);
     int64_t n = kDlWorkgroups / (tasks * slices);
     if (n > c.chunks / kDlLeast) n = c.chunks / kDlLeast;
-    if (n < 1) n = 1;
+    if (n < kDlFewest) n = 1;
+    c.narrow = n == 1 && c.dk > 64 && c.dk <= 128 && tasks * slices <= kDlNarrow;
     c.seg_chunks = c.chunks ? (int)((c.chunks + n - 1) / n) : 1;
     c.nseg = c.chunks ? (c.chunks + c.seg_chunks - 1) / c.seg_chunks : 1;
 }
@@ -1159,7 +1169,7 @@ size_t delta_ws_bytes(int64_t B, int64_t L, int Hv, int dk, int dv, int io_bf16)
     const int64_t held = std::max(kDlTri, tasks), tri = chunks > held / tasks ? held : tasks * chunks;
     // segments: at most kDlWorkgroups over all heads and slices of any call
     const int slices = (dv + dl_cols(dk) - 1) / dl_cols(dk);
-    const int64_t segs = chunks >= 2 * kDlLeast ? kDlWorkgroups / slices : 0;
+    const int64_t segs = chunks >= kDlFewest * kDlLeast ? kDlWorkgroups / slices : 0;
     const int64_t carry = chunks > kDlTri / tasks ? tasks * dk * dv : 0;
     return (size_t)(tri * dl_floats(io_bf16) + segs * (dk * dv + dl_wide(dk) * dl_wide(dk)) + carry) * sizeof(float);
 }

@@ -101,6 +101,7 @@ struct DeltaCall {
     float *state;
     // the chunked form: chunks chunk0 .. chunk0 + chunks - 1 of every row at a time, in nseg segments of seg_chunks
     int chunk0, chunks, nseg, seg_chunks;
+    int narrow;                 // slices of 64 columns where others have 128
     float *tri;                 // [B Hv][chunks] systems and gates (delta_tri_floats each)
     float *ent, *move;          // of several segments: [B Hv][nseg][dk][dv] states before them, [B Hv][nseg][dk][dk] what they do to a state
     float *carry;               // [B Hv][dk][dv] states between two runs of chunks
