@@ -591,7 +591,8 @@ __global__ __launch_bounds__(WAVES * kWave, DK <= 128 || WAVES == 8 ? 2 : 1) voi
                 split_to<BF16, HALF>(p[0], ps + (D::frag(it, jt / PER) * kWave + lane) * E + jt % PER * 4, D::TRI);
             }
         }
-        // K E (rows are positions), and O^T = E^T Q^T (columns are positions)
+        __builtin_amdgcn_s_setprio(1);
+        // K E
         V4 R[NC][CT] = {}, O[OUT ? NC : 1][OUT ? CT : 1] = {};
 #pragma unroll
         for (int kb = 0; kb < DK / KB; ++kb) {
@@ -616,7 +617,7 @@ __global__ __launch_bounds__(WAVES * kWave, DK <= 128 || WAVES == 8 ? 2 : 1) voi
                         }
                     }
         }
-        // R = V - diag(e^G) K E
+        __builtin_amdgcn_s_setprio(0);
 #pragma unroll
         for (int it = 0; it < CT; ++it) {
             const V4 e = *smem_ptr(reinterpret_cast<const V4*>(&gs[16 * it + 4 * g]));
