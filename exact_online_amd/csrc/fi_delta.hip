@@ -16,6 +16,10 @@ namespace fi {
 // exchange, and rows of the slice are whole lines of memory.  Both products
 // with the state before the position are formed at once, S^T k and S^T q; then
 // o = a S^T q + (k . q) u needs no second pass over S.
+// Bound by the state, read and written once: 200 rows x 32 heads of 128 x 128 (845 MB
+// with q, k, v and o) take 148 to 166 us, 5.1 to 5.7 TB/s, what a large copy reaches
+// (5.0).  One row: 4.9 us, a launch and two trips to memory.  Further positions of a call
+// cost 12 us each (64 rows of these), vector operations on the state in its registers.
 constexpr int kDsThreads = 256, kDsWaves = kDsThreads / kWave;
 constexpr int kDsCols = 32;
 constexpr int kDsRows = kDsThreads / (kDsCols / 4);   // rows in one sweep
@@ -176,6 +180,19 @@ hipError_t launch_delta_step(const DeltaCall& c, hipStream_t st) {
 // state before it is linear: S = M E + N; OUT = false forms N (the state from
 // zero) and M (the same, without values, from the identity: dk more columns),
 // k_delta_join the states before the segments, and OUT = true starts from those.
+//
+// Numbers (bf16): the operands of the matrix cores are bf16.  q, k and v are that as they
+// are; S, T, R = V - .. and U, held in fp32, enter the state's recurrence in three parts
+// each, which hold all of their 24 bits (products of parts below 2^-24 are left out): the state is as far from
+// 64 bits as fp32 sums are, 2e-7 of its norm (with two parts 2e-6, for 15% less time).  Outputs are rounded to
+// bf16, and take S, P and U in two parts, 2^-18 of them.  fp32: fp32 products throughout.
+//
+// Measured: one row of 65536, 16 heads of 128 x 128, bf16 (1.07 GB once: 220 us): 1130 us: systems
+// 148, segments' states 535 to 560, join 45, outputs 390 to 420.  8 ragged rows of up to 2048, 32
+// heads: 272 to 278, systems 76, outputs 200.  fp32, two rows of 4001, 16 heads of 64 x 64: 131.  Bound by
+// the instructions of a wave: a product of 16 cycles and the four vector operations that go with
+// it (splits most of all) take 26 to 27 together even side by side, and make two thirds of
+// the time; LDS is 34 to 43% busy, memory a fifth.
 template <bool BF16>
 struct Dl {
     static constexpr int C = BF16 ? 64 : 32, CT = C / 16;               // positions of a chunk, tiles of them
@@ -203,7 +220,8 @@ __device__ __forceinline__ float exp_of(Gate a, Gate b) {   // e^{a - b}, a <= b
     return __builtin_amdgcn_exp2f(((a.hi - b.hi) + (a.lo - b.lo)) * kLog2E);
 }
 
-// One chunk's T and gates.  A wave has 16 rows of A: it forms the block on the diagonal, inverts
+// One chunk's T and gates (reading k and writing them, 13 KB for 64 positions of bf16, bounds 64K x 16 heads to
+// 100 us; 148 are taken, half of a wave's time in the substitution and its waits).  A wave has 16 rows of A: it forms the block on the diagonal, inverts
 // it by substitution to D_i (stable, where powers of A would not be: equal keys make them as
 // large as binomials), and the blocks before it; then the waves meet, and
 //     T_ij = -(sum_{j < k <= i} T_ik A_kj) D_j,   j = i - 1, i - 2, ..,
@@ -388,7 +406,9 @@ __device__ __forceinline__ void split_to(V4 x, typename Mm<BF16>::T* to, int pit
 // A wave has NC = DVS / 64 tiles of 16 columns of S in its registers, which are the
 // operand of its products as they lie there: lane (g, l16) of tile kt has column l16 and the rows row_of(kt) + r,
 // so that the tiles of one operand hold rows that follow one another for each lane.
-// The waves meet only in P and in what is staged.
+// The waves meet only in P and in what is staged.  Outputs of 128-wide heads take eight waves of one tile (one workgroup
+// on a CU: four waves of two tiles, 256 registers each, leave a SIMD one wave: ragged rows 316 and 503 us), the
+// segments' states four of two (two workgroups on a CU; 64K positions 530 and 606 us).
 template <bool BF16, int DK, int WAVES, int NC, bool OUT, bool VEC>
 __global__ __launch_bounds__(WAVES * kWave, DK <= 128 || WAVES == 8 ? 2 : 1) void k_delta_chunk(DeltaCall a) {
     using M = Mm<BF16>;
@@ -591,8 +611,9 @@ __global__ __launch_bounds__(WAVES * kWave, DK <= 128 || WAVES == 8 ? 2 : 1) voi
                 split_to<BF16, HALF>(p[0], ps + (D::frag(it, jt / PER) * kWave + lane) * E + jt % PER * 4, D::TRI);
             }
         }
+        // K E (rows are positions), and O^T = E^T Q^T (columns are positions).  The longest run of products goes
+        // first where another wave of the SIMD splits or stages (ragged rows 284 -> 278 us, 64K positions 1163 -> 1129).
         __builtin_amdgcn_s_setprio(1);
-        // K E
         V4 R[NC][CT] = {}, O[OUT ? NC : 1][OUT ? CT : 1] = {};
 #pragma unroll
         for (int kb = 0; kb < DK / KB; ++kb) {
@@ -618,6 +639,7 @@ __global__ __launch_bounds__(WAVES * kWave, DK <= 128 || WAVES == 8 ? 2 : 1) voi
                     }
         }
         __builtin_amdgcn_s_setprio(0);
+        // R = V - diag(e^G) K E
 #pragma unroll
         for (int it = 0; it < CT; ++it) {
             const V4 e = *smem_ptr(reinterpret_cast<const V4*>(&gs[16 * it + 4 * g]));
@@ -765,7 +787,8 @@ __global__ __launch_bounds__(WAVES * kWave, DK <= 128 || WAVES == 8 ? 2 : 1) voi
 // The chunked form with chunks of 16 positions, all of it in one wave: a wave follows a
 // row and head with 16 columns of S, forms T and P for itself and meets no other.  For
 // calls of a few chunks of 16, where one launch and no workspace are worth more than
-// forming T once for all columns.
+// forming T once for all columns.  Bound by the state's way from memory: five held positions of 64 rows, 32 heads of 128 x
+// 128 (147 MB) 38.6 us, 3.8 TB/s; where the state is written too 68 (4.1 TB/s).
 constexpr int kDfWaves = 4, kDfC = 16;
 
 template <bool BF16, int DK, bool VEC>

@@ -33,6 +33,9 @@ __device__ __forceinline__ void turn(double x, float& cos_, float& sin_) {
 // with 2^log lanes to a head.  A lane has P pairs of units of E elements, of
 // which both halves of every pair to be turned are its own: nothing is
 // exchanged but the sum of squares.  The position's angles are formed once.
+// Bound by memory: 16384 positions of 32 + 8 heads of 128, bf16 (336 MB), 74 us, 4.5 TB/s (a
+// copy 5.0), the vector units 65% busy (without the next pass's loads ahead 80 us).  A few tokens: 4.4 us, a launch
+// and a trip to memory.
 template <bool BF16, int E, int P, bool ADJACENT>
 __global__ __launch_bounds__(kRoThreads) void k_rotary(RotaryCall a, int log, int64_t positions) {
     using T = typename Mm<BF16>::T;
