@@ -1098,7 +1098,10 @@ __global__ __launch_bounds__(dj_threads(DK)) void k_delta_join(DeltaCall a, int 
 
 namespace {
 
-constexpr int64_t kDlTri = 32768;       // chunks of all heads whose systems are held at a time (bf16: 436 MB)
+// Chunks of all heads whose systems are held at a time (bf16: 436 MB), and of each head at least (53 KB; each
+// further run of chunks reads and writes the state, 64 KB of 128 x 128, once more).
+constexpr int64_t kDlTri = 32768, kDlTriEach = 4;
+int64_t dl_held(int64_t tasks) { return std::max(kDlTri / tasks, kDlTriEach); }
 constexpr int64_t kDlWorkgroups = 256;  // wanted of a launch
 
 int dl_chunk(int io_bf16) { return io_bf16 ? Dl<true>::C : Dl<false>::C; }
@@ -1153,7 +1156,7 @@ DeltaRoute delta_route(const DeltaCall& c) {
 
 void plan_delta(DeltaCall& c) {
     const int C = dl_chunk(c.io_bf16);
-    const int64_t tasks = c.B * c.Hv, all = (c.L + C - 1) / C, most = kDlTri / tasks < 1 ? 1 : kDlTri / tasks;
+    const int64_t tasks = c.B * c.Hv, all = (c.L + C - 1) / C, most = dl_held(tasks);
     c.chunk0 = 0;
     c.chunks = (int)(all < most ? all : most);
     const int slices = (c.dv + dl_cols(c.dk) - 1) / dl_cols(c.dk);
@@ -1189,12 +1192,12 @@ size_t delta_ws_bytes(int64_t B, int64_t L, int Hv, int dk, int dv, int io_bf16)
     c.B = B, c.Hv = Hv, c.io_bf16 = io_bf16;
     if (delta_route(c) != DeltaRoute::chunks) return 0;   // nor do smaller calls
     const int64_t C = dl_chunk(io_bf16), tasks = B * Hv, chunks = (L + C - 1) / C;
-    // systems: of all chunks, or of as many as are held at a time (one of each head at least)
-    const int64_t held = std::max(kDlTri, tasks), tri = chunks > held / tasks ? held : tasks * chunks;
+    // systems: of all chunks, or of as many as are held at a time of any call
+    const int64_t tri = std::min(tasks * chunks, std::max(kDlTri, tasks * kDlTriEach));
     // segments: at most kDlWorkgroups over all heads and slices of any call
     const int slices = (dv + dl_cols(dk) - 1) / dl_cols(dk);
     const int64_t segs = chunks >= kDlFewest * kDlLeast ? kDlWorkgroups / slices : 0;
-    const int64_t carry = chunks > kDlTri / tasks ? tasks * dk * dv : 0;
+    const int64_t carry = chunks > dl_held(tasks) ? tasks * dk * dv : 0;
     return (size_t)(tri * dl_floats(io_bf16) + segs * (dk * dv + dl_wide(dk) * dl_wide(dk)) + carry) * sizeof(float);
 }
 

@@ -462,7 +462,8 @@ typedef struct {
     int32_t hold;             /* nonzero: no state is changed (positions that may yet be taken back) */
 } fi_delta_args;
 
-/* fi_delta_create: allocates the workspace of the longest prompt.  Synchronous.
+/* fi_delta_create: allocates the workspace of the longest prompt (up to half a GB, and 53 KB for each row and head
+ * where those are more than 8192).  Synchronous.
  * FI_ERR_INVALID for a NULL pointer, a size < 1, Hv not a multiple of Hk, an
  * infinite or NaN scale, an unknown dtype or sizes that overflow;
  * FI_ERR_UNSUPPORTED for dk or dv > 256, L > FI_MAX_L, B Hv > 2^20 or a device
@@ -496,8 +497,8 @@ void fi_delta_destroy(fi_delta *s);
  *         y[a] = x[a] cos - x[b] sin,  y[b] = x[b] cos + x[a] sin
  *
  * with (a, b) = (i, i + rot/2) or (2i, 2i + 1); elements from rot on are not
- * turned.  Everything is fp32 (the angles are reduced in 64 bits), rounded to
- * io_dtype once.  Calls run on the device that was current when the handle was made.
+ * turned.  Everything is fp32, the sums of squares too (the angles are reduced in
+ * 64 bits), rounded to io_dtype once.  Calls run on the device that was current when the handle was made.
  */
 typedef enum { FI_NORM_NONE = 0, FI_NORM_RMS = 1, FI_NORM_L2 = 2 } fi_norm;
 typedef enum { FI_PAIRS_HALVES = 0, FI_PAIRS_ADJACENT = 1 } fi_pairs;

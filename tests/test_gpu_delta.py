@@ -246,6 +246,20 @@ def test_more_chunks_than_are_held_at_a_time(fresh, hold, dtype, L):
     check(x, dtype, lens=[L, L - 300, 77, 0], fresh=fresh, hold=hold)
 
 
+@pytest.mark.parametrize("dtype,L", [("bf16", 300), ("f32", 150)])
+def test_many_rows(dtype, L):
+    """19200 heads, whose systems of 5 chunks are formed 4 chunks at a time: the same numbers as those of fewer rows."""
+    x = inputs(21, 4, L, 2, 32, 24, 8, dtype)
+    _, st = check(x, dtype)
+    d = [t.cuda().repeat(150, *[1] * (t.dim() - 1)) for t in x]
+    o = torch.empty(600, L, 32, 8, dtype=x[2].dtype, device="cuda")
+    with fi.DeltaRule(600, L, 2, 32, 24, 8, 0.3, DT[dtype][1], stream()) as op:
+        op.prompt(*d[:5], o, d[5])
+        torch.cuda.synchronize()
+    assert torch.equal(o[:4].repeat(150, 1, 1, 1), o)
+    assert torch.equal(st.repeat(150, 1, 1, 1), d[5])
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_prompt_in_pieces_then_steps(dtype):
     """A prompt in calls of odd lengths and then single steps equals one prompt."""
