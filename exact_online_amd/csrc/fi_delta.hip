@@ -187,9 +187,9 @@ hipError_t launch_delta_step(const DeltaCall& c, hipStream_t st) {
 // 64 bits as fp32 sums are, 2e-7 of its norm (with two parts 2e-6, for 15% less time).  Outputs are rounded to
 // bf16, and take S, P and U in two parts, 2^-18 of them.  fp32: fp32 products throughout.
 //
-// Measured: one row of 65536, 16 heads of 128 x 128, bf16 (1.07 GB once: 220 us): 1130 us: systems
-// 148, segments' states 535 to 560, join 45, outputs 390 to 420.  8 ragged rows of up to 2048, 32
-// heads: 272 to 278, systems 76, outputs 200.  fp32, two rows of 4001, 16 heads of 64 x 64: 131.  Bound by
+// Measured: one row of 65536, 16 heads of 128 x 128, bf16 (1.07 GB once: 218 us): 1106 to 1130 us (under
+// the profiler systems 157, segments' states 583, join 47, outputs 515).  8 ragged rows of up to 2048, 32
+// heads: 272 to 278, systems 76 of them.  fp32, two rows of 4001, 16 heads of 64 x 64: 131.  Bound by
 // the instructions of a wave: a product of 16 cycles and the four vector operations that go with
 // it (splits most of all) take 26 to 27 together even side by side, and make two thirds of
 // the time; LDS is 34 to 43% busy, memory a fifth.
