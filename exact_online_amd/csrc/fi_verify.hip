@@ -267,24 +267,27 @@ __global__ __launch_bounds__(kVeThreads) void k_verify_keep(VerifyCall a) {
     __syncthreads();
     if (wave == 0) {
         bool keep = false;
-        double lp = 0.0;
-        if (known) {
-            const Sum p = got[lane];
-            if (is_some(p)) {
-                double q = 1.0;
-                if (a.draft) {
-                    const Sum s = got[a.N + 1 + lane];
-                    q = is_some(s) ? (weight(zq, s.ref, a.draft_scale, to) - kVeLeast) / s.sum : __builtin_nan("");
-                }
-                keep = (double)u * q < (weight(zp, p.ref, a.scale, to) - kVeLeast) / p.sum;
-                lp = (((double)zp - p.ref) * (a.scale / kVeTable) - log2(p.sum)) * 0.69314718055994530942;
+        Sum p = {0.0, 0.0};
+        if (known) p = got[lane];
+        if (is_some(p)) {
+            // u q < p, times both sums
+            Sum s = {0.0, 1.0};
+            double q = 1.0;
+            if (a.draft) {
+                s = got[a.N + 1 + lane];
+                q = is_some(s) ? weight(zq, s.ref, a.draft_scale, to) - kVeLeast : __builtin_nan("");
             }
+            keep = (double)u * q * p.sum < (weight(zp, p.ref, a.scale, to) - kVeLeast) * s.sum;
         }
         const int kept = __builtin_ctzll(~__ballot(keep));   // (lane 63 keeps none)
         if (lane == 0) kept_ = kept;
         if (me == 0 && lane <= a.N && lane != kept) {
             a.out[b * (a.N + 1) + lane] = lane < kept ? x : -1;
-            if (a.logprob) a.logprob[b * (a.N + 1) + lane] = lane < kept ? (float)lp : 0.f;
+            if (a.logprob) {
+                double lp = 0.0;
+                if (lane < kept) lp = (((double)zp - p.ref) * (a.scale / kVeTable) - log2(p.sum)) * 0.69314718055994530942;
+                a.logprob[b * (a.N + 1) + lane] = (float)lp;
+            }
         }
         if (me == 0 && lane == 0) a.kept[b] = kept;
     }
