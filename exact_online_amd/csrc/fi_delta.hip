@@ -443,6 +443,7 @@ __global__ __launch_bounds__(WAVES * kWave, DK <= 128 || WAVES == 8 ? 2 : 1) voi
     int c1 = c0 + a.seg_chunks;
     if (c1 > stop) c1 = stop;
     if (!OUT && c1 >= stop) return;      // a row's last segment hands nothing on
+    if (moves && seg == 0 && a.chunk0 == 0 && a.fresh) return;   // (there is nothing before it to move)
 
     if constexpr (OUT) {                 // o is zero past the row's end
         const bool last = seg == a.nseg - 1 && a.chunk0 + a.chunks >= (a.L + C - 1) / C;
@@ -1078,9 +1079,10 @@ __global__ __launch_bounds__(dj_threads(DK)) void k_delta_join(DeltaCall a, int 
             if (s + 2 < segs) ask(s + 1, ahead, next);
         }
         V4 acc[2] = {add, {0.f, 0.f, 0.f, 0.f}};   // two, as a product waits for the one before
+        if (s || from)   // (before a fresh row's first segment there is nothing, and M_0 is not formed)
 #pragma unroll
-        for (int kt = 0; kt < KT; ++kt)
-            acc[kt % 2] = Mm<false>::mma(m[kt], *smem_ptr(reinterpret_cast<const V4*>(&es[s % 2][l16 * PE + 16 * kt + 4 * g])), acc[kt % 2]);
+            for (int kt = 0; kt < KT; ++kt)
+                acc[kt % 2] = Mm<false>::mma(m[kt], *smem_ptr(reinterpret_cast<const V4*>(&es[s % 2][l16 * PE + 16 * kt + 4 * g])), acc[kt % 2]);
         acc[0] += acc[1];
         *smem_ptr(reinterpret_cast<V4*>(&es[(s + 1) % 2][l16 * PE + row0])) = acc[0];
         float* const to = ent + (int64_t)(s + 1) * dk * dv;
