@@ -433,8 +433,9 @@ void fi_scores_destroy(fi_scores *s);
  * stored in fp32, and o is rounded to io_dtype once.  log_decay is <= 0, -inf for
  * a = 0.  Keys of length one and beta in [0, 2] keep S bounded
  * (fi_rotary_run norms them); others are taken, and S grows as the formula
- * has it.  Calls run on the device that was current when the handle was made.  States, slots and rows out of the pool are as fi_lattn's; two
- * rows of one call must not share a slot unless the call holds.
+ * has it.  Calls run on the device that was current when the handle was made.
+ * States, slots and rows out of the pool are as fi_lattn's; two rows of one call
+ * must not share a slot unless the call holds.
  */
 typedef struct fi_delta fi_delta;   /* opaque; owns its device memory */
 typedef struct {
@@ -473,9 +474,10 @@ int fi_delta_create(const fi_delta_config *cfg, fi_delta **out);
 /* fi_delta_prompt: L given positions of every row, from the row's state, which is
  * left after its last position.  B = 0 and L = 0 are allowed.  FI_ERR_INVALID
  * for a NULL pointer, sizes beyond the config's, fewer than B states without
- * slots, or a pointer that is not aligned to its element.  A NaN or infinity in an input at t makes
- * every later output of its row and head and the state not finite, and can make
- * outputs of up to 63 positions before t NaN. */
+ * slots, or a pointer that is not aligned to its element.  A NaN or infinity in
+ * q, k, v or beta at t, or a NaN in log_decay, can make every output of its row
+ * in the heads that read it, from up to 63 positions before t on, and their
+ * states NaN or infinite; other rows and heads do not change. */
 int fi_delta_prompt(fi_delta *s, const fi_delta_args *a);
 
 /* fi_delta_step: one new position of every row in the recurrent form; L is 1,
