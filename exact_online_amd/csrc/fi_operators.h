@@ -134,7 +134,7 @@ hipError_t launch_rotary(RotaryCall c, hipStream_t st);
 
 // ------------------------------------------------------------ drafted tokens
 constexpr int kVerifyMaxRows = 1 << 22;   // rows of logits of a call
-constexpr double kVerifyOctave = 32 * 1.4426950408889634074;   // 32 log2 e
+constexpr double kVerifyOctave = 256 * 1.4426950408889634074;   // 256 log2 e
 
 struct VerifyCall {
     int64_t B, V;

@@ -5,10 +5,11 @@
 // fp32 tells apart.
 //
 // Three launches: sums of all rows of logits; what is kept, and the weights that the token
-// is drawn from; the token.  64 rows of up to 5 drafts x 100003, bf16 (77 MB: 16 us): 42 + 20 + 6.4 us;
-// 96 of 8 x 32768 without drafts' logits (57 MB) 27 + 11 + 5; one row of 4 x 131072, fp32, 5.2 + 7.5 + 5.0.
-// Bound by the vector units (52 to 62% busy): some 24 operations of 64 bits or around them for
-// each logit.  With the series alone (23 operations of 64 bits, some of them slow ones) the sums took 69 us.
+// is drawn from; the token.  64 rows of up to 5 drafts x 100003, bf16 (77 MB: 16 us): 35 + 18 + 6.4 us;
+// 96 of 8 x 32768 without drafts' logits (57 MB) 24 + 10.4 + 5; one row of 4 x 131072, fp32, 4.8 + 6.7 + 5.0.
+// Bound by the vector units (50 to 59% busy, with 3 waves of a SIMD on average: rows differ): 11 operations
+// of 64 bits and 5 around them for each logit.  With the series alone (23 operations of 64 bits, some of them slow
+// ones) the sums took 69 us.  More waves at a time (64 registers) change nothing.
 #include <type_traits>
 
 #include "fi_opdev.hpp"
@@ -20,42 +21,57 @@ constexpr int kVeRun = 8;                          // logits of a thread that fo
 constexpr int kVeBlock = kVeThreads * kVeRun;      // logits of a workgroup at a time
 constexpr int kVeMaxParts = 2 * kWave, kVeMaxBlocks = 2 * kWave;
 constexpr int kVeMaxDrafts = 63, kVeMaxRows = 2 * kVeMaxDrafts + 1;
-constexpr int kVeTable = 32;                       // powers of an octave
+constexpr int kVeTable = 256;                      // powers of an octave
 constexpr double kVeLow = -1020.0 * kVeTable;      // the least power that is formed
 constexpr double kVeNone = -1e300;                 // the reference of a part without a token
 
-// 2^{x / 32} for kVeLow <= x <= 32000 to 2^-48 of itself: n = rint(x), 2^{n / 32} from a
-// table of 32 in LDS (whatever lanes read of it, no two entries share a bank) and an exponent, and the
-// series of e^{(x - n) ln 2 / 32} to the 5th power (the next term is 2e-15).  Scales
-// come with the 32, so that an operation has one constant at most.
+// 2^{x / 256} for kVeLow <= x <= 256000 to 2^-48 of itself: n = rint(x), 2^{n / 256} from a
+// table in LDS and an exponent, and the series of e^{r ln 2 / 256}, r = x - n, to the 4th power (the
+// next term is 4e-17).  The table's entry i is less i << 12 in its high word, so that n << 12 is added whole.
+// Scales come with the 256, so that an operation has one constant at most.  (With 32 entries and the 5th
+// power, and the exponent put into the product, the sums took 42 us for 35, 27 for 24.)
 struct Powers {
     const FI_SHARED double* table;
-    double first;   // (ln 2 / 32)^5 / 5!, kept in a register
+    double first;   // (ln 2 / 256)^4 / 4!, kept in a register
 };
 __device__ __forceinline__ Powers make_powers(double* t, int tid) {
-    if (tid < kVeTable) t[tid] = exp2((double)tid / kVeTable);
-    double first = 3.973709984549416e-11;
+    if (tid < kVeTable)
+        t[tid] = __longlong_as_double(__double_as_longlong(exp2((double)tid / kVeTable)) - ((long long)tid << 44));
+    double first = 2.239395190875157e-12;
     asm("" : "+v"(first));
     return {smem_ptr(t), first};
 }
-__device__ __forceinline__ double power(double x, const Powers& to) {
-    constexpr double shift = 6755399441055744.0;   // 1.5 2^52: a sum's lowest bits are the nearest whole number
-    const double k = x + shift, r = x - (k - shift);
+struct Factors {
+    double scale, series;
+};
+constexpr double kVeShift = 6755399441055744.0;   // 1.5 2^52: a sum's lowest bits are the nearest whole number
+__device__ __forceinline__ Factors raised(double k, double r, const Powers& to) {   // k = n + kVeShift
+    using Words = uint32_t __attribute__((ext_vector_type(2)));
     const uint32_t n = (uint32_t)(uint64_t)__double_as_longlong(k);
-    double p = __builtin_fma(r, to.first, 9.172562701824643e-09);   // the 4th power's, and so on
-    p = __builtin_fma(r, p, 1.693850972437182e-06);
-    p = __builtin_fma(r, p, 0.0002345961982022468);
-    p = __builtin_fma(r, p, 0.02166084939249829);
+    double p = __builtin_fma(r, to.first, 3.308302680541371e-09);   // the 3rd power's, and so on
+    p = __builtin_fma(r, p, 3.665565596910106e-06);
+    p = __builtin_fma(r, p, 0.0027076061740622863);
     p = __builtin_fma(r, p, 1.0);
-    const uint64_t u = (uint64_t)__double_as_longlong(to.table[n & (kVeTable - 1)] * p);
-    const uint32_t high = (uint32_t)(u >> 32) + ((n & ~(uint32_t)(kVeTable - 1)) << 15);   // (n >> 5) << 20
-    return __longlong_as_double((long long)((uint64_t)high << 32 | (uint32_t)u));
+    Words t = __builtin_bit_cast(Words, (double)to.table[n & (kVeTable - 1)]);
+    t.y += n << 12;
+    return {__builtin_bit_cast(double, t), p};
 }
-// A logit's weight against the reference; what is far below it or -inf weighs next to nothing (2^kVeLow).
+__device__ __forceinline__ Factors power(double x, const Powers& to) {
+    const double k = x + kVeShift;
+    return raised(k, x - (k - kVeShift), to);
+}
+constexpr double kVeLeast = 0x1p-1020;   // 2^{kVeLow / 256}
+// What a sum against `ref` is times against the larger reference `now`.
+__device__ __forceinline__ double share(double ref, double now, double c, const Powers& to) {
+    const Factors f = power(fmax((ref - now) * c, kVeLow), to);
+    return f.scale * f.series;
+}
+// A logit's weight against the reference; what is far below it or -inf weighs nothing: the clamped
+// power is kVeLeast, without a rounding.
 __device__ __forceinline__ double weight(float z, double ref, double c, const Powers& to) {
-    return power(fmax(((double)z - ref) * c, kVeLow), to);
+    const Factors f = power(fmax(((double)z - ref) * c, kVeLow), to);
+    return __builtin_fma(f.scale, f.series, -kVeLeast);
 }
-constexpr double kVeLeast = 0x1p-1020;   // 2^{kVeLow / 32}: taken off where nothing has to be 0
 
 __device__ __forceinline__ int drafts_of(const VerifyCall& a, int64_t b) {
     const int n = a.lens ? a.lens[b] : a.N;
@@ -71,7 +87,7 @@ __device__ __forceinline__ const typename Mm<BF16>::T* logits_of(const VerifyCal
                     : static_cast<const T*>(a.draft) + b * a.draft_row + (i - a.N - 1) * a.draft_ld;
 }
 
-// A wave takes one part of one row of logits: the sum of 2^((z - R) c / 32) with a reference R near the
+// A wave takes one part of one row of logits: the sum of 2^((z - R) c / 256) with a reference R near the
 // largest z (differences first: they are exact, however large the logits are).  A row
 // that is no distribution has a sum that is NaN or 0.
 template <bool BF16>
@@ -109,6 +125,7 @@ __global__ __launch_bounds__(kVeThreads) void k_verify_sums(VerifyCall a) {
     const Powers to = make_powers(table_, threadIdx.x);
     __syncthreads();
     if (!here) return;
+    const double low = kVeLow / c;
     double R = kVeNone, sum = 0.0;
     bool good = true;
     for (int64_t v = v0; v < v1; v += UN * STEP) {
@@ -123,14 +140,18 @@ __global__ __launch_bounds__(kVeThreads) void k_verify_sums(VerifyCall a) {
             }
         if (__ballot(most > -inf && ((double)most - R) * c > 64.0 * kVeTable)) {
             const double now = (double)wave_max(most);
-            sum *= power(fmax((R - now) * c, kVeLow), to);
+            sum *= share(R, now, c, to);
             R = now;
         }
         double s[4] = {};
 #pragma unroll
         for (int u = 0; u < UN; ++u)
 #pragma unroll
-            for (int e = 0; e < E; ++e) s[(u * E + e) % 4] += weight((float)f[u][e], R, c, to);
+            for (int e = 0; e < E; ++e) {   // (what is clamped adds some 2^-1020)
+                const double x = fmax((double)(float)f[u][e] - R, low), k = __builtin_fma(x, c, kVeShift);
+                const Factors w = raised(k, __builtin_fma(x, c, kVeShift - k), to);
+                s[(u * E + e) % 4] = __builtin_fma(w.scale, w.series, s[(u * E + e) % 4]);
+            }
         sum += (s[0] + s[1]) + (s[2] + s[3]);
 #pragma unroll
         for (int u = 0; u < UN; ++u) f[u] = next[u];
@@ -164,7 +185,7 @@ __device__ __forceinline__ Sum whole(Parts p, double c, const Powers& to) {
     const double R = (double)most;
     double s = 0.0;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) s += p.sum[i] * power(fmax((p.ref[i] - R) * c, kVeLow), to);
+    for (int i = 0; i < 2; ++i) s += p.sum[i] * share(p.ref[i], R, c, to);
     return {R, sum64(s)};
 }
 __device__ __forceinline__ bool is_some(Sum s) { return s.sum > 0.0 && s.sum < __builtin_inf(); }   // false for NaN
@@ -179,8 +200,8 @@ struct Weights {
     // (each product rounded by itself: equal logits leave nothing)
     __device__ __forceinline__ double of(float zp, float zq, int64_t at, const Powers& to) const {
 #pragma clang fp contract(off)
-        double w = (weight(zp, p.ref, cp, to) - kVeLeast) * ip;
-        if (less) w = fmax(w - (weight(zq, q.ref, cq, to) - kVeLeast) * iq, 0.0);
+        double w = weight(zp, p.ref, cp, to) * ip;
+        if (less) w = fmax(w - weight(zq, q.ref, cq, to) * iq, 0.0);
         return at == without ? 0.0 : w;
     }
 };
@@ -275,9 +296,9 @@ __global__ __launch_bounds__(kVeThreads) void k_verify_keep(VerifyCall a) {
             double q = 1.0;
             if (a.draft) {
                 s = got[a.N + 1 + lane];
-                q = is_some(s) ? weight(zq, s.ref, a.draft_scale, to) - kVeLeast : __builtin_nan("");
+                q = is_some(s) ? weight(zq, s.ref, a.draft_scale, to) : __builtin_nan("");
             }
-            keep = (double)u * q * p.sum < (weight(zp, p.ref, a.scale, to) - kVeLeast) * s.sum;
+            keep = (double)u * q * p.sum < weight(zp, p.ref, a.scale, to) * s.sum;
         }
         const int kept = __builtin_ctzll(~__ballot(keep));   // (lane 63 keeps none)
         if (lane == 0) kept_ = kept;
@@ -429,9 +450,9 @@ __global__ __launch_bounds__(kVeThreads) void k_verify_draw(VerifyCall a) {
 namespace {
 
 // Waves wanted of the sums' launch, so many that rows without drafts and their neighbours even out (us with
-// 8192 / 16384 / 32768: 64 rows of up to 5 drafts x 100003 80 / 72 / 70, 96 of 8 x 32768 42 / 42 / 44).
+// 8192 / 16384 / 32768: 64 rows of up to 5 drafts x 100003 60 / 57 / 57, 96 of 8 x 32768 38 / 38 / 41).
 constexpr int64_t kVeWanted = 16384;
-constexpr int64_t kVeKeepers = 2048;   // workgroups wanted of the weights'
+constexpr int64_t kVeKeepers = 2048;   // workgroups wanted of the weights' (with 4096: 60, 38)
 
 int64_t rows_in(const VerifyCall& c) { return c.B * (c.draft ? 2 * c.N + 1 : c.N + 1); }
 
