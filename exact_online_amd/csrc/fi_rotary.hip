@@ -36,7 +36,10 @@ __device__ __forceinline__ void turn(double x, float& cos_, float& sin_) {
 // Bound by memory: 16384 positions of 32 + 8 heads of 128, bf16 (336 MB), 74 us, 4.5 TB/s (a
 // copy 5.0), the vector units 65% busy (without the next pass's loads ahead 80 us).  A few tokens: 4.4 us, a launch
 // and a trip to memory.
-template <bool BF16, int E, int P, bool ADJACENT>
+// PART: some elements are not turned, and are chosen as they are (as a turn by 0 an infinity or a NaN
+// would reach its neighbour): two choices a pair, 16384 positions of 40 heads of 80, 48 of them
+// turned, 49 us for 46; heads that are turned whole go without.
+template <bool BF16, int E, int P, bool ADJACENT, bool PART>
 __global__ __launch_bounds__(kRoThreads) void k_rotary(RotaryCall a, int log, int64_t positions) {
     using T = typename Mm<BF16>::T;
     using Unit = T __attribute__((ext_vector_type(E)));
@@ -121,8 +124,10 @@ __global__ __launch_bounds__(kRoThreads) void k_rotary(RotaryCall a, int log, in
 #pragma unroll
                 for (int e = 0; e < E; ++e) {
                     const int i = ADJACENT ? 2 * e : e, j = ADJACENT ? 2 * e + 1 : E + e;
-                    r[i / E][i % E] = (T)fmaf(v[p][i], cs[p][e], -v[p][j] * sn[p][e]);
-                    r[j / E][j % E] = (T)fmaf(v[p][j], cs[p][e], v[p][i] * sn[p][e]);
+                    // (what is not turned is no pair: an infinity or a NaN stays by itself)
+                    const bool turned = !PART || pair[p] + e < half;
+                    r[i / E][i % E] = (T)(turned ? fmaf(v[p][i], cs[p][e], -v[p][j] * sn[p][e]) : v[p][i]);
+                    r[j / E][j % E] = (T)(turned ? fmaf(v[p][j], cs[p][e], v[p][i] * sn[p][e]) : v[p][j]);
                 }
                 if (some && c0[p] < d) *gmem(reinterpret_cast<Unit*>(y + c0[p])) = r[0];
                 if (some && c1[p] < d) *gmem(reinterpret_cast<Unit*>(y + c1[p])) = r[1];
@@ -136,6 +141,10 @@ namespace {
 constexpr int64_t kRoWanted = 4096;        // waves wanted of a launch
 constexpr int64_t kRoBlocks = 1 << 16;     // workgroups of a launch at most
 
+template <bool BF16, int E, int P, bool ADJACENT, bool PART>
+void rotary_launch(const RotaryCall& c, int log, int64_t positions, unsigned grid, hipStream_t st) {
+    k_rotary<BF16, E, P, ADJACENT, PART><<<grid, kRoThreads, 0, st>>>(c, log, positions);
+}
 template <bool BF16, int E, int P>
 void rotary_go(RotaryCall c, hipStream_t st) {
     const int pairs = (c.d + 2 * E - 1) / (2 * E);   // of units, of a head
@@ -147,8 +156,9 @@ void rotary_go(RotaryCall c, hipStream_t st) {
     c.shares = (int)(shares < 1 ? 1 : shares > passes ? passes : shares);
     const int64_t blocks = (positions * c.shares + kRoWaves - 1) / kRoWaves;
     const unsigned grid = (unsigned)(blocks < kRoBlocks ? blocks : kRoBlocks);
-    if (c.pairs) k_rotary<BF16, E, P, true><<<grid, kRoThreads, 0, st>>>(c, log, positions);
-    else k_rotary<BF16, E, P, false><<<grid, kRoThreads, 0, st>>>(c, log, positions);
+    const bool part = c.rot < c.d;
+    if (c.pairs) part ? rotary_launch<BF16, E, P, true, true>(c, log, positions, grid, st) : rotary_launch<BF16, E, P, true, false>(c, log, positions, grid, st);
+    else part ? rotary_launch<BF16, E, P, false, true>(c, log, positions, grid, st) : rotary_launch<BF16, E, P, false, false>(c, log, positions, grid, st);
 }
 
 template <bool BF16>

@@ -499,7 +499,7 @@ void fi_delta_destroy(fi_delta *s);
  *         y[a] = x[a] cos - x[b] sin,  y[b] = x[b] cos + x[a] sin
  *
  * with (a, b) = (i, i + rot/2) or (2i, 2i + 1); elements from rot on are not
- * turned.  Everything is fp32, the sums of squares too (the angles are reduced in
+ * turned: what is not finite there reaches no other element but by the norm.  Everything is fp32, the sums of squares too (the angles are reduced in
  * 64 bits), rounded to io_dtype once.  Calls run on the device that was current when the handle was made.
  */
 typedef enum { FI_NORM_NONE = 0, FI_NORM_RMS = 1, FI_NORM_L2 = 2 } fi_norm;
