@@ -1172,7 +1172,7 @@ void plan_delta(DeltaCall& c) {
 
 namespace {
 
-// the workspace's parts, in floats
+// the workspace's parts, in floats; whole 16-byte units, in which systems and moves are read
 struct DeltaParts {
     size_t tri, ent, move, carry;
     size_t all() const { return tri + ent + move + carry; }
@@ -1180,7 +1180,7 @@ struct DeltaParts {
 DeltaParts delta_parts(const DeltaCall& c) {
     const size_t tasks = (size_t)c.B * c.Hv, states = (size_t)c.dk * c.dv, segs = c.nseg > 1 ? tasks * c.nseg : 0;
     const int C = dl_chunk(c.io_bf16);
-    return {tasks * c.chunks * dl_floats(c.io_bf16), segs * states, segs * dl_wide(c.dk) * dl_wide(c.dk),
+    return {tasks * c.chunks * dl_floats(c.io_bf16), (segs * states + 3) / 4 * 4, segs * dl_wide(c.dk) * dl_wide(c.dk),
             (c.L + C - 1) / C > c.chunks ? tasks * states : 0};
 }
 
@@ -1200,7 +1200,15 @@ size_t delta_ws_bytes(int64_t B, int64_t L, int Hv, int dk, int dv, int io_bf16)
     const int slices = (dv + dl_cols(dk) - 1) / dl_cols(dk);
     const int64_t segs = chunks >= kDlFewest * kDlLeast ? kDlWorkgroups / slices : 0;
     const int64_t carry = chunks > dl_held(tasks) ? tasks * dk * dv : 0;
-    return (size_t)(tri * dl_floats(io_bf16) + segs * (dk * dv + dl_wide(dk) * dl_wide(dk)) + carry) * sizeof(float);
+    return (size_t)(tri * dl_floats(io_bf16) + (segs * dk * dv + 3) / 4 * 4 + segs * dl_wide(dk) * dl_wide(dk) + carry) * sizeof(float);
+}
+
+void place_delta(DeltaCall& c, float* ws) {
+    const DeltaParts p = delta_parts(c);
+    c.tri = ws;
+    c.ent = c.tri + p.tri;
+    c.move = c.ent + p.ent;
+    c.carry = p.carry ? c.move + p.move : nullptr;
 }
 
 hipError_t launch_delta_prompt(DeltaCall c, float* ws, hipStream_t st) {
@@ -1208,12 +1216,8 @@ hipError_t launch_delta_prompt(DeltaCall c, float* ws, hipStream_t st) {
     if (route == DeltaRoute::steps) return launch_delta_step(c, st);
     if (route == DeltaRoute::few) return launch_delta_few(c, st);
     plan_delta(c);
+    place_delta(c, ws);
     const int C = dl_chunk(c.io_bf16), all = (c.L + C - 1) / C, held = c.chunks;
-    const DeltaParts p = delta_parts(c);
-    c.tri = ws;
-    c.ent = c.tri + p.tri;
-    c.move = c.ent + p.ent;
-    c.carry = p.carry ? c.move + p.move : nullptr;
     do {
         if (all - c.chunk0 < held) c.chunks = all - c.chunk0;
         if (c.io_bf16) delta_dims<true>(c, st);

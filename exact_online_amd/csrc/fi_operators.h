@@ -114,6 +114,7 @@ hipError_t launch_delta_prompt(DeltaCall c, float *ws, hipStream_t st);
 enum class DeltaRoute { steps, few, chunks };
 DeltaRoute delta_route(const DeltaCall &c);
 void plan_delta(DeltaCall &c);   // chunks at a time, segments
+void place_delta(DeltaCall &c, float *ws);   // a planned call's tri, ent, move and carry
 size_t delta_ws_used(const DeltaCall &c);
 size_t delta_ws_bytes(int64_t B, int64_t L, int Hv, int dk, int dv, int io_bf16);
 
