@@ -463,8 +463,9 @@ typedef struct {
     int32_t hold;             /* nonzero: no state is changed (positions that may yet be taken back) */
 } fi_delta_args;
 
-/* fi_delta_create: allocates the workspace of the longest prompt (up to half a GB, and 53 KB for each row and head
- * where those are more than 8192).  Synchronous.
+/* fi_delta_create: allocates the workspace of the longest prompt: at most 437 MB for the systems of its chunks (64 positions;
+ * fp32: 32), or 54 KB for each row and head where those are more than 8192; at most 101 MB for the states of segments;
+ * and where all rows and heads have more than 32768 chunks, 4 dk dv bytes for each row and head.  Synchronous.
  * FI_ERR_INVALID for a NULL pointer, a size < 1, Hv not a multiple of Hk, an
  * infinite or NaN scale, an unknown dtype or sizes that overflow;
  * FI_ERR_UNSUPPORTED for dk or dv > 256, L > FI_MAX_L, B Hv > 2^20 or a device

@@ -1,8 +1,11 @@
 // The parts of the delta rule's workspace for calls of random sizes, odd head sizes most of all: every part lies
 // behind the one before, within what the call uses, and what is read in 16-byte units begins at one.
+// With three numbers as arguments: handles of random sizes take no more than the header says of fi_delta_create: MB for
+// systems, KB for each row and head in their place, MB for segments.
 #include <algorithm>
 #include <cmath>
 #include <cstdio>
+#include <cstdlib>
 #include <random>
 
 #include "fi_operators.h"
@@ -15,7 +18,26 @@ static int64_t spread(int64_t lo, int64_t hi) {   // over the logarithm
     return std::min(hi, (int64_t)std::exp(std::log((double)lo) + (rng() >> 11) * 0x1p-53 * std::log((hi + 1.0) / lo)));
 }
 
-int main() {
+static int bounds(double systems, double each, double segments) {
+    double most[2] = {};
+    for (int i = 0; i < 2000000; ++i) {
+        const int64_t Hv = spread(1, 4096), B = spread(1, kLattnMaxRows / Hv), L = spread(1, (int64_t)1 << 25);
+        const int wide = (int)from(0, 3), dk = wide ? (int)from(1, 256) : 256, dv = wide > 1 ? (int)from(1, 256) : 128 << from(0, 1), bf = (int)from(0, 1);
+        const double rows = (double)B * Hv, chunks = (double)((L + (bf ? 63 : 31)) / (bf ? 64 : 32)), have = (double)delta_ws_bytes(B, L, (int)Hv, dk, dv, bf);
+        const double bound = std::max(systems * 1e6, each * 1e3 * rows) + segments * 1e6 + (rows * chunks > 32768 ? 4.0 * dk * dv * rows : 0.0);
+        most[rows > 8192] = std::max(most[rows > 8192], have / bound);
+        if (have > bound) {
+            std::printf("delta: %lld x %lld, %lld heads of %d x %d, bf16 %d: %.0f bytes, %.0f at most\n", (long long)B, (long long)L, (long long)Hv, dk, dv, bf,
+                        have, bound);
+            return 1;
+        }
+    }
+    std::printf("ok: at most %.3f and %.3f of the bound\n", most[0], most[1]);
+    return most[0] > 0.9 && most[1] > 0.9 ? 0 : 1;   // nor does the header say much more than they take
+}
+
+int main(int argc, char** argv) {
+    if (argc == 4) return bounds(std::atof(argv[1]), std::atof(argv[2]), std::atof(argv[3]));
     alignas(256) static float base[64];
     long split = 0, carried = 0, odd = 0;
     for (int i = 0; i < 300000; ++i) {
