@@ -630,7 +630,8 @@ class DeltaRule(_Owner):
     fp32 [B, L, Hv] of any strides; state is [slots, Hv, dk, dv], fp32 and
     contiguous, updated in place (with hold: read only); lens and slots are int32
     tensors [B].  All are on the handle's device, the one that was current when it was made;
-    other shapes, types, strides and devices are refused."""
+    other shapes, types, strides and devices are refused.  A handle holds a workspace
+    only: layers of one shape on one stream share one."""
 
     _destroy = staticmethod(fi_delta_destroy)
 

@@ -70,7 +70,7 @@ class DeltaDecoder:
         self.dense = {n: dense(n) for n in p if n != "emb"}
         freq = (1e4 ** (-torch.arange(dh // 4) * 4.0 / dh)).float().cuda()      # half of a head is turned
         self.turn = fi.Rotary(B, L, Hk, Hk, dh, freq, fi.FI_NORM_L2, 1e-6, io_dtype=io, stream=s)
-        self.mix = [fi.DeltaRule(B, L, Hk, Hv, dh, dh, 1.0, io, stream=s) for _ in range(self.layers)]
+        self.mix = fi.DeltaRule(B, L, Hk, Hv, dh, dh, 1.0, io, stream=s)         # one workspace for all layers: the states are ours
         self.state = [torch.zeros(B, Hv, dh, dh, device="cuda") for _ in range(self.layers)]
         self.at = torch.zeros(B, dtype=torch.int32, device="cuda")               # where the rows' next positions stand
         empty = lambda *shape, t=dtype: torch.empty(*shape, dtype=t, device="cuda")  # noqa: E731
@@ -100,7 +100,7 @@ class DeltaDecoder:
             self.turn.run(q, k, q, k, first=self.at)
             a, b = gates(raw.view(B, T, -1))
             self.gate[i] = (self.gate[i][0], a, b)
-            self.mix[i].prompt(q, k, v, a, b, att.view(B, T, self.Hv, self.dh), self.state[i], lens=lens, fresh=fresh, hold=hold)
+            self.mix.prompt(q, k, v, a, b, att.view(B, T, self.Hv, self.dh), self.state[i], lens=lens, fresh=fresh, hold=hold)
             self.dense[f"{i}.o"].run(att, p[f"{i}.o"], x, res=x)
             self.dense[f"{i}.up"].run(x, p[f"{i}.up"], hid)
             self.dense[f"{i}.down"].run(hid, p[f"{i}.down"], x, res=x)
@@ -113,11 +113,11 @@ class DeltaDecoder:
         """After a held run over T positions: the states move over the first lens [B] of them."""
         att = self.att[:self.B * T].view(self.B, T, self.Hv, self.dh)
         for i in range(self.layers):
-            self.mix[i].prompt(*self._heads(i, T), *self.gate[i][1:], att, self.state[i], lens=lens)
+            self.mix.prompt(*self._heads(i, T), *self.gate[i][1:], att, self.state[i], lens=lens)
         self.at += lens
 
     def close(self):
-        for h in (self.turn, *self.mix, *self.dense.values()):
+        for h in (self.turn, self.mix, *self.dense.values()):
             h.close()
 
 
