@@ -17,7 +17,7 @@ namespace fi {
 // with the state before the position are formed at once, S^T k and S^T q; then
 // o = a S^T q + (k . q) u needs no second pass over S.
 // Bound by the state, read and written once: 200 rows x 32 heads of 128 x 128 (845 MB
-// with q, k, v and o) take 148 to 166 us, 5.1 to 5.7 TB/s, what a large copy reaches
+// with q, k, v and o) take 164 to 168 us, 5.0 to 5.2 TB/s, what a large copy reaches
 // (5.0).  One row: 4.9 us, a launch and two trips to memory.  Further positions of a call
 // cost 12 us each (64 rows of these), vector operations on the state in its registers.
 constexpr int kDsThreads = 256, kDsWaves = kDsThreads / kWave;
@@ -174,7 +174,7 @@ hipError_t launch_delta_step(const DeltaCall& c, hipStream_t st) {
 //     S = e^{G_C} E + K^T diag(e^{G_C - G_j}) U
 // T does not depend on the state: k_delta_tri forms it for all chunks at once.
 // k_delta_chunk then follows a row's chunks, a workgroup to a head and a slice of
-// DVS columns of S, 16 columns to a wave.
+// columns of S, 16 or 32 columns to a wave.
 //
 // Long rows of few heads are split into segments.  What a segment does to the
 // state before it is linear: S = M E + N; OUT = false forms N (the state from
@@ -189,10 +189,12 @@ hipError_t launch_delta_step(const DeltaCall& c, hipStream_t st) {
 //
 // Measured: one row of 65536, 16 heads of 128 x 128, bf16 (1.07 GB once: 218 us): 1106 to 1130 us (under
 // the profiler systems 157, segments' states 583, join 47, outputs 515).  8 ragged rows of up to 2048, 32
-// heads: 272 to 278, systems 76 of them.  fp32, two rows of 4001, 16 heads of 64 x 64: 131.  Bound by
-// the instructions of a wave: a product of 16 cycles and the four vector operations that go with
-// it (splits most of all) take 26 to 27 together even side by side, and make two thirds of
-// the time; LDS is 34 to 43% busy, memory a fifth.
+// heads: 269 to 278, systems 76 of them.  fp32, two rows of 4001, 16 heads of 64 x 64: 131 to 134.  Two thirds
+// of the time are the instructions of a wave: a product of 16 cycles and the four vector operations that go with
+// it (splits most of all) take 26 to 27 together even side by side; the rest is waits, with 1.4 to 1.8
+// waves on a SIMD.  LDS is 20 to 43% busy, memory a fifth.  Wide heads (no more than one wave on a SIMD, some of its
+// registers in scratch), two rows of 4000, 8 heads of 192 x 192 and 256 x 256: bf16 373 and 386, fp32 846 and 889;
+// 16 rows of 1000, which are not split: 317 and 339, 856 and 902.
 template <bool BF16>
 struct Dl {
     static constexpr int C = BF16 ? 64 : 32, CT = C / 16;               // positions of a chunk, tiles of them
@@ -403,7 +405,7 @@ __device__ __forceinline__ void split_to(V4 x, typename Mm<BF16>::T* to, int pit
     } else *smem_ptr(reinterpret_cast<V4*>(to)) = x;
 }
 
-// A wave has NC = DVS / 64 tiles of 16 columns of S in its registers, which are the
+// A slice is DVS = 16 NC WAVES columns.  A wave has NC tiles of 16 columns of S in its registers, which are the
 // operand of its products as they lie there: lane (g, l16) of tile kt has column l16 and the rows row_of(kt) + r,
 // so that the tiles of one operand hold rows that follow one another for each lane.
 // The waves meet only in P and in what is staged.  Outputs of 128-wide heads take eight waves of one tile (one workgroup
@@ -1150,6 +1152,7 @@ void delta_dims(const DeltaCall& c, hipStream_t st) {
 // / 20, of 5: 10 / 10 / 20, of 48: - / 19 / 21, of 64: - / 23 / 21; 64 rows of 2: 50 / 66 / 129, of 5: 88 / 68 / 130,
 // of 48: - / 133 / 140, of 64: - / 158 / 146.  fp32, whose products take longer, 64 rows of 5: 91 / 122 / 148, of 8:
 // 125 / - / 148, of 16: 238 / 143 / 151, of 32: - / 215 / 160; one row of 32: 38 / 20 / 24, of 48: - / 25 / 32).
+// Other head sizes go by the same borders, which were not measured for them.
 DeltaRoute delta_route(const DeltaCall& c) {
     if (c.L <= (c.io_bf16 ? 3 : 6)) return DeltaRoute::steps;
     const bool busy = c.B * c.Hv > 512;   // the CUs are full

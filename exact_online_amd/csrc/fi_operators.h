@@ -102,8 +102,9 @@ struct DeltaCall {
     // the chunked form: chunks chunk0 .. chunk0 + chunks - 1 of every row at a time, in nseg segments of seg_chunks
     int chunk0, chunks, nseg, seg_chunks;
     int narrow;                 // slices of 64 columns where others have 128
-    float *tri;                 // [B Hv][chunks] systems and gates (delta_tri_floats each)
-    float *ent, *move;          // of several segments: [B Hv][nseg][dk][dv] states before them, [B Hv][nseg][dk][dk] what they do to a state
+    float *tri;                 // [B Hv][chunks] systems and gates (dl_floats each)
+    float *ent, *move;          // of several segments: [B Hv][nseg][dk][dv] states before them, [B Hv][nseg][w][w] what they do to a
+                                // state, w the keys of the kernel (dk, up to 64, 128 or 256)
     float *carry;               // [B Hv][dk][dv] states between two runs of chunks
 };
 

@@ -1,14 +1,14 @@
 // fi_verify.hip -- drafted tokens against the target's probabilities (fi_verify_*).
 //
-// Everything is held in 64 bits: which token a random number falls on depends
+// Everything is held in 64 bits, powers to 2^-48 of themselves: which token a random number falls on depends
 // on running sums of up to 2^31 probabilities, whose borders lie closer than
 // fp32 tells apart.
 //
 // Three launches: sums of all rows of logits; what is kept, and the weights that the token
 // is drawn from; the token.  64 rows of up to 5 drafts x 100003, bf16 (77 MB: 16 us): 35 + 18 + 6.4 us;
 // 96 of 8 x 32768 without drafts' logits (57 MB) 24 + 10.4 + 5; one row of 4 x 131072, fp32, 4.8 + 6.7 + 5.0.
-// Bound by the vector units (50 to 59% busy, with 3 waves of a SIMD on average: rows differ): 11 operations
-// of 64 bits and 5 around them for each logit.  With the series alone (23 operations of 64 bits, some of them slow
+// The sums are 11 operations of 64 bits and 5 around them for each logit, which keep the vector units 50 to 59% busy, with 3
+// waves of a SIMD on average (parts of places without drafts have none); the rest is waits.  With the series alone (23 operations of 64 bits, some of them slow
 // ones) the sums took 69 us.  More waves at a time (64 registers) change nothing.
 #include <type_traits>
 

@@ -555,7 +555,8 @@ void fi_rotary_destroy(fi_rotary *s);
  *           then -1
  *     logprob = log p_i(out[i]), 0 behind the last
  *
- * all in 64 bits.  Where w is zero everywhere (a draft that neither allows), the token is
+ * all held in 64 bits (probabilities down to 2^-900 of the largest to 2^-38 of themselves; below 2^-1020 of it they
+ * may count as none).  Where w is zero everywhere (a draft that neither allows), the token is
  * drawn from p_kept.  A logit of -inf is a token that is ruled out.  A draft
  * outside [0, V) is not kept.  Logits with a NaN or +inf, or without any token left, are no
  * distribution: a target's keep no draft, and out there is -1, logprob NaN; a draft's do not keep it
