@@ -9,6 +9,22 @@
 
 namespace fi {
 
+// A state's decay by a = e^g, the same for all of the wave: near one as S + (a - 1) S, as the rounding of a (up to
+// 2^-25 of S, always to one side) would add up over long memories; from a half down as a S, as a - 1 near -1 holds
+// a to no more than 2^-25 of the whole S, which may be all that is left.  FLAT: two operations for one, and no branch.
+template <bool FLAT, class Each>
+__device__ __forceinline__ void decayed(float em1, float a, Each each) {
+    if constexpr (FLAT) {
+        const bool near = em1 > -0.5f;
+        const float f = near ? em1 : a, c = near ? 1.f : 0.f;
+        each([f, c](float s) { return fmaf(f, s, c * s); });
+    } else if (__uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(em1))) > -0.5f) {
+        each([em1](float s) { return fmaf(em1, s, s); });
+    } else {
+        each([a](float s) { return a * s; });
+    }
+}
+
 // ------------------------------------------------------------ recurrent form
 // Position by position: a workgroup has dk x 32 of one (row, head)'s state in its
 // registers, thread (r, c) = (tid / 8, tid % 8) the columns 4c .. 4c+3 of the
@@ -76,9 +92,13 @@ __global__ __launch_bounds__(kDsThreads) void k_delta_step(DeltaCall a) {
         const int at = t % 2;
         if (tid < ROWS) ks[at][tid] = nk, qs[at][tid] = nq;
         if (tid < kDsCols) vs[at][tid] = nv;
-        const float em1 = expm1f(nld), beta = nbeta;   // a - 1
+        const float em1 = expm1f(nld), decay = expf(nld), beta = nbeta;
         __syncthreads();
         if (t + 1 < len) ask(t + 1);
+        decayed<false>(em1, decay, [&](auto f) {
+#pragma unroll
+            for (int i = 0; i < 4 * RPT; ++i) S[i / 4][i % 4] = f(S[i / 4][i % 4]);
+        });
         V4 sk = {0.f, 0.f, 0.f, 0.f}, sq = sk;
         float kq = 0.f;
 #pragma unroll
@@ -87,9 +107,6 @@ __global__ __launch_bounds__(kDsThreads) void k_delta_step(DeltaCall a) {
             kq = fmaf(k, q, kq);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                // a S as S + (a - 1) S: the rounding of a (up to 2^-25 of S a step, always
-                // to one side) would add up over long memories
-                S[i][j] = fmaf(em1, S[i][j], S[i][j]);
                 sk[j] = fmaf(k, S[i][j], sk[j]);
                 sq[j] = fmaf(q, S[i][j], sq[j]);
             }
@@ -193,8 +210,8 @@ hipError_t launch_delta_step(const DeltaCall& c, hipStream_t st) {
 // of the time are the instructions of a wave: a product of 16 cycles and the four vector operations that go with
 // it (splits most of all) take 26 to 27 together even side by side; the rest is waits, with 1.4 to 1.8
 // waves on a SIMD.  LDS is 20 to 43% busy, memory a fifth.  Wide heads (no more than one wave on a SIMD, some of its
-// registers in scratch), two rows of 4000, 8 heads of 192 x 192 and 256 x 256: bf16 373 and 386, fp32 846 and 889;
-// 16 rows of 1000, which are not split: 317 and 339, 856 and 902.
+// registers in scratch), two rows of 4000, 8 heads of 192 x 192 and 256 x 256: bf16 389 and 402, fp32 861 and 909;
+// 16 rows of 1000, which are not split: 352 and 353, 865 and 916 (without the branch of a state's decay 317 and 339, 855 and 900).
 template <bool BF16>
 struct Dl {
     static constexpr int C = BF16 ? 64 : 32, CT = C / 16;               // positions of a chunk, tiles of them
@@ -642,6 +659,12 @@ __global__ __launch_bounds__(WAVES * kWave, DK <= 128 || WAVES == 8 ? 2 : 1) voi
                     }
         }
         __builtin_amdgcn_s_setprio(0);
+        // S: its decay, as E is not read again.  bf16 by a branch (64K positions 1105 us here, 1118 before S's products, 1120
+        // without one), fp32 without (two rows of 4001 133; by a branch 137, before S's products 134.5)
+        decayed<!BF16>(expm1f(gs[3 * C - 1]) + gs[C - 1] * gs[4 * C - 1], gs[C - 1], [&](auto f) {
+#pragma unroll
+            for (int i = 0; i < NC * KT * 4; ++i) S[i / (4 * KT)][i / 4 % KT][i % 4] = f(S[i / (4 * KT)][i / 4 % KT][i % 4]);
+        });
         // R = V - diag(e^G) K E
 #pragma unroll
         for (int it = 0; it < CT; ++it) {
@@ -734,15 +757,7 @@ __global__ __launch_bounds__(WAVES * kWave, DK <= 128 || WAVES == 8 ? 2 : 1) voi
             }
         }
         if constexpr (!EARLY) fetch_all(c + 1 < c1 ? c + 1 : c);
-        // S: its decay as S + (e^G - 1) S (the rounding of e^G would add up over the chunks of
-        // a long memory), then the chunk's own products
-        const float d = expm1f(gs[3 * C - 1]) + gs[C - 1] * gs[4 * C - 1];
-#pragma unroll
-        for (int nc = 0; nc < NC; ++nc)
-#pragma unroll
-            for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) S[nc][kt][r] = fmaf(d, S[nc][kt][r], S[nc][kt][r]);
+        // S takes the chunk's own products
 #pragma unroll
         for (int kb = 0; kb < C / KB; ++kb) {
             Frag f[NC][PARTS];
@@ -983,7 +998,11 @@ __global__ __launch_bounds__(kDfWaves * kWave, BF16 && DK <= 128 ? 3 : DK <= 128
         }
         __builtin_amdgcn_sched_barrier(0);
         if (moves) {
-            const float d = expm1f(end.hi) + exp_of(end, zero) * end.lo;
+            const float whole = exp_of(end, zero);
+            decayed<!BF16>(expm1f(end.hi) + whole * end.lo, whole, [&](auto to) {
+#pragma unroll
+                for (int i = 0; i < 4 * KT; ++i) S[i / 4][i % 4] = to(S[i / 4][i % 4]);
+            });
             Frag f[PARTS];
             operand(U * to_end, f);
 #pragma unroll
@@ -998,8 +1017,6 @@ __global__ __launch_bounds__(kDfWaves * kWave, BF16 && DK <= 128 ? 3 : DK <= 128
 #pragma unroll
                     for (int e = 0; e < 4; ++e) k[e] = smem_ptr(ks)[place(4 * g + e, 4 * kt + l16 / 4) + l16 % 4];
                 }
-#pragma unroll
-                for (int r = 0; r < 4; ++r) S[kt][r] = fmaf(d, S[kt][r], S[kt][r]);
 #pragma unroll
                 for (int i = PARTS - 1; i >= 0; --i) S[kt] = M::mma(k, f[i], S[kt]);
                 if (kt % 4 == 3) __builtin_amdgcn_sched_barrier(0);

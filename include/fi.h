@@ -431,7 +431,7 @@ void fi_scores_destroy(fi_scores *s);
  *
  * q, k, v and o are of io_dtype, log_decay and beta fp32; S is held, summed and
  * stored in fp32, and o is rounded to io_dtype once.  log_decay is <= 0, -inf for
- * a = 0.  Keys of length one and beta in [0, 2] keep S bounded
+ * a = 0 (what is left of a state over up to 64 positions may count as nothing below 2^-126 of it).  Keys of length one and beta in [0, 2] keep S bounded
  * (fi_rotary_run norms them); others are taken, and S grows as the formula
  * has it.  Calls run on the device that was current when the handle was made.
  * States, slots and rows out of the pool are as fi_lattn's; two rows of one call
