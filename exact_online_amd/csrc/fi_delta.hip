@@ -205,8 +205,8 @@ hipError_t launch_delta_step(const DeltaCall& c, hipStream_t st) {
 // bf16, and take S, P and U in two parts, 2^-18 of them.  fp32: fp32 products throughout.
 //
 // Measured: one row of 65536, 16 heads of 128 x 128, bf16 (1.07 GB once: 218 us): 1092 to 1205 us on different cards (under
-// the profiler systems 157, segments' states 583, join 47, outputs 515).  8 ragged rows of up to 2048, 32
-// heads: 269 to 288, systems 76 of them.  fp32, two rows of 4001, 16 heads of 64 x 64: 131 to 134.  Two thirds
+// the profiler systems 161, segments' states 609, join 53, outputs 536).  8 ragged rows of up to 2048, 32
+// heads: 269 to 288, systems 79 of them.  fp32, two rows of 4001, 16 heads of 64 x 64: 131 to 134.  Two thirds
 // of the time are the instructions of a wave: a product of 16 cycles and the four vector operations that go with
 // it (splits most of all) take 26 to 27 together even side by side; the rest is waits, with 1.4 to 1.8
 // waves on a SIMD.  LDS is 20 to 43% busy, memory a fifth.  Wide heads (no more than one wave on a SIMD, some of its
